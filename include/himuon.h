@@ -58,7 +58,8 @@ extern "C" {
 typedef enum {
   HIMUON_BF16 = 0,   /* storage: bfloat16;  compute: bf16 tensor-core operands, fp32 accumulate */
   HIMUON_FP16 = 1,   /* storage: float16;   compute: fp16 tensor-core operands, fp32 accumulate */
-  HIMUON_FP32 = 2    /* storage: float32;   compute: fp32 on CUDA cores */
+  HIMUON_FP32 = 2,   /* storage: float32;   compute: fp32 on CUDA cores */
+  HIMUON_I8 = 3      /* storage: int8 codes of himuon_quantize (that call and himuon_expert_product_i8 only) */
 } himuon_dtype;
 
 enum {
@@ -253,6 +254,84 @@ HIMUON_API int64_t himuon_launch_count(void);
  */
 HIMUON_API int64_t himuon_plan_tiles(const himuon_mat *mats, int32_t n, const himuon_split *splits, int32_t tile,
                           int64_t *records, int64_t cap);
+
+/*
+ * ---------------------------------------------------------------- expert products
+ *
+ * The products around the weight matrices of a mixture of experts (and, with
+ * n = 1, of a single matrix): forward, input gradient and weight gradient over
+ * rows sorted by expert, and the forward product in 8-bit integers.
+ *
+ * Row groups.  `offsets` is a DEVICE array of n + 1 int32, non-decreasing,
+ * within 0 .. rows: rows offsets[e] .. offsets[e + 1] - 1 of the row operands
+ * belong to matrix e, and a group may be empty.  The array is read by the
+ * kernels (no host synchronisation, so the call can be captured into a CUDA
+ * graph and replayed with new offsets).  Rows outside every group are neither
+ * used nor written.  offsets may be NULL when n = 1: one group of all rows.
+ * Offsets that decrease or leave 0 .. rows are clamped to the nearest group
+ * bounds inside the arrays, and HIMUON_ERR_DEVICE is set in the device status
+ * word.
+ *
+ * Row operands may have 0 rows (their data pointer is then not read).  Sums are
+ * held in fp32 (int32 for the 8-bit product); each result is rounded once to
+ * its storage type.  Every data pointer is 16-byte aligned and every
+ * ld * sizeof a multiple of 16 bytes where a matrix has more than one row
+ * (HIMUON_ERR_ALIGNMENT); scale vectors need 4-byte alignment only.  The n
+ * matrices of one argument have the same shape, ld and dtype.  Outputs must not overlap inputs (except C and G
+ * below) or each other.  The calls keep nothing between them and take no
+ * workspace; results do not depend on timing, and calls on several streams may
+ * overlap.
+ */
+
+/*
+ * Y[r] = X[r] W_e (w_trans = 0, W_e is K x N) or X[r] W_e^T (w_trans = 1, W_e
+ * is N x K) for the rows r of every group e.  X is rows x K, Y rows x N, W an
+ * array of n matrices of equal shape.  X and W: BF16 or FP16 (the same for
+ * all); Y: BF16, FP16 or FP32.  The input gradient of a product is the product
+ * of the output gradient with the other w_trans.
+ */
+HIMUON_API int himuon_expert_product(const himuon_mat *X, const himuon_mat *W, int32_t n, const int32_t *offsets,
+                                     int32_t w_trans, const himuon_mat *Y, void *stream);
+
+/*
+ * G_e = alpha * sum over the rows r of group e of A[r]^T B[r] + beta * C_e.
+ * A is rows x P, B rows x Q, G an array of n matrices P x Q: with A = X and
+ * B = dY the gradient of W_e in Y = X W_e, with A = dY and B = X the one in
+ * Y = X W_e^T.  C: NULL (then beta must be 0) or n matrices P x Q that are
+ * added, e.g. the gradients of earlier micro-batches; C_e may be G_e itself
+ * (the same pointer, ld and dtype).  With beta = 0, C is not read.  An empty
+ * group gives beta * C_e.  A and B: BF16 or FP16 (the same); G and C: BF16,
+ * FP16 or FP32, each the same for all its matrices.  The matrices of G must
+ * not overlap (the same pointer twice is refused).
+ */
+HIMUON_API int himuon_expert_gradient(const himuon_mat *A, const himuon_mat *B, int32_t n, const int32_t *offsets,
+                                      float alpha, float beta, const himuon_mat *C, const himuon_mat *G,
+                                      void *stream);
+
+/*
+ * 8-bit codes of n matrices, one scale per row (dim = 0) or per column
+ * (dim = 1, the codes are stored transposed: one row of codes per column of
+ * the input).  With top = max |x| over the row or column:
+ *     scale = top / 127,   code = round(127 x / top), ties to even,
+ * so x ~ scale * code.  Where top = 0, scale and codes are 0; where the row or
+ * column holds an infinity or a NaN, scale is NaN and the codes are 0 (a
+ * product with them gives NaN).  `in`: BF16, FP16 or FP32 (per matrix);
+ * `codes`: I8, rows x cols (dim 0) or cols x rows (dim 1); `scale`: FP32,
+ * 1 x rows or 1 x cols.
+ */
+HIMUON_API int himuon_quantize(const himuon_mat *in, int32_t n, int32_t dim, const himuon_mat *codes,
+                               const himuon_mat *scale, void *stream);
+
+/*
+ * Y[r, c] = x_scale[r] * w_scale[e, c] * sum over k of X[r, k] W_e[c, k], for
+ * the rows r of every group e, the sum exact in int32.  X: I8 codes, rows x K;
+ * x_scale: FP32, 1 x rows; W: n matrices of I8 codes, N x K; w_scale: one FP32
+ * matrix n x N; Y: rows x N, BF16, FP16 or FP32.  K is at most 131071 (the
+ * sum's range); more is HIMUON_ERR_UNSUPPORTED.
+ */
+HIMUON_API int himuon_expert_product_i8(const himuon_mat *X, const himuon_mat *x_scale, const himuon_mat *W,
+                                        const himuon_mat *w_scale, int32_t n, const int32_t *offsets,
+                                        const himuon_mat *Y, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,509 @@
+"""Expert products against their definitions in 64 bits (needs a B200).
+
+Tolerances.  An output y = round(s) to a type of unit roundoff u (half of
+torch.finfo's eps) of an fp32 sum s of K products: the products of 16-bit
+values are exact in fp32, and each of the K additions, in any order, is off by
+at most 2^-23 of a partial sum, whose size is at most S = sum |a| |b| (2^-23
+rather than 2^-24: the tensor cores truncate instead of rounding).  So
+    |y - exact| <= (K + 16) 2^-23 S + u |exact| (1 + ...) + half the type's
+smallest step, the 16 covering the epilogue's operations (alpha, beta, the
+scales).  The 8-bit sum is exact, so there only the epilogue's part is left.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def hm():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from tiled_newton_schulz_b200 import himuon
+    himuon.load()
+    return himuon
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def matrix(shape, dtype, g, scale=1.0, lead=8, margin=0, fill=float("nan")):
+    """Normal values as a view into a larger buffer of `fill`: `margin` extra
+    columns and a pitch that is a multiple of `lead`."""
+    pitch = -(-(shape[-1] + margin) // lead) * lead
+    buf = torch.full((*shape[:-1], pitch), fill, device=DEV, dtype=torch.float32).to(dtype)
+    view = buf[..., :shape[-1]]
+    view.copy_(torch.randn(*shape, generator=g, device=DEV) * scale)
+    return view
+
+
+def offsets(counts, start=0):
+    return torch.tensor(np.concatenate([[start], start + np.cumsum(counts)]), dtype=torch.int32, device=DEV)
+
+
+def groups(off):
+    o = off.tolist()
+    return list(zip(o, o[1:]))
+
+
+def close(y, exact, size, k, dtype):
+    f = torch.finfo(dtype)
+    y = y.double()
+    lim = (k + 16) * 2.0 ** -23 * size + f.eps / 2 * exact.abs() * (1 + 2 ** -8) + f.smallest_normal * f.eps / 2
+    d = (y - exact).abs()
+    assert torch.isfinite(y).all()
+    bad = d > lim
+    assert not bad.any(), f"{int(bad.sum())} off, worst {float((d / lim).max()):.3g} of the bound, {bad.nonzero()[:4].tolist()}"
+
+
+def check_product(hm, dtype, out, K, N, counts, trans, start=0, behind=0, listed=False, seed=0, margin=0):
+    g = gen(seed)
+    n, off = len(counts), offsets(counts, start)
+    rows = start + sum(counts) + behind
+    X = matrix((rows, K), dtype, g, margin=margin)
+    X[:start] = float("nan")                      # rows outside every group must not matter
+    X[rows - behind:] = float("inf")
+    W = matrix((n, N, K) if trans else (n, K, N), dtype, g, 0.5, margin=margin)
+    Y = torch.full((rows, -(-(N + margin) // 8) * 8), -7.0, device=DEV).to(out)
+    Yv = Y[:, :N]
+    hm.expert_product(X, [w for w in W] if listed else W, Yv, off, w_trans=trans)
+    assert hm.device_status() == 0
+    for e, (a, b) in enumerate(groups(off)):
+        x, w = X[a:b].double(), W[e].double()
+        w = w.T if trans else w
+        close(Yv[a:b], x @ w, x.abs() @ w.abs(), K, out)
+    assert (Y[:start] == -7).all() and (Y[rows - behind:] == -7).all() and (Y[:, N:] == -7).all()
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "fp32"), ("fp16", "bf16")])
+@pytest.mark.parametrize("K,N,counts", [
+    (64, 128, [1]),
+    (8, 8, [0, 1, 0, 2]),
+    (1, 1, [3]),
+    (200, 136, [5, 0, 33, 130, 1]),
+    (129, 257, [31, 32, 33, 0]),
+    (512, 384, [300, 257, 0, 256, 17]),
+    (1100, 2050, [100, 7]),
+])
+def test_product(hm, dtype, out, K, N, counts, trans):
+    check_product(hm, TYPES[dtype], TYPES[out], K, N, counts, trans, seed=K + N)
+
+
+@pytest.mark.parametrize("trans", [False, True])
+def test_product_views_rows_outside_groups_and_lists(hm, trans):
+    check_product(hm, torch.bfloat16, torch.bfloat16, 320, 264, [40, 0, 90], trans, start=13, behind=70, listed=True,
+                  margin=24)
+    check_product(hm, torch.float16, torch.float32, 72, 40, [1, 1, 1], trans, start=1, behind=1, margin=8)
+
+
+@pytest.mark.parametrize("n,listed", [(130, True), (300, False), (700, False)])
+def test_product_many_experts(hm, n, listed):
+    rng = np.random.default_rng(n)
+    check_product(hm, torch.bfloat16, torch.bfloat16, 72, 136, rng.integers(0, 4, n).tolist(), False, listed=listed)
+    counts = np.zeros(n, dtype=int)
+    counts[n - 1], counts[n // 2] = 70, 1
+    check_product(hm, torch.bfloat16, torch.float32, 64, 64, counts.tolist(), True, start=2, listed=listed)
+
+
+@pytest.mark.parametrize("rows", [1, 8, 64, 700])
+@pytest.mark.parametrize("K,N", [(4096, 1024), (1024, 4096), (2048, 256)])
+@pytest.mark.parametrize("trans", [False, True])
+def test_product_few_rows_long_sums(hm, rows, K, N, trans):
+    rng = np.random.default_rng(rows)
+    check_product(hm, torch.bfloat16, torch.bfloat16, K, N, rng.multinomial(rows, np.ones(6) / 6).tolist(), trans)
+
+
+def test_product_one_group_without_offsets_and_empty_operands(hm):
+    g = gen(3)
+    X, W = matrix((77, 96), torch.bfloat16, g), matrix((1, 96, 48), torch.bfloat16, g)
+    Y = torch.empty(77, 48, device=DEV, dtype=torch.float32)
+    hm.expert_product(X, W, Y)
+    x, w = X.double(), W[0].double()
+    close(Y, x @ w, x.abs() @ w.abs(), 96, torch.float32)
+    hm.expert_product(X[:0], W, Y[:0])
+    hm.expert_product(X[:0], W, Y[:0], torch.zeros(2, dtype=torch.int32, device=DEV))
+    # a single row of a width that is no multiple of 16 bytes
+    X1, W1, Y1 = X[:1, :93].contiguous(), W[:, :93], torch.empty(1, 45, device=DEV, dtype=torch.bfloat16)
+    hm.expert_product(X1, W1[:, :, :45], Y1)
+    x, w = X1.double(), W1[0, :, :45].double()
+    close(Y1, x @ w, x.abs() @ w.abs(), 93, torch.bfloat16)
+    assert hm.device_status() == 0
+
+
+def test_product_shared_matrix_and_nonfinite_rows(hm):
+    """One matrix for two groups; a row with an infinity or a NaN changes no other row."""
+    g = gen(4)
+    W1 = matrix((160, 96), torch.bfloat16, g)
+    X = matrix((50, 160), torch.bfloat16, g)
+    off = offsets([20, 30])
+    Y = torch.empty(50, 96, device=DEV, dtype=torch.bfloat16)
+    hm.expert_product(X, [W1, W1], Y, off)
+    want = Y.clone()
+    X[7, 3], X[20, 159] = float("nan"), float("inf")
+    hm.expert_product(X, [W1, W1], Y, off)
+    keep = [r for r in range(50) if r not in (7, 20)]
+    assert torch.equal(Y[keep], want[keep])
+    assert Y[7].isnan().all() and not torch.isfinite(Y[20]).any()
+
+
+def check_gradient(hm, dtype, out, P, Q, counts, beta=0.0, alpha=1.0, cdtype=None, alias=False, start=0, behind=0,
+                   listed=False, seed=0, margin=0):
+    g = gen(seed)
+    n, off = len(counts), offsets(counts, start)
+    rows = start + sum(counts) + behind
+    A = matrix((rows, P), dtype, g, margin=margin)
+    B = matrix((rows, Q), dtype, g, margin=margin)
+    for t, v in ((A, float("nan")), (B, float("inf"))):   # rows outside every group must not matter
+        t[:start] = v
+        t[rows - behind:] = v
+    pitch = -(-(Q + margin) // 8) * 8
+    G = torch.full((n, P, pitch), -7.0, device=DEV).to(out)
+    Gv = G[:, :, :Q]
+    C = None
+    if beta != 0 or cdtype is not None:
+        C = matrix((n, P, Q), cdtype or out, g, 3.0)
+        if alias:
+            Gv.copy_(C)
+    c0 = C.double() if C is not None else None
+    lst = (lambda t: [m for m in t]) if listed else (lambda t: t)
+    hm.expert_gradient(A, B, lst(Gv), off, alpha=alpha, beta=beta, C=lst(Gv if alias else C) if C is not None else None)
+    assert hm.device_status() == 0
+    for e, (a, b) in enumerate(groups(off)):
+        x, y = A[a:b].double(), B[a:b].double()
+        exact, size = alpha * (x.T @ y), abs(alpha) * (x.abs().T @ y.abs())
+        if beta != 0:
+            exact, size = exact + beta * c0[e], size + abs(beta) * c0[e].abs()
+        close(Gv[e], exact, size, b - a, out)
+    assert (G[:, :, Q:] == -7).all()
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "fp32"), ("fp16", "fp32")])
+@pytest.mark.parametrize("beta", [0.0, 1.0])
+@pytest.mark.parametrize("P,Q,counts", [
+    (128, 128, [64]),
+    (8, 8, [0, 1, 0, 2]),
+    (1, 1, [3]),
+    (136, 200, [5, 0, 33, 130, 1]),
+    (257, 129, [31, 16, 17, 0]),
+    (384, 512, [300, 257, 0, 15, 128]),
+    (64, 2050, [63, 65]),
+])
+def test_gradient(hm, dtype, out, beta, P, Q, counts):
+    check_gradient(hm, TYPES[dtype], TYPES[out], P, Q, counts, beta=beta, seed=P + Q)
+
+
+def test_gradient_views_scales_types_and_alias(hm):
+    bf, f32 = torch.bfloat16, torch.float32
+    check_gradient(hm, bf, bf, 120, 264, [40, 0, 90], start=13, behind=70, listed=True, margin=24, alpha=-0.5)
+    check_gradient(hm, bf, f32, 120, 264, [40, 0, 90], beta=1.0, alias=True, start=3, behind=5, listed=True)
+    check_gradient(hm, bf, bf, 120, 264, [40, 0, 90], beta=0.95, alias=True, margin=40)
+    check_gradient(hm, torch.float16, bf, 72, 40, [9, 9], beta=-2.0, alpha=0.25, cdtype=f32)
+    check_gradient(hm, bf, f32, 72, 40, [9, 9], beta=1.0, cdtype=torch.float16)
+    check_gradient(hm, bf, f32, 40, 72, [0, 0, 0], beta=1.0)
+    check_gradient(hm, bf, f32, 40, 72, [0, 0, 0])
+
+
+def test_gradient_leaves_c_unread_without_beta(hm):
+    g = gen(8)
+    A, B = matrix((20, 48), torch.bfloat16, g), matrix((20, 56), torch.bfloat16, g)
+    G = torch.full((1, 48, 56), float("nan"), device=DEV)
+    hm.expert_gradient(A, B, G, beta=0.0, C=G)
+    x, y = A.double(), B.double()
+    close(G[0], x.T @ y, x.abs().T @ y.abs(), 20, torch.float32)
+    hm.expert_gradient(A[:0], B[:0], G)                       # no rows: zeros
+    assert (G == 0).all()
+
+
+@pytest.mark.parametrize("n,listed", [(130, True), (300, False)])
+def test_gradient_many_experts(hm, n, listed):
+    rng = np.random.default_rng(n)
+    check_gradient(hm, torch.bfloat16, torch.bfloat16, 72, 136, rng.integers(0, 6, n).tolist(), listed=listed)
+
+
+def test_gradient_long_sum(hm):
+    check_gradient(hm, torch.bfloat16, torch.float32, 200, 264, [5003, 1])
+    check_gradient(hm, torch.bfloat16, torch.bfloat16, 64, 64, [9001])
+
+
+def test_gradient_against_differences(hm):
+    """The products are linear in W and in X, so differences along one entry are the gradients up to rounding."""
+    g = gen(9)
+    off = offsets([37, 0, 64])
+    X, W = matrix((101, 80), torch.bfloat16, g), matrix((3, 80, 48), torch.bfloat16, g)
+    dY = matrix((101, 48), torch.bfloat16, g)
+    G = torch.empty(3, 80, 48, device=DEV)
+    dX = torch.empty(101, 80, device=DEV)
+    hm.expert_gradient(X, dY, G, off)
+    hm.expert_product(dY, W, dX, off, w_trans=True)
+
+    def loss(x, w):
+        y = torch.empty(101, 48, device=DEV)
+        hm.expert_product(x, w, y, off)
+        return float((y.double() * dY.double()).sum())
+
+    base = loss(X, W)
+    # every fp32 output of a forward product is within (K + 16) 2^-23 sum |x| |w| of its sum; times |dY|, summed
+    err = 2 * (80 + 16) * 2.0 ** -23 * float((X.double().abs().sum(1) * 6 * dY.double().abs().sum(1)).sum())
+    for e, i, j in [(0, 0, 0), (0, 79, 47), (1, 3, 3), (2, 17, 40)]:
+        w = W.clone()
+        w[e, i, j] = W[e, i, j] + 4
+        h = float(w[e, i, j].double() - W[e, i, j].double())
+        x = X[slice(*groups(off)[e]), i].double() @ dY[slice(*groups(off)[e]), j].double()
+        assert abs((loss(X, w) - base) / h - float(G[e, i, j])) <= err / abs(h) + 1e-4 * abs(float(x))
+    for r, i in [(0, 0), (36, 79), (37, 5), (100, 33)]:
+        x = X.clone()
+        x[r, i] = X[r, i] + 4
+        h = float(x[r, i].double() - X[r, i].double())
+        assert abs((loss(x, W) - base) / h - float(dX[r, i])) <= err / abs(h) + 1e-4 * abs(float(dX[r, i]))
+
+
+# ---------------------------------------------------------------- 8 bits
+def exact_codes(x):
+    x = x.double()
+    top = x.abs().amax(1, keepdim=True)
+    return torch.where(top > 0, 127 * x / top, torch.zeros_like(x)), top[:, 0]
+
+
+@pytest.mark.parametrize("dim", [0, 1])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (5, 8), (33, 257), (64, 4096), (1000, 72), (3, 11008)])
+def test_quantize(hm, dim, dtype, rows, cols):
+    x = matrix((rows, cols), TYPES[dtype], gen(rows + cols), 2.0, margin=16)
+    x[rows // 2] = 0
+    if rows > 1:
+        x[0] = x[0].abs().amax() * torch.randint(-254, 255, (cols,), generator=gen(1), device=DEV).to(x.dtype) / 254
+        x[0, 0] = x[0].abs().amax()
+    xt = x.T if dim else x
+    L, n = xt.shape
+    q = torch.full((L, -(-n // 16) * 16 + 16), 99, dtype=torch.int8, device=DEV)
+    s = torch.empty(L, device=DEV)
+    hm.quantize([x], [q[:, :n]], [s], dim=dim)
+    want, top = exact_codes(xt)
+    assert torch.equal(s, (top / 127).float())
+    if dtype == "fp32":   # 127 x and the quotient are each rounded: a code may fall to the other side of a near tie
+        assert ((q[:, :n].double() - want).abs() <= 0.5 + 127 * 2.0 ** -22).all()
+    else:                 # halves are met exactly (round's ties go to even, as the codes')
+        assert torch.equal(q[:, :n].double(), want.round())
+    assert (q[:, n:] == 99).all()
+    assert hm.device_status() == 0
+
+
+def test_quantize_lists_and_nonfinite(hm):
+    g = gen(5)
+    shapes = [(3, 40), (100, 8), (1, 300)] * 30
+    xs = [matrix(s, [torch.bfloat16, torch.float32][i % 2], g) for i, s in enumerate(shapes)]
+    xs[0][1, 7], xs[1][50, 3], xs[3][0, 0] = float("nan"), float("-inf"), float("inf")
+    qs = [torch.full((r, -(-c // 16) * 16), 99, dtype=torch.int8, device=DEV)[:, :c] for r, c in shapes]
+    ss = [torch.empty(r, device=DEV) for r, _ in shapes]
+    hm.quantize(xs, qs, ss)
+    for i, (x, q, s) in enumerate(zip(xs, qs, ss)):
+        fine = torch.isfinite(x).all(1)
+        want, top = exact_codes(x[fine])
+        assert ((q[fine].double() - want).abs() <= 0.5 + 127 * 2.0 ** -22).all()
+        assert torch.equal(s[fine], (top / 127).float())
+        assert s[~fine].isnan().all() and (q[~fine] == 0).all()
+    assert int(sum((~torch.isfinite(x).all(1)).sum() for x in xs)) == 3
+    tiny = torch.tensor([[1e-40, -2e-40, 0, 0]] * 2, dtype=torch.bfloat16, device=DEV).repeat(1, 2).contiguous()
+    q, s = torch.empty(2, 16, dtype=torch.int8, device=DEV)[:, :8], torch.empty(2, device=DEV)
+    hm.quantize([tiny], [q], [s])
+    assert torch.equal(q.double(), exact_codes(tiny)[0].round())
+    hm.quantize([tiny[:0]], [q[:0]], [s[:0]])
+
+
+def check_i8(hm, out, K, N, counts, start=0, behind=0, listed=False, full=False, seed=0):
+    g = gen(seed)
+    n, off = len(counts), offsets(counts, start)
+    rows = start + sum(counts) + behind
+    pitch = -(-K // 16) * 16 + 16
+    lo, hi = (127, 128) if full else (-128, 128)
+    X = torch.randint(lo, hi, (rows, pitch), generator=g, device=DEV).to(torch.int8)[:, :K]
+    W = torch.randint(lo, hi, (n, N, pitch), generator=g, device=DEV).to(torch.int8)[:, :, :K]
+    xs = torch.rand(rows, generator=g, device=DEV) + 0.01
+    ws = torch.rand(n, N + 3, generator=g, device=DEV)[:, :N] + 0.01
+    xs[:start] = float("nan")
+    Y = torch.full((rows, -(-N // 8) * 8 + 8), -7.0, device=DEV).to(out)
+    hm.expert_product_i8(X, xs, [w for w in W] if listed else W, ws, Y[:, :N], off)
+    assert hm.device_status() == 0
+    for e, (a, b) in enumerate(groups(off)):
+        exact = (X[a:b].double() @ W[e].double().T) * xs[a:b].double()[:, None] * ws[e].double()
+        close(Y[a:b, :N], exact, exact.abs(), 0, out)
+    assert (Y[:start] == -7).all() and (Y[rows - behind:] == -7).all() and (Y[:, N:] == -7).all()
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("K,N,counts", [
+    (128, 128, [1]),
+    (1, 1, [3, 0, 1]),
+    (200, 136, [5, 0, 33, 130, 1]),
+    (129, 257, [31, 32, 33, 0]),
+    (1024, 384, [300, 257, 0, 256, 17]),
+    (4096, 136, [2, 9, 1, 1]),
+])
+def test_product_i8(hm, out, K, N, counts):
+    check_i8(hm, TYPES[out], K, N, counts, seed=K + N) if out != "fp16" else check_i8_small(hm, K, N, counts)
+
+
+def check_i8_small(hm, K, N, counts):
+    """fp16 results: scales that keep them in fp16's range."""
+    g = gen(K)
+    off, rows = offsets(counts), sum(counts)
+    pitch = -(-K // 16) * 16
+    X = torch.randint(-128, 128, (rows, pitch), generator=g, device=DEV).to(torch.int8)[:, :K]
+    W = torch.randint(-128, 128, (len(counts), N, pitch), generator=g, device=DEV).to(torch.int8)[:, :, :K]
+    xs, ws = torch.full((rows,), 1e-3, device=DEV), torch.full((len(counts), N), 2e-3, device=DEV)
+    Y = torch.empty(rows, -(-N // 8) * 8, device=DEV, dtype=torch.float16)[:, :N]
+    hm.expert_product_i8(X, xs, W, ws, Y, off)
+    for e, (a, b) in enumerate(groups(off)):
+        exact = (X[a:b].double() @ W[e].double().T) * xs[a:b].double()[:, None] * ws[e].double()
+        close(Y[a:b], exact, exact.abs(), 0, torch.float16)
+
+
+def test_product_i8_edges(hm):
+    check_i8(hm, torch.float32, 300, 200, [40, 0, 20], start=5, behind=9, listed=True)
+    check_i8(hm, torch.float32, 11008, 64, [3, 5], full=True)                    # sums beyond 2^24
+    check_i8(hm, torch.bfloat16, 131071, 8, [2], full=True)                      # the longest sum
+    check_i8(hm, torch.bfloat16, 64, 72, np.random.default_rng(1).integers(0, 3, 300).tolist())
+
+
+# ---------------------------------------------------------------- how they are called
+def test_bad_offsets_are_reported_and_stay_in_bounds(hm):
+    g = gen(11)
+    X, W = matrix((40, 64), torch.bfloat16, g), matrix((3, 64, 32), torch.bfloat16, g)
+    Y = torch.full((60, 32), -7.0, device=DEV, dtype=torch.bfloat16)
+    G = torch.empty(3, 64, 32, device=DEV)
+    q, w8 = torch.ones(40, 64, dtype=torch.int8, device=DEV), torch.ones(3, 32, 64, dtype=torch.int8, device=DEV)
+    s1, s2 = torch.ones(40, device=DEV), torch.ones(3, 32, device=DEV)
+    for bad in ([0, 10, 5, 40], [-3, 10, 20, 40], [0, 10, 20, 55], [0, 50, 20, 40], [70, 80, 90, 100]):
+        off = torch.tensor(bad, dtype=torch.int32, device=DEV)
+        hm.expert_product(X, W, Y[:40], off)
+        assert hm.device_status() == -7                                          # HIMUON_ERR_DEVICE
+        hm.expert_gradient(X, X[:, :32], G, off)
+        assert hm.device_status() == -7
+        hm.expert_product_i8(q, s1, w8, s2, Y[:40], off)
+        assert hm.device_status() == -7
+    assert (Y[40:] == -7).all()
+    assert hm.device_status() == 0
+
+
+def test_streams_and_graph_replay_with_new_offsets(hm):
+    """Two streams at once; two captured graphs, replayed in turn with other
+    offsets and inputs in the same buffers, beside eager calls."""
+    g = gen(12)
+    X, W = matrix((600, 256), torch.bfloat16, g), matrix((4, 256, 384), torch.bfloat16, g)
+    dY = matrix((600, 384), torch.bfloat16, g)
+    off = offsets([100, 200, 0, 300])
+    other = offsets([256, 1, 343, 0])
+
+    def eager(o):
+        y, gr = torch.zeros(600, 384, device=DEV), torch.zeros(4, 256, 384, device=DEV)
+        hm.expert_product(X, W, y, o)
+        hm.expert_gradient(X, dY, gr, o)
+        return y, gr
+
+    want, want_other = eager(off), eager(other)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for s, o in ((s1, off), (s2, other), (s1, other), (s2, off)):
+        y, gr = torch.zeros(600, 384, device=DEV), torch.zeros(4, 256, 384, device=DEV)
+        torch.cuda.synchronize()
+        got.append((y, gr, o, s))
+    for y, gr, o, s in got:
+        hm.expert_product(X, W, y, o, stream=s)
+        with torch.cuda.stream(s):
+            hm.expert_gradient(X, dY, gr, o)
+    torch.cuda.synchronize()
+    for y, gr, o, _ in got:
+        w = want if o is off else want_other
+        assert torch.equal(y, w[0]) and torch.equal(gr, w[1])
+
+    cur = off.clone()
+    outs = [(torch.zeros(600, 384, device=DEV), torch.zeros(4, 256, 384, device=DEV)) for _ in range(2)]
+    graphs = []
+    for y, gr in outs:
+        gph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gph):
+            hm.expert_product(X, W, y, cur)
+            hm.expert_gradient(X, dY, gr, cur)
+        graphs.append(gph)
+    for turn, (o, w) in enumerate(((off, want), (other, want_other), (off, want))):
+        cur.copy_(o)
+        for gph in graphs:
+            gph.replay()
+        y2, g2 = eager(o)
+        torch.cuda.synchronize()
+        for y, gr in (*outs, (y2, g2)):
+            assert torch.equal(y, w[0]) and torch.equal(gr, w[1])
+    assert hm.device_status() == 0
+
+
+def test_results_do_not_depend_on_other_groups_or_repeat(hm):
+    """The same call twice gives the same bits; so does a group alone and among others of other sizes."""
+    g = gen(13)
+    X, W = matrix((900, 512), torch.bfloat16, g), matrix((5, 512, 256), torch.bfloat16, g)
+    off = offsets([300, 0, 100, 477, 23])
+    Y = torch.empty(900, 256, device=DEV)
+    hm.expert_product(X, W, Y, off)
+    Z = torch.empty_like(Y)
+    hm.expert_product(X, W, Z, off)
+    assert torch.equal(Y, Z)
+    G, H = torch.empty(5, 512, 256, device=DEV), torch.empty(5, 512, 256, device=DEV)
+    hm.expert_gradient(X, X[:, :256], G, off)
+    hm.expert_gradient(X, X[:, :256], H, off)
+    assert torch.equal(G, H)
+
+
+def test_expert_layer_and_optimizer_step(hm):
+    """An expert layer's pass as it is used: forward, both gradients, the Muon step on the weights, the stepped
+    weights' 8-bit codes and the product with them."""
+    import oracle
+    from tiled_newton_schulz_b200 import inputs
+    g = gen(14)
+    n, K, N, rows = 3, 256, 384, 500
+    off = offsets([200, 0, 300])
+    W = matrix((n, K, N), torch.bfloat16, g, 0.05)
+    M = matrix((n, K, N), torch.bfloat16, g, 0.01)
+    X = matrix((rows, K), torch.bfloat16, g)
+    Y, dX = torch.empty(rows, N, device=DEV, dtype=torch.bfloat16), torch.empty(rows, K, device=DEV, dtype=torch.bfloat16)
+    G = torch.empty(n, K, N, device=DEV, dtype=torch.bfloat16)
+    w0, m0 = W.double(), M.double()
+    hm.expert_product(X, W, Y, off)
+    dY = (Y.float() * 1e-3).to(torch.bfloat16)
+    hm.expert_product(dY, W, dX, off, w_trans=True)
+    hm.expert_gradient(X, dY, G, off)
+    x, dy = X.double(), dY.double()
+    for e, (a, b) in enumerate(groups(off)):
+        close(Y[a:b], x[a:b] @ w0[e], x[a:b].abs() @ w0[e].abs(), K, torch.bfloat16)
+        close(dX[a:b], dy[a:b] @ w0[e].T, dy[a:b].abs() @ w0[e].abs().T, N, torch.bfloat16)
+        close(G[e], x[a:b].T @ dy[a:b], x[a:b].abs().T @ dy[a:b].abs(), b - a, torch.bfloat16)
+    p = hm.params(128, inputs.QUINTIC, steps=5)
+    hm.momentum_step(list(W), list(M), list(G), 0.95, 0.02, p)
+    c32 = [tuple(float(np.float32(v)) for v in inputs.QUINTIC)] * 5
+    for e in range(n):
+        w1, _, o = oracle.momentum_step(w0[e].cpu().numpy(), m0[e].cpu().numpy(), G[e].double().cpu().numpy(), 0.95,
+                                        0.02, 128, c32)
+        got = (w0[e].cpu().numpy() - W[e].double().cpu().numpy()) / 0.02
+        # the step's own bound (3e-2 of O) and the rounding of W to bf16, divided by lr
+        lim = 3e-2 * np.linalg.norm(o) + 2.0 ** -8 * np.linalg.norm(w1) / 0.02
+        assert np.linalg.norm(got - o) <= lim
+    q = torch.empty(n, N, K, dtype=torch.int8, device=DEV)
+    ws = torch.empty(n, N, device=DEV)
+    hm.quantize(list(W), list(q), list(ws), dim=1)
+    xq, xs = torch.empty(rows, K, dtype=torch.int8, device=DEV), torch.empty(rows, device=DEV)
+    hm.quantize([X], [xq], [xs])
+    Y8 = torch.empty(rows, N, device=DEV)
+    hm.expert_product_i8(xq, xs, q, ws, Y8, off)
+    hm.expert_product(X, W, Y, off)
+    for e, (a, b) in enumerate(groups(off)):
+        # each code is off by at most half a step of its row's or channel's scale
+        ex, ew = xs[a:b].double()[:, None] / 2, ws[e].double()[None, :] / 2
+        lim = (x[a:b].abs().sum(1, keepdim=True) * ew + ex * W[e].double().abs().sum(0, keepdim=True) + K * ex * ew)
+        d = (Y8[a:b].double() - x[a:b] @ W[e].double()).abs()
+        assert (d <= lim * (1 + 2.0 ** -20)).all()
+    assert hm.device_status() == 0

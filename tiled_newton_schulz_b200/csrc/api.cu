@@ -1050,6 +1050,9 @@ int64_t workspace_one(const CallMats &cm, const himuon_split *splits, const himu
 
 }  // namespace
 
+int device_usable() { return check_device(); }
+int *device_status_word() { return status_ptr(); }
+
 // Staged NS (in -> out) with every device byte it needs taken from one
 // caller-supplied region `scratch` of `scratch_bytes` (256-byte aligned): the
 // block and tile tables first, the per-chunk workspace after them.  Builds the

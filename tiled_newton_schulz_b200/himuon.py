@@ -15,12 +15,13 @@ from typing import Sequence
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libhimuon.so")
 
-BF16, FP16, FP32 = 0, 1, 2
+BF16, FP16, FP32, I8 = 0, 1, 2, 3
 OK = 0
 OP_NS_TILED, OP_NS_FULL, OP_GRAM_NS, OP_MOMENTUM_STEP = 0, 1, 2, 3
 EXPORTS = ("himuon_ns_tiled", "himuon_ns_full", "himuon_gram_ns", "himuon_momentum_step",
            "himuon_workspace_size", "himuon_get_device_status", "himuon_status_string",
-           "himuon_version", "himuon_plan_tiles", "himuon_launch_count", "himuon_ns_static")
+           "himuon_version", "himuon_plan_tiles", "himuon_launch_count", "himuon_ns_static",
+           "himuon_expert_product", "himuon_expert_gradient", "himuon_quantize", "himuon_expert_product_i8")
 ERR_TOO_LARGE = -9
 STATIC_SCRATCH_BYTES = 32 << 20
 
@@ -77,6 +78,14 @@ def load() -> ctypes.CDLL:
         lib.himuon_launch_count.restype = i64
         lib.himuon_plan_tiles.argtypes = [P(Mat), i32, P(Split), i32, P(i64), i64]
         lib.himuon_plan_tiles.restype = i64
+        f32 = ctypes.c_float
+        lib.himuon_expert_product.argtypes = [P(Mat), vp, i32, vp, i32, P(Mat), vp]
+        lib.himuon_expert_gradient.argtypes = [P(Mat), P(Mat), i32, vp, f32, f32, vp, vp, vp]
+        lib.himuon_quantize.argtypes = [vp, i32, i32, vp, vp, vp]
+        lib.himuon_expert_product_i8.argtypes = [P(Mat), P(Mat), vp, P(Mat), i32, vp, P(Mat), vp]
+        for name in ("himuon_expert_product", "himuon_expert_gradient", "himuon_quantize",
+                     "himuon_expert_product_i8"):
+            getattr(lib, name).restype = ctypes.c_int
         _lib = lib
     return _lib
 
@@ -94,7 +103,7 @@ def _check(code: int, what: str) -> None:
 
 def _dtype_code(t) -> int:
     import torch
-    return {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}[t.dtype]
+    return {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32, torch.int8: I8}[t.dtype]
 
 
 def mat(t) -> Mat:
@@ -242,6 +251,130 @@ def momentum_step(W, M, G, mu: float, lr: float, p: Params, splits=None, update_
                                      _stream(stream))
     _check(rc, "himuon_momentum_step")
     return _ws
+
+
+# ---------------------------------------------------------------- expert products
+# himuon_mat as a numpy record: a 3-D tensor of stacked matrices is described
+# by a few array operations instead of one ctypes record per matrix.
+_MAT_RECORD = None
+
+
+def _stack(ts):
+    """(himuon_mat array, its address, n) of a list of 2-D tensors or of a 3-D
+    tensor of stacked matrices (unit column stride)."""
+    import numpy as np
+    if hasattr(ts, "dim"):
+        global _MAT_RECORD
+        if ts.dim() != 3 or ts.stride(2) != 1:
+            raise ValueError("stacked matrices are a 3-D tensor with unit column stride")
+        if _MAT_RECORD is None:
+            _MAT_RECORD = np.dtype([("data", "i8"), ("rows", "i8"), ("cols", "i8"), ("ld", "i8"), ("dtype", "i4"),
+                                    ("pad", "i4")])
+        n, rows, cols = ts.shape
+        rec = np.empty(n, _MAT_RECORD)
+        rec[:] = (0, rows, cols, ts.stride(1), _dtype_code(ts), 0)
+        rec["data"] = ts.data_ptr() + np.arange(n) * (ts.stride(0) * ts.element_size())
+        return rec, rec.ctypes.data, n
+    arr = _mats(ts)
+    return arr, ctypes.addressof(arr), len(ts)
+
+
+def _row_vector(t) -> Mat:
+    """himuon_mat of a contiguous 1-D tensor (a 1 x len matrix)."""
+    if t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1):
+        raise ValueError("scales are contiguous 1-D tensors")
+    return Mat(t.data_ptr(), 1, t.shape[0], max(1, t.shape[0]), _dtype_code(t))
+
+
+def _one_device(*operands):
+    """The CUDA device that every tensor of the operands (tensors, lists of
+    them or None) is on."""
+    dev = None
+    for op in operands:
+        for t in (op if isinstance(op, (list, tuple)) else (op,)):
+            if t is None:
+                continue
+            if not t.is_cuda or (dev is not None and t.device != dev):
+                raise ValueError("expert products need all their tensors on one CUDA device")
+            dev = t.device
+    return dev
+
+
+def _offsets(offsets, n):
+    import torch
+    if offsets is None:
+        return None
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() != n + 1 or not offsets.is_contiguous():
+        raise ValueError(f"offsets are a contiguous int32 tensor of n + 1 = {n + 1} entries")
+    return offsets.data_ptr()
+
+
+def _on_device(dev, name, stream, *args):
+    """Calls the entry point with the operands' device current, on `stream` or
+    on that device's current stream."""
+    import torch
+    if stream is not None and stream.device != dev:
+        raise ValueError("the stream is on another device than the tensors")
+    with torch.cuda.device(dev):
+        s = stream if stream is not None else torch.cuda.current_stream(dev)
+        _check(getattr(load(), name)(*args, s.cuda_stream), name)
+
+
+def expert_product(X, W, Y, offsets=None, w_trans: bool = False, stream=None) -> None:
+    """Y[r] = X[r] W_e (W_e: K x N), or X[r] W_e^T with `w_trans` (W_e: N x K),
+    for the rows r of every group e.
+
+    X: rows x K, Y: rows x N; W: a list of n matrices or a 3-D tensor;
+    `offsets`: int32 CUDA tensor of n + 1 row bounds (None: n = 1, all rows).
+    Rows outside every group are left as they were.
+    """
+    dev = _one_device(X, W, Y, offsets)
+    keep, w, n = _stack(W)
+    _on_device(dev, "himuon_expert_product", stream, mat(X), w, n, _offsets(offsets, n), int(bool(w_trans)), mat(Y))
+
+
+def expert_gradient(A, B, G, offsets=None, alpha: float = 1.0, beta: float = 0.0, C=None, stream=None) -> None:
+    """G_e = alpha * A[rows of e]^T B[rows of e] + beta * C_e for every group e.
+
+    A: rows x P, B: rows x Q; G and C: lists of n P x Q matrices or 3-D
+    tensors (C may be G; not read with beta = 0).  An empty group gives
+    beta * C_e.
+    """
+    dev = _one_device(A, B, G, C, offsets)
+    keep, g, n = _stack(G)
+    keep_c, c, nc = _stack(C) if C is not None else (None, None, n)
+    if nc != n:
+        raise ValueError("G and C differ in length")
+    _on_device(dev, "himuon_expert_gradient", stream, mat(A), mat(B), n, _offsets(offsets, n), float(alpha),
+               float(beta), c, g)
+
+
+def quantize(inputs, codes, scales, dim: int = 0, stream=None) -> None:
+    """8-bit codes of each matrix: one scale per row (dim 0), or per column
+    with the codes transposed (dim 1).
+
+    inputs: list of 2-D float tensors; codes: int8 tensors (transposed shape
+    for dim 1); scales: 1-D fp32 tensors.
+    """
+    if not len(inputs) == len(codes) == len(scales):
+        raise ValueError("inputs, codes and scales differ in length")
+    dev = _one_device(list(inputs), list(codes), list(scales))
+    n = len(inputs)
+    sc = (Mat * max(1, n))(*[_row_vector(s) for s in scales])
+    _on_device(dev, "himuon_quantize", stream, _mats(inputs), n, int(dim), _mats(codes), sc)
+
+
+def expert_product_i8(X, x_scale, W, w_scale, Y, offsets=None, stream=None) -> None:
+    """Y[r, c] = x_scale[r] * w_scale[e, c] * sum_k X[r, k] W_e[c, k] for the
+    rows r of every group e, the sum exact in int32.
+
+    X: int8 rows x K, x_scale: fp32 per row, W: n int8 matrices N x K (list or
+    3-D tensor), w_scale: fp32 n x N, Y: rows x N.
+    """
+    dev = _one_device(X, x_scale, W, w_scale, Y, offsets)
+    keep, w, n = _stack(W)
+    _on_device(dev, "himuon_expert_product_i8", stream, mat(X), _row_vector(x_scale), w, mat(w_scale), n,
+               _offsets(offsets, n), mat(Y))
 
 
 def launch_count() -> int:
