@@ -18,18 +18,9 @@ int *device_status_word();   // api.cu: the current device's status word
 
 namespace {
 
-// Matrices of one launch, by value in the kernel's parameters: a list of up to
-// kMaxList pointers (a longer list runs as several launches, each on its own
-// stretch of the offsets).
-constexpr int kMaxList = 64;
-struct PtrList {
-  void *p[kMaxList];
-};
-
 __device__ __forceinline__ float ld_any(const void *p, int32_t dtype, int64_t i) {
   if (dtype == HIMUON_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
   if (dtype == HIMUON_FP16) return __half2float(static_cast<const __half *>(p)[i]);
-  if (dtype == HIMUON_I8) return static_cast<float>(static_cast<const int8_t *>(p)[i]);
   return static_cast<const float *>(p)[i];
 }
 __device__ __forceinline__ void st_any(void *p, int32_t dtype, int64_t i, float v) {
@@ -38,85 +29,457 @@ __device__ __forceinline__ void st_any(void *p, int32_t dtype, int64_t i, float 
   else static_cast<float *>(p)[i] = v;
 }
 
-// Rows [lo, hi) of group e; a bound outside 0 .. rows or below the one before
-// it is clamped and reported.
-__device__ __forceinline__ void group_rows(const int32_t *offsets, int32_t e, int64_t rows, int *status, int64_t &lo,
-                                           int64_t &hi) {
-  if (!offsets) {
-    lo = 0;
-    hi = rows;
-    return;
-  }
-  lo = offsets[e];
-  hi = offsets[e + 1];
-  if (lo < 0 || hi < lo || hi > rows) set_status(status, HIMUON_ERR_DEVICE);
-  lo = min(max(lo, (int64_t)0), rows);
-  hi = min(max(hi, lo), rows);
-}
+// One launch takes the matrices of up to kMaxStack groups when they lie at
+// equal distances (one tensor map, or a base and a stride), else a list of up
+// to kMaxList in the kernel's parameters; longer calls run as several
+// launches, each on its own stretch of the offsets.
+constexpr int kMaxList = 64;
+constexpr int kMaxStack = 256;
 
-struct ProductArgs {
-  const void *X;
-  int64_t rows, ldx;
-  PtrList W;
-  int64_t ldw;
+// ---------------------------------------------------------------- the product kernel
+// Both directions are one tcgen05 product per output tile, D (128 x up to 256,
+// fp32 or int32 in tensor memory) = A B^T over 128-byte stretches of K:
+//   product:  A = W_e (128 channels), B = X (up to 256 rows of group e), so the
+//             ragged side is the MMA's N, which is any multiple of 16: a group
+//             of 5 rows costs a 16-column tile, not a 128-row one.
+//   gradient: A = the 128 columns of operand A, B = 256 columns of operand B,
+//             K = the group's rows (both operands MN-major).
+constexpr uint32_t kABytes = 16384;     // 128 rows (or 2 x 64 MN columns) x 128 bytes of K
+constexpr uint32_t kBoxBytes = 4096;    // 32 rows of X x 128 bytes
+constexpr uint32_t kRing = 196608;      // operand ring
+constexpr int kMaxStages = 9;
+constexpr uint32_t kStageOut = 4096;    // per epilogue warp: 32 x 32 fp32, swizzled
+constexpr int kEpiWarps = 8;
+constexpr int kTileN = 256;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr uint32_t kBarBytes = 256;
+constexpr uint32_t kSmem = kRing + kEpiWarps * kStageOut + kBarBytes + 4 * (kMaxStack + 4) + 1024;
+static_assert(kSmem <= 232448, "shared memory of one CTA");
+
+template <int NMAP, int NPTR>
+struct MmaArgs {
+  CUtensorMap w[NMAP];     // product: W; gradient: operand A
+  CUtensorMap x;           // product: X; gradient: operand B
   const int32_t *offsets;
-  int32_t n, dtype, w_trans;
-  const float *x_scale;
-  const float *w_scale;   // row e: group e's channel scales, ld_scale apart
+  int64_t rows;
+  int32_t n;
+  int32_t K;               // product: length of the sums
+  int32_t M, N;            // product: M channels; gradient: G is M x N
+  uint32_t idesc;          // without the N field
+  int *status;
+  const float *x_scale, *w_scale;
   int64_t ld_scale;
-  void *Y;
-  int64_t ldy;
-  int32_t ydtype;
-  int64_t K, N;
-  int *status;
+  // outputs: product Y (one matrix), gradient G and C
+  char *out[NPTR];
+  const char *c[NPTR];
+  int64_t out_stride, c_stride;   // NPTR == 1: bytes between consecutive matrices
+  int64_t ldo, ldc;
+  int32_t odtype, cdtype, has_c;
+  float alpha, beta;
 };
 
-// One thread per output element, blocks of 16 rows x 16 columns of a group.
-template <typename Acc>
-__global__ void __launch_bounds__(256) product_kernel(const __grid_constant__ ProductArgs a) {
-  const int32_t e = blockIdx.z;
-  int64_t lo, hi;
-  group_rows(a.offsets, e, a.rows, a.status, lo, hi);
-  const int64_t c = blockIdx.x * 16ll + (threadIdx.x & 15);
-  for (int64_t r = lo + blockIdx.y * 16ll + (threadIdx.x >> 4); r < hi; r += 16ll * gridDim.y) {
-    if (c >= a.N) continue;
-    Acc acc = 0;
-    for (int64_t k = 0; k < a.K; ++k) {
-      const float w = ld_any(a.W.p[e], a.dtype, a.w_trans ? c * a.ldw + k : k * a.ldw + c);
-      acc += static_cast<Acc>(ld_any(a.X, a.dtype, r * a.ldx + k)) * static_cast<Acc>(w);
+__device__ __forceinline__ void mma_i8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// A bounded wait by a whole warp: its lanes agree whether to go on.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, int *status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, phase, status));
+}
+
+// Bound i of the groups, clamped into 0 .. rows.
+__device__ __forceinline__ int32_t bound_at(const int32_t *offsets, int32_t i, int64_t rows) {
+  if (!offsets) return i == 0 ? 0 : static_cast<int32_t>(rows);
+  return static_cast<int32_t>(min(max((int64_t)offsets[i], (int64_t)0), rows));
+}
+
+// A group of cnt rows runs as ceil(cnt / 256) tiles of equal width (a multiple of 16).
+__device__ __forceinline__ int32_t row_tiles(int32_t cnt) { return (cnt + kTileN - 1) / kTileN; }
+__device__ __forceinline__ int32_t tile_width(int32_t cnt) {
+  const int32_t mt = row_tiles(cnt);
+  return mt == 0 ? 0 : ((cnt + mt - 1) / mt + 15) / 16 * 16;
+}
+
+struct Tile {
+  int32_t e;        // group
+  int32_t m0;       // first row of D in the output: channel (product) or row of G
+  int32_t n0;       // product: first row of X; gradient: first column of G
+  int32_t width;    // columns of D: a multiple of 16
+  int32_t valid;    // of them, inside the output
+  int32_t lo, hi;   // the group's rows
+};
+
+template <int GRAD, typename Args>
+__device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int32_t idx) {
+  Tile t;
+  const int32_t mt_m = (a.M + 127) / 128;
+  if (GRAD) {
+    const int32_t mt_n = (a.N + kTileN - 1) / kTileN;
+    t.e = idx / (mt_m * mt_n);
+    const int32_t r = idx - t.e * mt_m * mt_n;
+    t.m0 = (r % mt_m) * 128;
+    t.n0 = (r / mt_m) * kTileN;
+    t.valid = min(kTileN, a.N - t.n0);
+    t.width = (t.valid + 15) / 16 * 16;
+    t.lo = bound_at(a.offsets, t.e, a.rows);
+    t.hi = max(t.lo, bound_at(a.offsets, t.e + 1, a.rows));
+  } else {
+    // the group whose row tiles hold row tile idx / mt_m: start[e] <= it < start[e + 1]
+    const int32_t u = idx / mt_m;
+    int32_t lo = 0, hi = a.n - 1;
+    while (lo < hi) {
+      const int32_t mid = (lo + hi + 1) / 2;
+      if (start[mid] <= u) lo = mid;
+      else hi = mid - 1;
     }
-    float v = static_cast<float>(acc);
-    if (a.x_scale) v = v * a.x_scale[r] * a.w_scale[e * a.ld_scale + c];
-    st_any(a.Y, a.ydtype, r * a.ldy + c, v);
+    t.e = lo;
+    t.lo = bound_at(a.offsets, t.e, a.rows);
+    t.hi = max(t.lo, bound_at(a.offsets, t.e + 1, a.rows));
+    const int32_t cnt = t.hi - t.lo, mt = row_tiles(cnt);
+    t.width = tile_width(cnt);
+    // bands of up to 8 row tiles, row tile fastest: the tiles in flight share
+    // a few panels of W and of X
+    const int32_t r = idx - start[t.e] * mt_m;
+    const int32_t g = r / (8 * mt_m), rr = r % (8 * mt_m);
+    const int32_t gm = min(8, mt - 8 * g);
+    const int32_t tt = 8 * g + rr % gm;
+    t.m0 = (rr / gm) * 128;
+    t.n0 = t.lo + tt * t.width;
+    t.valid = min(t.width, t.hi - t.n0);
+  }
+  return t;
+}
+
+__device__ __forceinline__ void ld4_any(const char *p, int32_t dtype, int64_t i, float (&v)[4]) {
+  if (dtype == HIMUON_FP32) {
+    const float4 f = *reinterpret_cast<const float4 *>(p + 4 * i);
+    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p + 2 * i);
+    float2 a, b;
+    if (dtype == HIMUON_FP16) {
+      a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
+      b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
+    } else {
+      a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.x));
+      b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.y));
+    }
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+  }
+}
+__device__ __forceinline__ uint32_t pack2(int32_t dtype, float x, float y) {
+  if (dtype == HIMUON_FP16) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// A staged 32 x 32 block (row r's 16-byte chunk c at chunk c ^ (r & 7)) to the
+// output: `rows` x `cols` of it are inside.  16-bit outputs: 4 lanes per row,
+// 8 columns each; fp32: 8 lanes per row, 4 columns each, so every row of the
+// block is written as one 64- or 128-byte run.
+template <int W16>
+__device__ __forceinline__ void write_block(const float *st, int lane, char *out, int32_t odtype, int64_t ldo,
+                                            int32_t rows, int32_t cols, float alpha, const char *c, int32_t cdtype,
+                                            int64_t ldc, float beta, const float *row_scale) {
+  constexpr int kLanes = W16 ? 4 : 8, kCols = W16 ? 8 : 4, kPass = W16 ? 4 : 8;
+  const int32_t col = (lane % kLanes) * kCols;
+  if (col >= cols) return;
+  const bool whole = col + kCols <= cols;
+  float cv[kPass][kCols];
+  if (c) {
+#pragma unroll
+    for (int p = 0; p < kPass; ++p) {
+      const int32_t r = lane / kLanes + p * (32 / kLanes);
+      if (r >= rows) continue;
+      const int64_t o = r * ldc + col;
+      if (whole) {
+#pragma unroll
+        for (int h = 0; h < kCols; h += 4) ld4_any(c, cdtype, o + h, *reinterpret_cast<float(*)[4]>(&cv[p][h]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) cv[p][j] = col + j < cols ? ld_any(c, cdtype, o + j) : 0.f;
+      }
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < kPass; ++p) {
+    const int32_t r = lane / kLanes + p * (32 / kLanes);
+    if (r >= rows) continue;
+    float v[kCols];
+#pragma unroll
+    for (int h = 0; h < kCols; h += 4) {
+      const float4 f = *reinterpret_cast<const float4 *>(st + r * 32 + (((col + h) >> 2) ^ (r & 7)) * 4);
+      v[h] = f.x; v[h + 1] = f.y; v[h + 2] = f.z; v[h + 3] = f.w;
+    }
+    if (row_scale) {
+      const float s = row_scale[r];
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) v[j] *= s;
+    }
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      v[j] *= alpha;
+      if (c) v[j] = fmaf(beta, cv[p][j], v[j]);
+    }
+    const int64_t o = r * ldo + col;
+    if (whole) {
+      if (W16)
+        *reinterpret_cast<uint4 *>(out + 2 * o) = make_uint4(pack2(odtype, v[0], v[1]), pack2(odtype, v[2], v[3]),
+                                                             pack2(odtype, v[4 % kCols], v[5 % kCols]),
+                                                             pack2(odtype, v[6 % kCols], v[7 % kCols]));
+      else
+        *reinterpret_cast<float4 *>(out + 4 * o) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kCols; ++j)
+        if (col + j < cols) st_any(out, odtype, o + j, v[j]);
+    }
   }
 }
 
-struct GradientArgs {
-  const void *A, *B;
-  int64_t rows, lda, ldb;
-  const int32_t *offsets;
-  int32_t n, dtype;
-  float alpha, beta;
-  PtrList C, G;
-  int64_t ldc, ldg;
-  int32_t cdtype, gdtype, has_c;
-  int64_t P, Q;
-  int *status;
-};
+// KIND 0: 16-bit operands (kind::f16); 1: int8 (kind::i8).  A_MN: A is
+// MN-major (W stored K x channels; the gradient's operands).
+template <int KIND, int A_MN, int GRAD, int NMAP, int NPTR>
+__global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_constant__ MmaArgs<NMAP, NPTR> a) {
+  constexpr int kElems = KIND ? 128 : 64;   // K elements per stage
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float *out_stage = reinterpret_cast<float *>(sm + kRing);
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + kRing + kEpiWarps * kStageOut);
+  uint64_t *empty = full + kMaxStages;
+  uint64_t *acc_full = empty + kMaxStages;   // [2] accumulator b holds a finished tile
+  uint64_t *acc_empty = acc_full + 2;        // [2] accumulator b drained
+  uint64_t *done = acc_empty + 2;            // every MMA issued has completed
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  int32_t *widest = reinterpret_cast<int32_t *>(tmem_slot + 1);
+  int32_t *start = reinterpret_cast<int32_t *>(sm + kRing + kEpiWarps * kStageOut + kBarBytes);   // [n + 1]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-__global__ void __launch_bounds__(256) gradient_kernel(const __grid_constant__ GradientArgs a) {
-  const int32_t e = blockIdx.z;
-  int64_t lo, hi;
-  group_rows(a.offsets, e, a.rows, a.status, lo, hi);
-  const int64_t q = blockIdx.x * 16ll + (threadIdx.x & 15);
-  for (int64_t p = blockIdx.y * 16ll + (threadIdx.x >> 4); p < a.P; p += 16ll * gridDim.y) {
-    if (q >= a.Q) continue;
-    float acc = 0.f;
-    for (int64_t r = lo; r < hi; ++r)
-      acc = fmaf(ld_any(a.A, a.dtype, r * a.lda + p), ld_any(a.B, a.dtype, r * a.ldb + q), acc);
-    float v = a.alpha * acc;
-    if (a.has_c) v = fmaf(a.beta, ld_any(a.C.p[e], a.cdtype, p * a.ldc + q), v);
-    st_any(a.G.p[e], a.gdtype, p * a.ldg + q, v);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full + b, 1);
+      mbar_init(acc_empty + b, kEpiWarps);
+    }
+    mbar_init(done, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&a.x);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp == 2) {
+    // start[e]: row tiles of the groups before e; widest: the widest tile
+    int32_t base = 0, w = 0;
+    for (int32_t e0 = 0; e0 < a.n; e0 += 32) {
+      const int32_t e = e0 + lane;
+      int32_t cnt = 0;
+      if (e < a.n) {
+        const int32_t lo = bound_at(a.offsets, e, a.rows), hi = bound_at(a.offsets, e + 1, a.rows);
+        cnt = max(hi - lo, 0);
+        if (a.offsets && (a.offsets[e] < 0 || a.offsets[e + 1] < a.offsets[e] || a.offsets[e + 1] > a.rows))
+          set_status(a.status, HIMUON_ERR_DEVICE);
+      }
+      w = max(w, tile_width(cnt));
+      int32_t s = row_tiles(cnt);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t up = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += up;
+      }
+      if (e < a.n) start[e + 1] = base + s;
+      base += __shfl_sync(0xffffffffu, s, 31);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) w = max(w, __shfl_xor_sync(0xffffffffu, w, o));
+    if (lane == 0) {
+      start[0] = 0;
+      *widest = w;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int32_t mt_m = (a.M + 127) / 128;
+  const int32_t n_tiles = GRAD ? a.n * mt_m * ((a.N + kTileN - 1) / kTileN) : start[a.n] * mt_m;
+  // a stage holds 128 rows of A and the widest tile's columns of B; narrow
+  // tiles (few rows per expert) get more stages, so that enough of W is in
+  // flight
+  const uint32_t b_bytes = GRAD ? (min(a.N, kTileN) + 63) / 64 * 8192u : (*widest + 31) / 32 * kBoxBytes;
+  const uint32_t stage_bytes = kABytes + b_bytes;
+  const int stages = min(static_cast<int>(kRing / stage_bytes), kMaxStages);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t phase = 1;   // parity of the stage's last release; the first round finds it free
+      bool ok = true;
+      int64_t issued = 0;
+      for (int32_t idx = blockIdx.x; idx < n_tiles && ok; idx += gridDim.x) {
+        const Tile t = tile_at<GRAD>(a, start, idx);
+        const int32_t len = GRAD ? t.hi - t.lo : a.K;
+        const CUtensorMap *mw = NMAP > 1 ? &a.w[t.e] : &a.w[0];
+        const int32_t z = NMAP > 1 ? 0 : t.e;
+        const int32_t boxes = GRAD ? (t.width + 63) / 64 : (t.width + 31) / 32;
+        const uint32_t bytes = kABytes + boxes * (GRAD ? 8192u : kBoxBytes);
+        for (int32_t k = 0; k < len; k += kElems) {
+          if (!(ok = mbar_wait(empty + s, phase, a.status))) break;
+          uint8_t *As = sm + s * stage_bytes, *Bs = As + kABytes;
+          mbar_arrive_expect_tx(full + s, bytes);
+          if (GRAD) {
+            tma_load_2d(As, &a.w[0], t.m0, t.lo + k, full + s);
+            tma_load_2d(As + 8192, &a.w[0], t.m0 + 64, t.lo + k, full + s);
+            for (int32_t j = 0; j < boxes; ++j) tma_load_2d(Bs + 8192 * j, &a.x, t.n0 + 64 * j, t.lo + k, full + s);
+          } else {
+            if (A_MN) {
+              tma_load_3d(As, mw, t.m0, k, z, full + s);
+              tma_load_3d(As + 8192, mw, t.m0 + 64, k, z, full + s);
+            } else {
+              tma_load_3d(As, mw, k, t.m0, z, full + s);
+            }
+            for (int32_t j = 0; j < boxes; ++j) tma_load_2d(Bs + kBoxBytes * j, &a.x, k, t.n0 + 32 * j, full + s);
+          }
+          ++issued;
+          if (++s == stages) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // gave up: wait (bounded) for the loads still in flight before the CTA ends
+      if (!ok) {
+        for (int64_t i = max((int64_t)0, issued - stages); i < issued; ++i)
+          mbar_wait(full + i % stages, static_cast<uint32_t>((i / stages) & 1), a.status);
+      }
+    }
+  } else if (warp == 1) {
+    int s = 0;
+    uint32_t phase = 0;
+    int32_t j = 0;
+    bool ok = true;
+    for (int32_t idx = blockIdx.x; idx < n_tiles && ok; idx += gridDim.x, ++j) {
+      const Tile t = tile_at<GRAD>(a, start, idx);
+      const int32_t len = GRAD ? t.hi - t.lo : a.K;
+      const int b = j & 1;
+      if (j >= 2 && !(ok = warp_wait(acc_empty + b, static_cast<uint32_t>(((j >> 1) - 1) & 1), a.status))) break;
+      tc_fence_after();
+      const uint32_t d = tmem + static_cast<uint32_t>(b * kTileN);
+      const uint32_t idesc = a.idesc | (static_cast<uint32_t>(t.width >> 3) << 17);
+      for (int32_t k = 0; k < len; k += kElems) {
+        if (!(ok = warp_wait(full + s, phase, a.status))) break;
+        tc_fence_after();
+        uint8_t *As = sm + s * stage_bytes;
+        const int32_t left = len - k;
+        if (GRAD && left < kElems && (left & 15)) {
+          // the rows behind the group (other groups' or none) up to the next
+          // multiple of 16 must be zero in both operands: each is 128 bytes in
+          // every 64-column box
+          const int32_t pad = 16 - (left & 15), boxes = 2 + (t.width + 63) / 64;
+          for (int32_t i = lane; i < boxes * pad * 8; i += 32)
+            *reinterpret_cast<uint4 *>(As + (i / (pad * 8)) * 8192 + (left + (i / 8) % pad) * 128 + (i & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          const uint32_t as = smem_u32(As), bs = as + kABytes;
+          const int32_t steps = min(4, (left + kElems / 4 - 1) / (kElems / 4));
+          for (int32_t kk = 0; kk < steps; ++kk) {
+            const uint64_t ad = A_MN ? sw128_desc(as + kk * 2048, 8192, 1024) : sw128_desc(as + kk * 32, 16, 1024);
+            const uint64_t bd = GRAD ? sw128_desc(bs + kk * 2048, 8192, 1024) : sw128_desc(bs + kk * 32, 16, 1024);
+            if (KIND) mma_i8_ss(d, ad, bd, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+            else mma_ss(d, ad, bd, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+          }
+          mma_commit(empty + s);   // the stage is free once these MMAs have read it
+        }
+        if (++s == stages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+      if (ok && lane == 0) mma_commit(acc_full + b);
+    }
+    if (lane == 0) {
+      mma_commit(done);
+      mbar_wait(done, 0, a.status);   // nothing of this CTA's is in flight when TMEM is released
+    }
+  } else {
+    const int q = warp & 3;             // TMEM lanes 32 q .. 32 q + 31
+    const int half = (warp - 2) >> 2;   // the warp's 32-column groups: half, half + 2, ..
+    float *st = out_stage + (warp - 2) * (kStageOut / 4);
+    const bool w16 = a.odtype != HIMUON_FP32;
+    const int64_t osize = w16 ? 2 : 4, csize = a.cdtype == HIMUON_FP32 ? 4 : 2;
+    int32_t j = 0;
+    for (int32_t idx = blockIdx.x; idx < n_tiles; idx += gridDim.x, ++j) {
+      const Tile t = tile_at<GRAD>(a, start, idx);
+      const int b = j & 1;
+      if (!warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + static_cast<uint32_t>(b * kTileN) + (static_cast<uint32_t>(q * 32) << 16);
+      const int32_t m = t.m0 + 32 * q;       // this warp's 32 rows of D
+      const int32_t m_in = min(32, a.M - m);
+      const bool empty_sum = GRAD && t.hi == t.lo;
+      char *out = (NPTR > 1 ? a.out[GRAD ? t.e : 0] : a.out[0] + (GRAD ? t.e * a.out_stride : 0));
+      const char *c = !GRAD || !a.has_c ? nullptr : (NPTR > 1 ? a.c[t.e] : a.c[0] + t.e * a.c_stride);
+      float chan = 1.f;
+      if (KIND && lane < m_in) chan = a.w_scale[t.e * a.ld_scale + m + lane];
+#pragma unroll 1
+      for (int32_t i = half; i < (t.valid + 31) / 32; i += 2) {
+        float v[32];
+        if (empty_sum) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = 0.f;
+        } else {
+          tmem_ld32(taddr + 32 * i, v);
+          tmem_wait_ld();
+        }
+        __syncwarp();   // the last block's readers are done
+        if (GRAD) {     // lane: row m + lane of G, its 32 columns
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<float4 *>(st + lane * 32 + ((k ^ (lane & 7)) * 4)) =
+                make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        } else {        // lane: channel m + lane of 32 rows of Y
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            st[k * 32 + (((lane >> 2) ^ (k & 7)) * 4) + (lane & 3)] =
+                KIND ? static_cast<float>(__float_as_int(v[k])) * chan : v[k];
+        }
+        __syncwarp();
+        if (m_in <= 0) continue;
+        const int32_t r_in = GRAD ? m_in : min(32, t.valid - 32 * i), c_in = GRAD ? min(32, t.valid - 32 * i) : m_in;
+        const int64_t r0 = GRAD ? m : t.n0 + 32 * i, c0 = GRAD ? t.n0 + 32 * i : m;
+        char *o = out + (r0 * a.ldo + c0) * osize;
+        const char *cc = c ? c + (r0 * a.ldc + c0) * csize : nullptr;
+        const float *rs = KIND ? a.x_scale + r0 : nullptr;
+        if (w16) write_block<1>(st, lane, o, a.odtype, a.ldo, r_in, c_in, a.alpha, cc, a.cdtype, a.ldc, a.beta, rs);
+        else write_block<0>(st, lane, o, a.odtype, a.ldo, r_in, c_in, a.alpha, cc, a.cdtype, a.ldc, a.beta, rs);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty + b);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -198,37 +561,178 @@ int check_scale(const himuon_mat *m, int64_t rows, int64_t cols) {
   return HIMUON_OK;
 }
 
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<EncodeTiledFn>(p)
+               : nullptr;
+  }();
+  return fn;
+}
+
+// Map over `n` row-major matrices `stride` bytes apart (2-D when n = 0): boxes
+// of 128 bytes of columns x box_rows, 128-byte swizzle, zeros outside.
+bool make_map(CUtensorMap *map, const himuon_mat &m, int32_t n, int64_t stride, uint32_t box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const int64_t es = static_cast<int64_t>(size_of(m.dtype));
+  const CUtensorMapDataType dt = m.dtype == HIMUON_I8     ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                 : m.dtype == HIMUON_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  // the pitch of a single row is never used and may be any number
+  const int64_t pitch = m.rows > 1 ? m.ld * es : (m.cols * es + 15) / 16 * 16;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(m.cols), static_cast<cuuint64_t>(m.rows),
+                        static_cast<cuuint64_t>(n > 0 ? n : 1)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch), static_cast<cuuint64_t>(n > 1 ? stride : pitch * m.rows)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), box_rows, 1};
+  cuuint32_t es1[3] = {1, 1, 1};
+  return enc(map, dt, n > 0 ? 3 : 2, m.data, dims, strides, box, es1, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Do the matrices lie at equal, positive distances (a multiple of 16 bytes, in
+// a tensor map's range)?  `stride`: that distance.
+bool stacked(const himuon_mat *m, int32_t n, int64_t *stride) {
+  *stride = 0;
+  if (n == 1) return true;
+  const int64_t d = static_cast<const char *>(m[1].data) - static_cast<const char *>(m[0].data);
+  if (d <= 0 || d % 16 != 0 || d >= (int64_t)1 << 39) return false;
+  for (int32_t e = 1; e < n; ++e)
+    if (static_cast<const char *>(m[e].data) - static_cast<const char *>(m[e - 1].data) != d) return false;
+  *stride = d;
+  return true;
+}
+
+int sm_count() {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+template <int KIND, int A_MN, int GRAD, int NMAP, int NPTR>
+int launch_mma(const MmaArgs<NMAP, NPTR> &a, int64_t most_tiles, cudaStream_t stream) {
+  auto kern = expert_kernel<KIND, A_MN, GRAD, NMAP, NPTR>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    return HIMUON_ERR_CUDA;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(most_tiles, sm_count()));
+  count_launch();
+  kern<<<grid, kThreads, kSmem, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? HIMUON_OK : HIMUON_ERR_CUDA;
+}
+
+template <int NMAP, int NPTR>
+void common_args(MmaArgs<NMAP, NPTR> &a, const int32_t *offsets, int32_t e0, int32_t n, int64_t rows) {
+  a.offsets = offsets ? offsets + e0 : nullptr;
+  a.rows = rows;
+  a.n = n;
+  a.status = device_status_word();
+  a.x_scale = a.w_scale = nullptr;
+  a.ld_scale = 0;
+  a.has_c = 0;
+  a.ldc = a.c_stride = a.out_stride = 0;
+  a.cdtype = HIMUON_FP32;
+  a.alpha = 1.f;
+  a.beta = 0.f;
+}
+
+// D format and operand formats of the instruction descriptor (its N field is
+// set per tile): f32 from bf16/fp16, or s32 from s8.
+uint32_t idesc_of(int32_t dtype, uint32_t a_mn, uint32_t b_mn) {
+  if (dtype == HIMUON_I8) return (2u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
+  return idesc_f16(128, 0, dtype == HIMUON_FP16 ? 0u : 1u, a_mn, b_mn, 0);
+}
+
+template <int NMAP>
+int product_launch(const himuon_mat *X, const float *x_scale, const himuon_mat *W, int64_t stride,
+                   const himuon_mat *w_scale, int32_t e0, int32_t n, const int32_t *offsets, int32_t w_trans,
+                   const himuon_mat *Y, cudaStream_t stream) {
+  MmaArgs<NMAP, 1> a;
+  common_args(a, offsets, e0, n, X->rows);
+  const uint32_t w_rows = w_trans ? 128 : 64;
+  for (int32_t i = 0; i < (NMAP > 1 ? n : 1); ++i)
+    if (!make_map(&a.w[i], W[e0 + i], NMAP > 1 ? 1 : n, stride, w_rows)) return HIMUON_ERR_CUDA;
+  if (!make_map(&a.x, *X, 0, 0, 32)) return HIMUON_ERR_CUDA;
+  a.K = static_cast<int32_t>(X->cols);
+  a.M = static_cast<int32_t>(Y->cols);
+  a.N = 0;
+  a.idesc = idesc_of(X->dtype, w_trans ? 0 : 1, 0);
+  if (x_scale) {
+    a.x_scale = x_scale;
+    a.w_scale = static_cast<const float *>(w_scale->data) + e0 * w_scale->ld;
+    a.ld_scale = w_scale->ld;
+  }
+  a.out[0] = static_cast<char *>(Y->data);
+  a.c[0] = nullptr;
+  a.ldo = Y->ld;
+  a.odtype = Y->dtype;
+  const int64_t mt_m = (Y->cols + 127) / 128;
+  const int64_t most = mt_m * (X->rows / kTileN + std::min<int64_t>(n, X->rows));
+  if (X->dtype == HIMUON_I8) return launch_mma<1, 0, 0>(a, most, stream);
+  return w_trans ? launch_mma<0, 0, 0>(a, most, stream) : launch_mma<0, 1, 0>(a, most, stream);
+}
+
 int run_product(const himuon_mat *X, const float *x_scale, const himuon_mat *W, const himuon_mat *w_scale, int32_t n,
                 const int32_t *offsets, int32_t w_trans, const himuon_mat *Y, cudaStream_t stream) {
   if (X->rows == 0) return HIMUON_OK;
-  for (int32_t e0 = 0; e0 < n; e0 += kMaxList) {
-    ProductArgs a;
-    a.n = std::min(n - e0, kMaxList);
-    a.X = X->data;
-    a.rows = X->rows;
-    a.ldx = X->ld;
-    for (int32_t e = 0; e < a.n; ++e) a.W.p[e] = W[e0 + e].data;
-    a.ldw = W->ld;
-    a.offsets = offsets ? offsets + e0 : nullptr;
-    a.dtype = X->dtype;
-    a.w_trans = w_trans;
-    a.x_scale = x_scale;
-    a.w_scale = w_scale ? static_cast<const float *>(w_scale->data) + e0 * w_scale->ld : nullptr;
-    a.ld_scale = w_scale ? w_scale->ld : 0;
-    a.Y = Y->data;
-    a.ldy = Y->ld;
-    a.ydtype = Y->dtype;
-    a.K = X->cols;
-    a.N = Y->cols;
-    a.status = device_status_word();
-    const dim3 grid(static_cast<unsigned>((a.N + 15) / 16),
-                    static_cast<unsigned>(std::min<int64_t>((a.rows + 15) / 16, 64)), static_cast<unsigned>(a.n));
-    count_launch();
-    if (X->dtype == HIMUON_I8) product_kernel<int32_t><<<grid, 256, 0, stream>>>(a);
-    else product_kernel<float><<<grid, 256, 0, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return HIMUON_ERR_CUDA;
+  int64_t stride;
+  const bool st = stacked(W, n, &stride);
+  const int32_t cap = st ? kMaxStack : kMaxList;
+  for (int32_t e0 = 0; e0 < n; e0 += cap) {
+    const int32_t cnt = std::min(n - e0, cap);
+    const int rc = st ? product_launch<1>(X, x_scale, W, stride, w_scale, e0, cnt, offsets, w_trans, Y, stream)
+                      : product_launch<kMaxList>(X, x_scale, W, 0, w_scale, e0, cnt, offsets, w_trans, Y, stream);
+    if (rc) return rc;
   }
   return HIMUON_OK;
+}
+
+template <int NPTR>
+int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_t n, const int32_t *offsets,
+                    float alpha, float beta, const himuon_mat *C, int64_t c_stride, const himuon_mat *G,
+                    int64_t g_stride, cudaStream_t stream) {
+  MmaArgs<1, NPTR> a;
+  common_args(a, offsets, e0, n, A->rows);
+  if (A->rows == 0) {
+    // no row is ever loaded: the maps only have to be valid, and G's memory is
+    himuon_mat any = *G;
+    any.dtype = A->dtype;
+    any.rows = 1;
+    any.cols = 8;
+    if (!make_map(&a.w[0], any, 0, 0, 64)) return HIMUON_ERR_CUDA;
+    a.x = a.w[0];
+  } else if (!make_map(&a.w[0], *A, 0, 0, 64) || !make_map(&a.x, *B, 0, 0, 64)) {
+    return HIMUON_ERR_CUDA;
+  }
+  a.K = 0;
+  a.M = static_cast<int32_t>(A->cols);
+  a.N = static_cast<int32_t>(B->cols);
+  a.idesc = idesc_of(A->dtype, 1, 1);
+  a.alpha = alpha;
+  a.beta = beta;
+  a.has_c = C != nullptr;
+  for (int32_t i = 0; i < (NPTR > 1 ? n : 1); ++i) {
+    a.out[i] = static_cast<char *>(G[e0 + i].data);
+    a.c[i] = C ? static_cast<const char *>(C[e0 + i].data) : nullptr;
+  }
+  a.out_stride = g_stride;
+  a.c_stride = c_stride;
+  a.ldo = G->ld;
+  a.odtype = G->dtype;
+  if (C) {
+    a.ldc = C->ld;
+    a.cdtype = C->dtype;
+  }
+  const int64_t most = n * ((A->cols + 127) / 128) * ((B->cols + kTileN - 1) / kTileN);
+  return launch_mma<0, 1, 1>(a, most, stream);
 }
 
 }  // namespace
@@ -293,35 +797,16 @@ int himuon_expert_gradient(const himuon_mat *A, const himuon_mat *B, int32_t n, 
   if (std::adjacent_find(seen.begin(), seen.end()) != seen.end()) return HIMUON_ERR_INVALID;
   rc = device_usable();
   if (rc) return rc;
-  for (int32_t e0 = 0; e0 < n; e0 += kMaxList) {
-    GradientArgs a;
-    a.n = std::min(n - e0, kMaxList);
-    a.A = A->data;
-    a.B = B->data;
-    a.rows = A->rows;
-    a.lda = A->ld;
-    a.ldb = B->ld;
-    a.offsets = offsets ? offsets + e0 : nullptr;
-    a.dtype = A->dtype;
-    a.alpha = alpha;
-    a.beta = beta;
-    a.has_c = beta != 0.f;
-    for (int32_t e = 0; e < a.n; ++e) {
-      a.G.p[e] = G[e0 + e].data;
-      a.C.p[e] = a.has_c ? C[e0 + e].data : nullptr;
-    }
-    a.ldc = a.has_c ? C->ld : 0;
-    a.cdtype = a.has_c ? C->dtype : 0;
-    a.ldg = G->ld;
-    a.gdtype = G->dtype;
-    a.P = A->cols;
-    a.Q = B->cols;
-    a.status = device_status_word();
-    const dim3 grid(static_cast<unsigned>((a.Q + 15) / 16),
-                    static_cast<unsigned>(std::min<int64_t>((a.P + 15) / 16, 64)), static_cast<unsigned>(a.n));
-    count_launch();
-    gradient_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return HIMUON_ERR_CUDA;
+  if (beta == 0.f) C = nullptr;
+  int64_t g_stride, c_stride = 0;
+  const bool st = stacked(G, n, &g_stride) && (!C || stacked(C, n, &c_stride));
+  const int32_t cap = st ? kMaxStack : kMaxList;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  for (int32_t e0 = 0; e0 < n; e0 += cap) {
+    const int32_t cnt = std::min(n - e0, cap);
+    rc = st ? gradient_launch<1>(A, B, e0, cnt, offsets, alpha, beta, C, c_stride, G, g_stride, s)
+            : gradient_launch<kMaxList>(A, B, e0, cnt, offsets, alpha, beta, C, 0, G, 0, s);
+    if (rc) return rc;
   }
   return HIMUON_OK;
 }
