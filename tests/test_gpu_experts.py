@@ -226,6 +226,18 @@ def test_gradient_many_experts(hm, n, listed):
     check_gradient(hm, torch.bfloat16, torch.bfloat16, 72, 136, rng.integers(0, 6, n).tolist(), listed=listed)
 
 
+@pytest.mark.parametrize("counts", [[80, 37, 16, 100, 0, 192], [5, 144, 63, 64, 1000, 33], [17, 48, 300, 49, 2, 0, 31]])
+def test_gradient_many_tiles_per_cta_pair(hm, counts):
+    """Every pair runs several tiles, of groups whose last stretch of rows is whole, a multiple of 16 or neither."""
+    check_gradient(hm, torch.bfloat16, torch.float32, 1032, 2050, counts)
+
+
+@pytest.mark.parametrize("trans", [False, True])
+def test_product_many_tiles_per_cta_pair(hm, trans):
+    check_product(hm, torch.bfloat16, torch.bfloat16, 208, 4104, [257, 513, 1, 0, 700, 64, 31, 1025], trans)
+    check_i8(hm, torch.float32, 400, 2056, [257, 513, 1, 0, 700, 64, 31, 1025])
+
+
 def test_gradient_long_sum(hm):
     check_gradient(hm, torch.bfloat16, torch.float32, 200, 264, [5003, 1])
     check_gradient(hm, torch.bfloat16, torch.bfloat16, 64, 64, [9001])
@@ -309,6 +321,19 @@ def test_quantize_lists_and_nonfinite(hm):
         assert torch.equal(s[fine], (top / 127).float())
         assert s[~fine].isnan().all() and (q[~fine] == 0).all()
     assert int(sum((~torch.isfinite(x).all(1)).sum() for x in xs)) == 3
+    big = matrix((4, 264), torch.bfloat16, g, 1e37)       # 127 x is out of fp32's range
+    big[1] *= 20
+    for dim in (0, 1):
+        q = torch.empty(4, 272, dtype=torch.int8, device=DEV)[:, :264] if dim == 0 else \
+            torch.empty(264, 16, dtype=torch.int8, device=DEV)[:, :4]
+        s = torch.empty(4 if dim == 0 else 264, device=DEV)
+        hm.quantize([big], [q], [s], dim=dim)
+        lines = big.T if dim else big                        # (row 1 overflows bf16 in places)
+        fine = torch.isfinite(lines).all(1)
+        want, top = exact_codes(lines[fine])
+        assert torch.equal(q[fine].double(), want.round()) and torch.equal(s[fine], (top / 127).float())
+        assert s[~fine].isnan().all() and (q[~fine] == 0).all()
+    assert hm.device_status() == 0
     tiny = torch.tensor([[1e-40, -2e-40, 0, 0]] * 2, dtype=torch.bfloat16, device=DEV).repeat(1, 2).contiguous()
     q, s = torch.empty(2, 16, dtype=torch.int8, device=DEV)[:, :8], torch.empty(2, device=DEV)
     hm.quantize([tiny], [q], [s])

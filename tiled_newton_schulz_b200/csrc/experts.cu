@@ -37,29 +37,29 @@ constexpr int kMaxList = 64;
 constexpr int kMaxStack = 256;
 
 // ---------------------------------------------------------------- the product kernel
-// Both directions are one tcgen05 product per output tile, D (128 x up to 256,
+// Both directions are one tcgen05 product per output tile, D (256 x up to 256,
 // fp32 or int32 in tensor memory) = A B^T over 128-byte stretches of K:
-//   product:  A = W_e (128 channels), B = X (up to 256 rows of group e), so the
-//             ragged side is the MMA's N, which is any multiple of 16: a group
-//             of 5 rows costs a 16-column tile, not a 128-row one.
-//   gradient: A = the 128 columns of operand A, B = 256 columns of operand B,
+//   product:  A = W_e (256 channels), B = X (up to 256 rows of group e), so the
+//             ragged side is the MMA's N, which is any multiple of 32: a group
+//             of 5 rows costs a 32-column tile, not a 128-row one.
+//   gradient: A = 256 columns of operand A, B = 256 columns of operand B,
 //             K = the group's rows (both operands MN-major).
 constexpr uint32_t kABytes = 16384;     // 128 rows (or 2 x 64 MN columns) x 128 bytes of K
-constexpr uint32_t kBoxBytes = 4096;    // 32 rows of X x 128 bytes
+constexpr uint32_t kBoxBytes = 2048;    // 16 rows of X x 128 bytes
 constexpr uint32_t kRing = 196608;      // operand ring
-constexpr int kMaxStages = 9;
+constexpr int kMaxStages = 10;
 constexpr uint32_t kStageOut = 4096;    // per epilogue warp: 32 x 32 fp32, swizzled
 constexpr int kEpiWarps = 8;
-constexpr int kTileN = 256;
+constexpr int kTileM = 256, kTileN = 256;   // a CTA pair's tile of D
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr uint32_t kBarBytes = 256;
+constexpr uint32_t kBarBytes = 384;
 constexpr uint32_t kSmem = kRing + kEpiWarps * kStageOut + kBarBytes + 4 * (kMaxStack + 4) + 1024;
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
 template <int NMAP, int NPTR>
 struct MmaArgs {
   CUtensorMap w[NMAP];     // product: W; gradient: operand A
-  CUtensorMap x;           // product: X; gradient: operand B
+  CUtensorMap x[4];        // product: X in boxes of 128, 64, 32 and 16 rows; gradient: [0] operand B
   const int32_t *offsets;
   int64_t rows;
   int32_t n;
@@ -78,19 +78,58 @@ struct MmaArgs {
   float alpha, beta;
 };
 
-__device__ __forceinline__ void mma_i8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// Pair forms (CTA pairs, issued by the even CTA): both operands from shared
+// memory at the same offsets in both CTAs.
+__device__ __forceinline__ void mma_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-
+__device__ __forceinline__ void mma_i8_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// TMA loads into this CTA's shared memory that complete on an mbarrier of
+// either CTA of the pair (a shared::cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, int32_t x, int32_t y,
+                                                 uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar_cluster)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z,
+                                                 uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+      "%4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar_cluster)
+      : "memory");
+}
 // A bounded wait by a whole warp: its lanes agree whether to go on.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, int *status) {
   return __all_sync(0xffffffffu, mbar_wait(bar, phase, status));
+}
+// One thread's bounded wait for a phase that the pair's other CTA also arrives on.
+__device__ __forceinline__ bool lane_wait_cluster(uint64_t *bar, uint32_t phase, int *status) {
+  bool ok = mbar_try_wait_cluster(bar, phase);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1; !(ok = mbar_try_wait_cluster(bar, phase)); ++i)
+      if ((i & 255u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) break;
+    if (!ok) set_status(status, HIMUON_ERR_TIMEOUT_DEV);
+  }
+  return ok;
 }
 
 // Bound i of the groups, clamped into 0 .. rows.
@@ -99,18 +138,21 @@ __device__ __forceinline__ int32_t bound_at(const int32_t *offsets, int32_t i, i
   return static_cast<int32_t>(min(max((int64_t)offsets[i], (int64_t)0), rows));
 }
 
-// A group of cnt rows runs as ceil(cnt / 256) tiles of equal width (a multiple of 16).
+__device__ __forceinline__ int32_t m_tiles(int32_t M) { return (M + kTileM - 1) / kTileM; }
+__device__ __forceinline__ int32_t round32(int32_t x) { return (x + 31) / 32 * 32; }
+// A group of cnt rows runs as ceil(cnt / 256) tiles of equal width (a multiple
+// of 32: the pair's CTAs hold half of the rows each, in boxes of 16).
 __device__ __forceinline__ int32_t row_tiles(int32_t cnt) { return (cnt + kTileN - 1) / kTileN; }
 __device__ __forceinline__ int32_t tile_width(int32_t cnt) {
   const int32_t mt = row_tiles(cnt);
-  return mt == 0 ? 0 : ((cnt + mt - 1) / mt + 15) / 16 * 16;
+  return mt == 0 ? 0 : ((cnt + mt - 1) / mt + 31) / 32 * 32;
 }
 
 struct Tile {
   int32_t e;        // group
   int32_t m0;       // first row of D in the output: channel (product) or row of G
   int32_t n0;       // product: first row of X; gradient: first column of G
-  int32_t width;    // columns of D: a multiple of 16
+  int32_t width;    // columns of D: a multiple of 32
   int32_t valid;    // of them, inside the output
   int32_t lo, hi;   // the group's rows
 };
@@ -118,15 +160,15 @@ struct Tile {
 template <int GRAD, typename Args>
 __device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int32_t idx) {
   Tile t;
-  const int32_t mt_m = (a.M + 127) / 128;
+  const int32_t mt_m = m_tiles(a.M);
   if (GRAD) {
     const int32_t mt_n = (a.N + kTileN - 1) / kTileN;
     t.e = idx / (mt_m * mt_n);
     const int32_t r = idx - t.e * mt_m * mt_n;
-    t.m0 = (r % mt_m) * 128;
+    t.m0 = (r % mt_m) * kTileM;
     t.n0 = (r / mt_m) * kTileN;
     t.valid = min(kTileN, a.N - t.n0);
-    t.width = (t.valid + 15) / 16 * 16;
+    t.width = round32(t.valid);
     t.lo = bound_at(a.offsets, t.e, a.rows);
     t.hi = max(t.lo, bound_at(a.offsets, t.e + 1, a.rows));
   } else {
@@ -149,7 +191,7 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int
     const int32_t g = r / (8 * mt_m), rr = r % (8 * mt_m);
     const int32_t gm = min(8, mt - 8 * g);
     const int32_t tt = 8 * g + rr % gm;
-    t.m0 = (rr / gm) * 128;
+    t.m0 = (rr / gm) * kTileM;
     t.n0 = t.lo + tt * t.width;
     t.valid = min(t.width, t.hi - t.n0);
   }
@@ -248,38 +290,55 @@ __device__ __forceinline__ void write_block(const float *st, int lane, char *out
 
 // KIND 0: 16-bit operands (kind::f16); 1: int8 (kind::i8).  A_MN: A is
 // MN-major (W stored K x channels; the gradient's operands).
+//
+// A pair of CTAs (cluster of 2) works on one 256-row tile of D: each CTA holds
+// 128 of its rows (in its tensor memory) and of A's, and half of B's columns;
+// the even CTA issues the MMAs for both.  A single CTA with the same 128 x 256
+// tile writes and reads 96 + 96 bytes of operands per cycle of MMA in its
+// shared memory, more than its 128 bytes per cycle; the pair needs 64 + 64.
+// Persistent: warp 0 streams its CTA's operands through a ring of stages (TMA,
+// completing on the even CTA's barriers), warp 1 of the even CTA issues each
+// tile's MMAs into one of two accumulators, warps 2..9 of both drain the other
+// one meanwhile.
 template <int KIND, int A_MN, int GRAD, int NMAP, int NPTR>
-__global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_constant__ MmaArgs<NMAP, NPTR> a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    expert_kernel(const __grid_constant__ MmaArgs<NMAP, NPTR> a) {
   constexpr int kElems = KIND ? 128 : 64;   // K elements per stage
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float *out_stage = reinterpret_cast<float *>(sm + kRing);
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm + kRing + kEpiWarps * kStageOut);
-  uint64_t *empty = full + kMaxStages;
-  uint64_t *acc_full = empty + kMaxStages;   // [2] accumulator b holds a finished tile
-  uint64_t *acc_empty = acc_full + 2;        // [2] accumulator b drained
-  uint64_t *done = acc_empty + 2;            // every MMA issued has completed
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + kRing + kEpiWarps * kStageOut);   // even CTA: both CTAs' loads
+  uint64_t *empty = full + kMaxStages;        // each CTA: the stage's MMAs have read it
+  uint64_t *tail_full = empty + kMaxStages;   // each CTA: its own loads of a block that needs zeros
+  uint64_t *tail_ready = tail_full + kMaxStages;   // even CTA: both CTAs have written the zeros
+  uint64_t *acc_full = tail_ready + kMaxStages;    // [2] each CTA: accumulator b holds a finished tile
+  uint64_t *acc_empty = acc_full + 2;              // [2] even CTA: accumulator b drained by both CTAs
+  uint64_t *done = acc_empty + 2;                  // even CTA: every MMA issued has completed
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   int32_t *widest = reinterpret_cast<int32_t *>(tmem_slot + 1);
   int32_t *start = reinterpret_cast<int32_t *>(sm + kRing + kEpiWarps * kStageOut + kBarBytes);   // [n + 1]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t rank = static_cast<int32_t>(cluster_ctarank());
+  const int32_t first = static_cast<int32_t>(blockIdx.x >> 1), step = static_cast<int32_t>(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
+      mbar_init(tail_full + s, 1);
+      mbar_init(tail_ready + s, 2);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full + b, 1);
-      mbar_init(acc_empty + b, kEpiWarps);
+      mbar_init(acc_empty + b, 2 * kEpiWarps);
     }
     mbar_init(done, 1);
     fence_mbar_init();
-    tma_prefetch_desc(&a.x);
+    tma_prefetch_desc(&a.x[0]);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
   }
   if (warp == 2) {
     // start[e]: row tiles of the groups before e; widest: the widest tile
@@ -310,48 +369,76 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       *widest = w;
     }
   }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync_all();   // barriers of both CTAs are ready before either is signalled
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int32_t mt_m = (a.M + 127) / 128;
+  const int32_t mt_m = m_tiles(a.M);
   const int32_t n_tiles = GRAD ? a.n * mt_m * ((a.N + kTileN - 1) / kTileN) : start[a.n] * mt_m;
-  // a stage holds 128 rows of A and the widest tile's columns of B; narrow
-  // tiles (few rows per expert) get more stages, so that enough of W is in
-  // flight
-  const uint32_t b_bytes = GRAD ? (min(a.N, kTileN) + 63) / 64 * 8192u : (*widest + 31) / 32 * kBoxBytes;
-  const uint32_t stage_bytes = kABytes + b_bytes;
+  // a stage holds 128 rows of A and half of the widest tile's columns of B;
+  // narrow tiles (few rows per expert) get more stages, so that enough of W is
+  // in flight
+  const uint32_t b_bytes =
+      GRAD ? (round32(min(a.N, kTileN)) / 2 + 63) / 64 * 8192u : (*widest + 31) / 32 * kBoxBytes;
+  const uint32_t stage_bytes = (kABytes + b_bytes + 1023) / 1024 * 1024;
   const int stages = min(static_cast<int>(kRing / stage_bytes), kMaxStages);
 
   if (warp == 0) {
     if (lane == 0) {
+      const uint32_t full0 = mapa_shared(smem_u32(full), 0);
       int s = 0;
       uint32_t phase = 1;   // parity of the stage's last release; the first round finds it free
       bool ok = true;
       int64_t issued = 0;
-      for (int32_t idx = blockIdx.x; idx < n_tiles && ok; idx += gridDim.x) {
+      uint32_t was_tail = 0, tail_phase = 0;   // per stage: its last block's kind; tail_full's next parity
+      for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
         const Tile t = tile_at<GRAD>(a, start, idx);
         const int32_t len = GRAD ? t.hi - t.lo : a.K;
         const CUtensorMap *mw = NMAP > 1 ? &a.w[t.e] : &a.w[0];
         const int32_t z = NMAP > 1 ? 0 : t.e;
-        const int32_t boxes = GRAD ? (t.width + 63) / 64 : (t.width + 31) / 32;
+        const int32_t half = t.width / 2;
+        const int32_t m0 = t.m0 + 128 * rank, n0 = t.n0 + half * rank;
+        const int32_t boxes = GRAD ? (half + 63) / 64 : half / 16;
         const uint32_t bytes = kABytes + boxes * (GRAD ? 8192u : kBoxBytes);
         for (int32_t k = 0; k < len; k += kElems) {
           if (!(ok = mbar_wait(empty + s, phase, a.status))) break;
           uint8_t *As = sm + s * stage_bytes, *Bs = As + kABytes;
-          mbar_arrive_expect_tx(full + s, bytes);
           if (GRAD) {
-            tma_load_2d(As, &a.w[0], t.m0, t.lo + k, full + s);
-            tma_load_2d(As + 8192, &a.w[0], t.m0 + 64, t.lo + k, full + s);
-            for (int32_t j = 0; j < boxes; ++j) tma_load_2d(Bs + 8192 * j, &a.x, t.n0 + 64 * j, t.lo + k, full + s);
-          } else {
-            if (A_MN) {
-              tma_load_3d(As, mw, t.m0, k, z, full + s);
-              tma_load_3d(As + 8192, mw, t.m0 + 64, k, z, full + s);
+            const int32_t y = t.lo + k;
+            const bool tail = len - k < kElems && ((len - k) & 15);
+            was_tail = (was_tail & ~(1u << s)) | (static_cast<uint32_t>(tail) << s);
+            if (tail) {   // lands on this CTA's own barrier: its warp 1 has zeros to write before the MMAs
+              if (rank == 0) mbar_arrive(full + s);
+              mbar_arrive_expect_tx(tail_full + s, bytes);
+              tail_phase ^= 1u << s;
+              tma_load_2d(As, &a.w[0], m0, y, tail_full + s);
+              tma_load_2d(As + 8192, &a.w[0], m0 + 64, y, tail_full + s);
+              for (int32_t j = 0; j < boxes; ++j) tma_load_2d(Bs + 8192 * j, &a.x[0], n0 + 64 * j, y, tail_full + s);
             } else {
-              tma_load_3d(As, mw, k, t.m0, z, full + s);
+              if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * bytes);
+              const uint32_t bar = full0 + 8 * s;
+              tma_load_2d_pair(As, &a.w[0], m0, y, bar);
+              tma_load_2d_pair(As + 8192, &a.w[0], m0 + 64, y, bar);
+              for (int32_t j = 0; j < boxes; ++j) tma_load_2d_pair(Bs + 8192 * j, &a.x[0], n0 + 64 * j, y, bar);
             }
-            for (int32_t j = 0; j < boxes; ++j) tma_load_2d(Bs + kBoxBytes * j, &a.x, k, t.n0 + 32 * j, full + s);
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * bytes);
+            const uint32_t bar = full0 + 8 * s;
+            if (A_MN) {
+              tma_load_3d_pair(As, mw, m0, k, z, bar);
+              tma_load_3d_pair(As + 8192, mw, m0 + 64, k, z, bar);
+            } else {
+              tma_load_3d_pair(As, mw, k, m0, z, bar);
+            }
+            // this CTA's rows of the tile in at most four boxes, the largest first
+            int32_t at = 0;
+#pragma unroll
+            for (int32_t i = 0; i < 4; ++i)
+              if (boxes & (8 >> i)) {
+                tma_load_2d_pair(Bs + kBoxBytes * at, &a.x[i], k, n0 + 16 * at, bar);
+                at += 8 >> i;
+              }
           }
           ++issued;
           if (++s == stages) {
@@ -360,62 +447,104 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
           }
         }
       }
-      // gave up: wait (bounded) for the loads still in flight before the CTA ends
-      if (!ok) {
-        for (int64_t i = max((int64_t)0, issued - stages); i < issued; ++i)
-          mbar_wait(full + i % stages, static_cast<uint32_t>((i / stages) & 1), a.status);
+      // the last loads have landed before the CTA ends, also when something
+      // gave up (the even CTA's barriers see both CTAs' loads; the CTAs leave
+      // together)
+      for (int64_t i = max((int64_t)0, issued - stages); i < issued; ++i) {
+        const int st = static_cast<int>(i % stages);
+        if ((was_tail >> st) & 1) mbar_wait(tail_full + st, ((tail_phase >> st) & 1) ^ 1, a.status);
+        else if (rank == 0) mbar_wait(full + st, static_cast<uint32_t>((i / stages) & 1), a.status);
       }
     }
   } else if (warp == 1) {
-    int s = 0;
-    uint32_t phase = 0;
-    int32_t j = 0;
-    bool ok = true;
-    for (int32_t idx = blockIdx.x; idx < n_tiles && ok; idx += gridDim.x, ++j) {
-      const Tile t = tile_at<GRAD>(a, start, idx);
-      const int32_t len = GRAD ? t.hi - t.lo : a.K;
-      const int b = j & 1;
-      if (j >= 2 && !(ok = warp_wait(acc_empty + b, static_cast<uint32_t>(((j >> 1) - 1) & 1), a.status))) break;
-      tc_fence_after();
-      const uint32_t d = tmem + static_cast<uint32_t>(b * kTileN);
-      const uint32_t idesc = a.idesc | (static_cast<uint32_t>(t.width >> 3) << 17);
-      for (int32_t k = 0; k < len; k += kElems) {
-        if (!(ok = warp_wait(full + s, phase, a.status))) break;
+    if (rank == 0 || GRAD) {
+      const uint32_t ready0 = mapa_shared(smem_u32(tail_ready), 0);
+      int s = 0;
+      uint32_t phase = 0, tail_phase = 0;
+      int32_t j = 0;
+      bool ok = true;
+      // the MMAs over one stage, K elements k .. of `len` (even CTA, lane 0)
+      auto issue = [&](uint32_t d, uint32_t idesc, int32_t k, int32_t left) {
         tc_fence_after();
-        uint8_t *As = sm + s * stage_bytes;
-        const int32_t left = len - k;
-        if (GRAD && left < kElems && (left & 15)) {
-          // the rows behind the group (other groups' or none) up to the next
-          // multiple of 16 must be zero in both operands: each is 128 bytes in
-          // every 64-column box
-          const int32_t pad = 16 - (left & 15), boxes = 2 + (t.width + 63) / 64;
-          for (int32_t i = lane; i < boxes * pad * 8; i += 32)
-            *reinterpret_cast<uint4 *>(As + (i / (pad * 8)) * 8192 + (left + (i / 8) % pad) * 128 + (i & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
+        const uint32_t as = smem_u32(sm + s * stage_bytes), bs = as + kABytes;
+#pragma unroll
+        for (int32_t kk = 0; kk < 4; ++kk) {
+          if (kk * (kElems / 4) >= left) break;
+          const uint64_t ad = A_MN ? sw128_desc(as + kk * 2048, 8192, 1024) : sw128_desc(as + kk * 32, 16, 1024);
+          const uint64_t bd = GRAD ? sw128_desc(bs + kk * 2048, 8192, 1024) : sw128_desc(bs + kk * 32, 16, 1024);
+          if (KIND) mma_i8_ss_pair(d, ad, bd, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+          else mma_ss_pair(d, ad, bd, idesc, (k > 0 || kk > 0) ? 1u : 0u);
         }
-        if (lane == 0) {
-          const uint32_t as = smem_u32(As), bs = as + kABytes;
-          const int32_t steps = min(4, (left + kElems / 4 - 1) / (kElems / 4));
-          for (int32_t kk = 0; kk < steps; ++kk) {
-            const uint64_t ad = A_MN ? sw128_desc(as + kk * 2048, 8192, 1024) : sw128_desc(as + kk * 32, 16, 1024);
-            const uint64_t bd = GRAD ? sw128_desc(bs + kk * 2048, 8192, 1024) : sw128_desc(bs + kk * 32, 16, 1024);
-            if (KIND) mma_i8_ss(d, ad, bd, idesc, (k > 0 || kk > 0) ? 1u : 0u);
-            else mma_ss(d, ad, bd, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_pair(empty + s, 3);   // the stage is free in both CTAs once these MMAs have read it
+      };
+      for (int32_t idx = first; idx < n_tiles; idx += step, ++j) {
+        const Tile t = tile_at<GRAD>(a, start, idx);
+        const int32_t len = GRAD ? t.hi - t.lo : a.K;
+        const int b = j & 1;
+        const uint32_t d = tmem + static_cast<uint32_t>(b * kTileN);
+        const uint32_t idesc = a.idesc | (static_cast<uint32_t>(t.width >> 3) << 17);
+        const bool tail = GRAD && (len & 15);
+        const int32_t whole = tail ? len / kElems * kElems : len;   // up to here lane 0 works alone
+        if (rank == 0 && lane == 0) {
+          if (j >= 2) ok = lane_wait_cluster(acc_empty + b, static_cast<uint32_t>(((j >> 1) - 1) & 1), a.status);
+          tc_fence_after();
+          for (int32_t k = 0; k < whole && ok; k += kElems) {
+            if (!(ok = mbar_wait(full + s, phase, a.status))) break;
+            issue(d, idesc, k, len - k);
+            if (++s == stages) {
+              s = 0;
+              phase ^= 1;
+            }
           }
-          mma_commit(empty + s);   // the stage is free once these MMAs have read it
+          if (ok && !tail) mma_commit_pair(acc_full + b, 3);
         }
+        if (!GRAD) {   // (warp-uniform; the other lanes have nothing to do)
+          if (!ok) break;
+          continue;
+        }
+        if (rank != 0) {
+          const int32_t at = s + (whole + kElems - 1) / kElems;   // the stage after them (the ring may have gone round)
+          phase ^= (at / stages) & 1;
+          s = at % stages;
+        }
+        s = __shfl_sync(0xffffffffu, s, 0);
+        phase = __shfl_sync(0xffffffffu, phase, 0);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (!tail) continue;
+        // the rows behind the group (other groups' or none) up to the next
+        // multiple of 16 must be zero in both operands: each is 128 bytes in
+        // every 64-column box
+        const int32_t left = len - whole, pad = 16 - (left & 15), boxes = 2 + (t.width / 2 + 63) / 64;
+        uint8_t *As = sm + s * stage_bytes;
+        if (rank == 0) ok = mbar_wait(full + s, phase, a.status);
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(tail_full + s, (tail_phase >> s) & 1, a.status));
+        if (!ok) break;
+        for (int32_t i = lane; i < boxes * pad * 8; i += 32)
+          *reinterpret_cast<uint4 *>(As + (i / (pad * 8)) * 8192 + (left + (i / 8) % pad) * 128 + (i & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_cluster(ready0 + 8 * s);
+          if (rank == 0) {
+            ok = lane_wait_cluster(tail_ready + s, (tail_phase >> s) & 1, a.status);
+            if (ok) {
+              issue(d, idesc, whole, left);
+              mma_commit_pair(acc_full + b, 3);
+            }
+          }
+        }
+        tail_phase ^= 1u << s;
         if (++s == stages) {
           s = 0;
           phase ^= 1;
         }
+        if (!__all_sync(0xffffffffu, ok)) break;
       }
-      if (ok && lane == 0) mma_commit(acc_full + b);
     }
-    if (lane == 0) {
-      mma_commit(done);
-      mbar_wait(done, 0, a.status);   // nothing of this CTA's is in flight when TMEM is released
+    if (rank == 0 && lane == 0) {   // nothing is in flight when the pair leaves and releases its tensor memory
+      mma_commit_pair(done, 1);
+      mbar_wait(done, 0, a.status);
     }
   } else {
     const int q = warp & 3;             // TMEM lanes 32 q .. 32 q + 31
@@ -423,14 +552,15 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     float *st = out_stage + (warp - 2) * (kStageOut / 4);
     const bool w16 = a.odtype != HIMUON_FP32;
     const int64_t osize = w16 ? 2 : 4, csize = a.cdtype == HIMUON_FP32 ? 4 : 2;
+    const uint32_t free0 = mapa_shared(smem_u32(acc_empty), 0);
     int32_t j = 0;
-    for (int32_t idx = blockIdx.x; idx < n_tiles; idx += gridDim.x, ++j) {
+    for (int32_t idx = first; idx < n_tiles; idx += step, ++j) {
       const Tile t = tile_at<GRAD>(a, start, idx);
       const int b = j & 1;
       if (!warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + static_cast<uint32_t>(b * kTileN) + (static_cast<uint32_t>(q * 32) << 16);
-      const int32_t m = t.m0 + 32 * q;       // this warp's 32 rows of D
+      const int32_t m = t.m0 + 128 * rank + 32 * q;   // this warp's 32 rows of D
       const int32_t m_in = min(32, a.M - m);
       const bool empty_sum = GRAD && t.hi == t.lo;
       char *out = (NPTR > 1 ? a.out[GRAD ? t.e : 0] : a.out[0] + (GRAD ? t.e * a.out_stride : 0));
@@ -438,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       float chan = 1.f;
       if (KIND && lane < m_in) chan = a.w_scale[t.e * a.ld_scale + m + lane];
 #pragma unroll 1
-      for (int32_t i = half; i < (t.valid + 31) / 32; i += 2) {
+      for (int32_t i = half; i < (t.valid + 31) / 32 && m_in > 0; i += 2) {
         float v[32];
         if (empty_sum) {
 #pragma unroll
@@ -460,7 +590,6 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
                 KIND ? static_cast<float>(__float_as_int(v[k])) * chan : v[k];
         }
         __syncwarp();
-        if (m_in <= 0) continue;
         const int32_t r_in = GRAD ? m_in : min(32, t.valid - 32 * i), c_in = GRAD ? min(32, t.valid - 32 * i) : m_in;
         const int64_t r0 = GRAD ? m : t.n0 + 32 * i, c0 = GRAD ? t.n0 + 32 * i : m;
         char *o = out + (r0 * a.ldo + c0) * osize;
@@ -471,16 +600,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty + b);
+      if (lane == 0) mbar_arrive_cluster(free0 + 8 * b);
     }
   }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync_all();   // the pair leaves together: neither's memory goes while the other may signal or read it
   tc_fence_after();
-  if (warp == 1) {
-    __syncwarp();
-    tmem_dealloc(tmem, 512);
-  }
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
 struct QuantArgs {
@@ -492,36 +619,247 @@ struct QuantArgs {
   int32_t dim;
 };
 
-// code = round(127 x / top), ties to even: 127 x is exact in fp32 for 16-bit
-// x, and the division rounds correctly, so a tie in exact arithmetic is a tie
-// here.
-__device__ __forceinline__ int8_t code_of(float x, float top) {
-  return static_cast<int8_t>(__float2int_rn(__fdiv_rn(127.f * x, top)));
+// code = round(127 x / top), ties to even.  x and top are first multiplied by a
+// power of two (exact) that keeps 127 x and 1 / top in range; 127 x is then
+// exact for 16-bit x.  127 x times inv = 1 / top is off from the quotient by
+// less than 127 * 3 * 2^-24 < 3e-5, so it decides every code whose distance to
+// the next tie is more than that; nearer ones (about 1 in 5000) take the
+// correctly rounded division, which meets ties of 16-bit x exactly.  Adding
+// 1.5 * 2^23 rounds to an integer (ties to even) and leaves it in the low bits.
+// (The plain division for every element bounded the kernel by its
+// instructions: 8192 x 11008 bf16 in 464 us.)
+struct Coder {
+  float k, top, inv;
+  __device__ explicit Coder(float t) {
+    const float mul = t > 0x1p100f ? 0x1p-100f : t < 0x1p-100f ? 0x1p100f : 1.f;
+    top = t * mul;
+    k = 127.f * mul;
+    inv = __fdiv_rn(1.f, top);
+  }
+  // the code in the low byte; `far`: the largest distance to the code so far
+  __device__ __forceinline__ uint32_t near_code(float x, float &far) const {
+    const float r = x * k, t = fmaf(r, inv, 12582912.f);
+    far = fmaxf(far, fabsf(fmaf(r, inv, -(t - 12582912.f))));
+    return __float_as_uint(t);
+  }
+  __device__ __forceinline__ uint32_t exact_code(float x) const {
+    return __float_as_uint(__fdiv_rn(x * k, top) + 12582912.f);
+  }
+  __device__ __forceinline__ uint32_t operator()(float x) const {
+    float far = 0.f;
+    const uint32_t c = near_code(x, far);
+    return far <= 0.4999f ? c : exact_code(x);
+  }
+};
+__device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// One warp per row (dim 0) or column (dim 1).
-__global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ QuantArgs a) {
+// What the scale and the codes of a line with this maximum are: a line that
+// holds an infinity or a NaN has `top` infinite here (the maximum of the bits of
+// |x|: a NaN's are above infinity's).
+__device__ __forceinline__ bool line_ok(uint32_t top_bits) { return top_bits > 0 && top_bits < 0x7f800000u; }
+__device__ __forceinline__ float line_scale(uint32_t top_bits) {
+  return top_bits < 0x7f800000u ? __fdiv_rn(__uint_as_float(top_bits), 127.f) : __uint_as_float(0x7fffffffu);
+}
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// 8 consecutive elements (16-byte aligned for 16-bit types, 32 for fp32)
+__device__ __forceinline__ void ld8_any(const void *p, int32_t dtype, int64_t i, float (&v)[8]) {
+  ld4_any(static_cast<const char *>(p), dtype, i, *reinterpret_cast<float(*)[4]>(&v[0]));
+  ld4_any(static_cast<const char *>(p), dtype, i + 4, *reinterpret_cast<float(*)[4]>(&v[4]));
+}
+
+// One scale per row: TPR threads per row.  The row stays in registers between
+// the two passes (kHold runs of 8 elements per thread, all loads in flight
+// together; longer rows are read again, from L2).  HBM-bound: 3 bytes per
+// 16-bit element.
+template <int F32>
+struct Run8;   // 8 consecutive elements as loaded
+template <>
+struct Run8<0> {
+  uint4 u;
+  __device__ __forceinline__ void load(const char *p, int64_t i) { u = *reinterpret_cast<const uint4 *>(p + 16 * i); }
+  // |x| of 16-bit floats orders as an integer: two maxima at a time
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(u.x & m, u.y & m), __vmaxu2(u.z & m, u.w & m));
+  }
+  __device__ __forceinline__ float get(int j, int32_t dtype) const {
+    const uint32_t w = j < 2 ? u.x : j < 4 ? u.y : j < 6 ? u.z : u.w;
+    if (dtype == HIMUON_BF16) return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
+    const __half2 h = *reinterpret_cast<const __half2 *>(&w);
+    return j & 1 ? __high2float(h) : __low2float(h);
+  }
+};
+template <>
+struct Run8<1> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const char *p, int64_t i) {
+    a = *reinterpret_cast<const float4 *>(p + 32 * i);
+    b = *reinterpret_cast<const float4 *>(p + 32 * i + 16);
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    return max(max(max(abs_bits(a.x), abs_bits(a.y)), max(abs_bits(a.z), abs_bits(a.w))),
+               max(max(abs_bits(b.x), abs_bits(b.y)), max(abs_bits(b.z), abs_bits(b.w))));
+  }
+  __device__ __forceinline__ float get(int j, int32_t) const {
+    const float4 &f = j < 4 ? a : b;
+    return (j & 3) == 0 ? f.x : (j & 3) == 1 ? f.y : (j & 3) == 2 ? f.z : f.w;
+  }
+};
+template <int F32>
+constexpr int kHold = F32 ? 4 : 8;
+
+template <int F32, int TPR>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constant__ QuantArgs a) {
+  __shared__ uint32_t part[8];
   const int32_t z = blockIdx.y;
-  const int64_t lines = a.dim ? a.cols[z] : a.rows[z], len = a.dim ? a.rows[z] : a.cols[z];
-  const int64_t line = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (line >= lines) return;
-  const int64_t step = a.dim ? a.ld[z] : 1, base = a.dim ? line : line * a.ld[z];
-  float top = 0.f;
-  bool bad = false;
-  for (int64_t i = lane; i < len; i += 32) {
-    const float x = fabsf(ld_any(a.in[z], a.dtype[z], base + i * step));
-    bad |= !(x <= 3.402823466e38f);
-    top = fmaxf(top, x);
+  const int64_t row = blockIdx.x * static_cast<int64_t>(256 / TPR) + threadIdx.x / TPR;
+  const int t = threadIdx.x % TPR;
+  const int32_t dt = a.dtype[z];
+  const int64_t cols = a.cols[z], runs = cols / 8;
+  const bool live = row < a.rows[z] && (dt == HIMUON_FP32) == (F32 == 1);
+  const char *in = static_cast<const char *>(a.in[z]) + (live ? row * a.ld[z] : 0) * (F32 ? 4 : 2);
+  Run8<F32> v[kHold<F32>];
+  uint32_t top = 0;   // F32: bits of the maximum; else two 16-bit maxima
+  if (live) {
+#pragma unroll
+    for (int h = 0; h < kHold<F32>; ++h)
+      if (t + h * TPR < runs) v[h].load(in, t + h * TPR);
+#pragma unroll
+    for (int h = 0; h < kHold<F32>; ++h)
+      if (t + h * TPR < runs) top = F32 ? max(top, v[h].top()) : __vmaxu2(top, v[h].top());
+    for (int64_t i = t + static_cast<int64_t>(kHold<F32>) * TPR; i < runs; i += TPR) {
+      Run8<F32> w;
+      w.load(in, i);
+      top = F32 ? max(top, w.top()) : __vmaxu2(top, w.top());
+    }
+  }
+  if (!F32) {   // the 16-bit maximum as an fp32's bits
+    const uint32_t m = max(top >> 16, top & 0xffffu);
+    const uint16_t h = static_cast<uint16_t>(m);
+    top = dt == HIMUON_FP16 ? abs_bits(__half2float(*reinterpret_cast<const __half *>(&h))) : m << 16;
+  }
+  if (live)
+    for (int64_t i = 8 * runs + t; i < cols; i += TPR) top = max(top, abs_bits(ld_any(in, dt, i)));
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (TPR > 32) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    __syncthreads();
+    constexpr int kWarps = TPR / 32;
+    const int w0 = threadIdx.x / TPR * kWarps;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = max(top, part[w0 + w]);
+  }
+  if (!live) return;
+  if (t == 0) a.scale[z][row] = line_scale(top);
+  int8_t *out = a.codes[z] + row * a.ldq[z];
+  const bool ok = line_ok(top);
+  const Coder code(ok ? __uint_as_float(top) : 1.f);
+  auto put8 = [&](int64_t i, const Run8<F32> &x) {
+    uint32_t u[8];
+    float far = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = code.near_code(x.get(j, dt), far);
+    if (!(far <= 0.4999f)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = code.exact_code(x.get(j, dt));
+    }
+    *reinterpret_cast<uint2 *>(out + 8 * i) =
+        ok ? make_uint2(bytes4(u[0], u[1], u[2], u[3]), bytes4(u[4], u[5], u[6], u[7])) : make_uint2(0, 0);
+  };
+#pragma unroll
+  for (int h = 0; h < kHold<F32>; ++h)
+    if (t + h * TPR < runs) put8(t + h * TPR, v[h]);
+  for (int64_t i = t + static_cast<int64_t>(kHold<F32>) * TPR; i < runs; i += TPR) {
+    Run8<F32> w;
+    w.load(in, i);
+    put8(i, w);
+  }
+  for (int64_t i = 8 * runs + t; i < cols; i += TPR) out[i] = ok ? static_cast<int8_t>(code(ld_any(in, dt, i))) : 0;
+}
+
+// Rows of at most `widest` columns: the fewest threads per row that hold it.
+template <int F32>
+void quantize_rows(const QuantArgs &a, int64_t most, int64_t widest, unsigned zs, cudaStream_t st) {
+  const int64_t per = 8 * kHold<F32>;
+  auto go = [&](auto kern, int tpr) {
+    count_launch();
+    kern<<<dim3(static_cast<unsigned>((most + 256 / tpr - 1) / (256 / tpr)), zs), 256, 0, st>>>(a);
+  };
+  if (widest <= 32 * per) go(quantize_rows_kernel<F32, 32>, 32);
+  else if (widest <= 64 * per) go(quantize_rows_kernel<F32, 64>, 64);
+  else if (widest <= 128 * per) go(quantize_rows_kernel<F32, 128>, 128);
+  else go(quantize_rows_kernel<F32, 256>, 256);
+}
+
+// One scale per column, codes transposed: a CTA takes 64 columns (128 bytes of
+// a 16-bit row); the first pass finds the columns' maxima, the second (from
+// L2) codes blocks of 128 rows and turns them through shared memory.
+__global__ void __launch_bounds__(256) quantize_cols_kernel(const __grid_constant__ QuantArgs a) {
+  __shared__ uint32_t tops[8][64];
+  __shared__ __align__(16) int8_t turn[64][128 + 16];
+  const int32_t z = blockIdx.y;
+  const int64_t c0 = blockIdx.x * 64ll;
+  const int64_t rows = a.rows[z], cols = a.cols[z], ld = a.ld[z];
+  if (c0 >= cols) return;
+  const int32_t dt = a.dtype[z];
+  const int c8 = threadIdx.x & 7, r0 = threadIdx.x >> 3;   // 8 columns, 32 rows at a time
+  const int64_t c = c0 + 8 * c8;
+  const bool whole = c + 8 <= cols;
+  auto load = [&](int64_t r, float(&x)[8]) {
+    if (whole) ld8_any(a.in[z], dt, r * ld + c, x);
+    else
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = c + j < cols ? ld_any(a.in[z], dt, r * ld + c + j) : 0.f;
+  };
+  uint32_t top[8] = {};
+#pragma unroll 4
+  for (int64_t r = r0; r < rows; r += 32) {
+    float x[8];
+    load(r, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top[j] = max(top[j], abs_bits(x[j]));
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  bad = __any_sync(0xffffffffu, bad);
-  for (int64_t i = lane; i < len; i += 32) {
-    const float x = ld_any(a.in[z], a.dtype[z], base + i * step);
-    a.codes[z][line * a.ldq[z] + i] = (bad || top == 0.f) ? 0 : code_of(x, top);
+  for (int j = 0; j < 8; ++j) {
+    top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 8));
+    top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
+    if ((threadIdx.x & 31) < 8) tops[threadIdx.x >> 5][8 * c8 + j] = top[j];
   }
-  if (lane == 0) a.scale[z][line] = bad ? __int_as_float(0x7fffffff) : top / 127.f;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+#pragma unroll
+    for (int w = 0; w < 8; ++w) top[j] = max(top[j], tops[w][8 * c8 + j]);
+    if (r0 == 0 && c + j < cols) a.scale[z][c + j] = line_scale(top[j]);
+  }
+  for (int64_t b = 0; b < rows; b += 128) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t r = b + r0 + 32 * k;
+      if (r >= rows) continue;
+      float x[8];
+      load(r, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool ok = line_ok(top[j]);
+        turn[8 * c8 + j][r0 + 32 * k] = ok ? static_cast<int8_t>(Coder(__uint_as_float(top[j]))(x[j])) : 0;
+      }
+    }
+    __syncthreads();
+    const int64_t in = min(rows - b, (int64_t)128);
+    for (int i = threadIdx.x; i < 64 * 8; i += 256) {   // 16 rows of a column at a time
+      const int col = i >> 3, r = (i & 7) * 16;
+      if (c0 + col >= cols || r >= in) continue;
+      int8_t *out = a.codes[z] + (c0 + col) * a.ldq[z] + b + r;
+      if (r + 16 <= in) *reinterpret_cast<uint4 *>(out) = *reinterpret_cast<const uint4 *>(&turn[col][r]);
+      else
+        for (int k = 0; r + k < in; ++k) out[k] = turn[col][r + k];
+    }
+  }
 }
 
 // ---------------------------------------------------------------- argument checks
@@ -623,7 +961,7 @@ int launch_mma(const MmaArgs<NMAP, NPTR> &a, int64_t most_tiles, cudaStream_t st
   auto kern = expert_kernel<KIND, A_MN, GRAD, NMAP, NPTR>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return HIMUON_ERR_CUDA;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(most_tiles, sm_count()));
+  const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(most_tiles, sm_count() / 2));
   count_launch();
   kern<<<grid, kThreads, kSmem, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? HIMUON_OK : HIMUON_ERR_CUDA;
@@ -647,8 +985,8 @@ void common_args(MmaArgs<NMAP, NPTR> &a, const int32_t *offsets, int32_t e0, int
 // D format and operand formats of the instruction descriptor (its N field is
 // set per tile): f32 from bf16/fp16, or s32 from s8.
 uint32_t idesc_of(int32_t dtype, uint32_t a_mn, uint32_t b_mn) {
-  if (dtype == HIMUON_I8) return (2u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
-  return idesc_f16(128, 0, dtype == HIMUON_FP16 ? 0u : 1u, a_mn, b_mn, 0);
+  if (dtype == HIMUON_I8) return (2u << 4) | (1u << 7) | (1u << 10) | ((kTileM >> 4) << 24);
+  return idesc_f16(kTileM, 0, dtype == HIMUON_FP16 ? 0u : 1u, a_mn, b_mn, 0);
 }
 
 template <int NMAP>
@@ -660,7 +998,8 @@ int product_launch(const himuon_mat *X, const float *x_scale, const himuon_mat *
   const uint32_t w_rows = w_trans ? 128 : 64;
   for (int32_t i = 0; i < (NMAP > 1 ? n : 1); ++i)
     if (!make_map(&a.w[i], W[e0 + i], NMAP > 1 ? 1 : n, stride, w_rows)) return HIMUON_ERR_CUDA;
-  if (!make_map(&a.x, *X, 0, 0, 32)) return HIMUON_ERR_CUDA;
+  for (int i = 0; i < 4; ++i)
+    if (!make_map(&a.x[i], *X, 0, 0, 128 >> i)) return HIMUON_ERR_CUDA;
   a.K = static_cast<int32_t>(X->cols);
   a.M = static_cast<int32_t>(Y->cols);
   a.N = 0;
@@ -674,7 +1013,7 @@ int product_launch(const himuon_mat *X, const float *x_scale, const himuon_mat *
   a.c[0] = nullptr;
   a.ldo = Y->ld;
   a.odtype = Y->dtype;
-  const int64_t mt_m = (Y->cols + 127) / 128;
+  const int64_t mt_m = (Y->cols + kTileM - 1) / kTileM;
   const int64_t most = mt_m * (X->rows / kTileN + std::min<int64_t>(n, X->rows));
   if (X->dtype == HIMUON_I8) return launch_mma<1, 0, 0>(a, most, stream);
   return w_trans ? launch_mma<0, 0, 0>(a, most, stream) : launch_mma<0, 1, 0>(a, most, stream);
@@ -708,8 +1047,8 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
     any.rows = 1;
     any.cols = 8;
     if (!make_map(&a.w[0], any, 0, 0, 64)) return HIMUON_ERR_CUDA;
-    a.x = a.w[0];
-  } else if (!make_map(&a.w[0], *A, 0, 0, 64) || !make_map(&a.x, *B, 0, 0, 64)) {
+    a.x[0] = a.w[0];
+  } else if (!make_map(&a.w[0], *A, 0, 0, 64) || !make_map(&a.x[0], *B, 0, 0, 64)) {
     return HIMUON_ERR_CUDA;
   }
   a.K = 0;
@@ -731,7 +1070,7 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
     a.ldc = C->ld;
     a.cdtype = C->dtype;
   }
-  const int64_t most = n * ((A->cols + 127) / 128) * ((B->cols + kTileN - 1) / kTileN);
+  const int64_t most = n * ((A->cols + kTileM - 1) / kTileM) * ((B->cols + kTileN - 1) / kTileN);
   return launch_mma<0, 1, 1>(a, most, stream);
 }
 
@@ -830,7 +1169,8 @@ int himuon_quantize(const himuon_mat *in, int32_t n, int32_t dim, const himuon_m
     const int32_t cnt = std::min(n - e0, kMaxList);
     QuantArgs a;
     a.dim = dim;
-    int64_t most = 0;
+    int64_t most = 0, widest = 0;
+    bool any16 = false, any32 = false;
     for (int32_t e = 0; e < cnt; ++e) {
       const himuon_mat &m = in[e0 + e];
       a.in[e] = m.data;
@@ -842,11 +1182,19 @@ int himuon_quantize(const himuon_mat *in, int32_t n, int32_t dim, const himuon_m
       a.ldq[e] = codes[e0 + e].ld;
       a.dtype[e] = m.dtype;
       most = std::max(most, dim ? m.cols : m.rows);
+      widest = std::max(widest, m.cols);
+      (m.dtype == HIMUON_FP32 ? any32 : any16) = true;
     }
     if (most == 0) continue;
-    const dim3 grid(static_cast<unsigned>((most + 7) / 8), static_cast<unsigned>(cnt));
-    count_launch();
-    quantize_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const unsigned zs = static_cast<unsigned>(cnt);
+    if (dim) {
+      count_launch();
+      quantize_cols_kernel<<<dim3(static_cast<unsigned>((most + 63) / 64), zs), 256, 0, st>>>(a);
+    } else {   // one launch per storage width among the call's matrices
+      if (any16) quantize_rows<0>(a, most, widest, zs, st);
+      if (any32) quantize_rows<1>(a, most, widest, zs, st);
+    }
     if (cudaGetLastError() != cudaSuccess) return HIMUON_ERR_CUDA;
   }
   return HIMUON_OK;
