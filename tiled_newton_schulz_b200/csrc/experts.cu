@@ -116,20 +116,31 @@ __device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *m
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar_cluster)
       : "memory");
 }
-// A bounded wait by a whole warp: its lanes agree whether to go on.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, int *status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, phase, status));
+// One thread of the converged warp (the same one every time).  The loops that
+// issue copies and MMAs are run by whole warps, with only the instruction
+// itself in the elected thread's branch: their addresses and descriptors then
+// stay in uniform registers.  (Run by lane 0 alone, each stage's copies took
+// about 500 cycles to issue and its MMAs 450, which bounded every case.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
-// One thread's bounded wait for a phase that the pair's other CTA also arrives on.
-__device__ __forceinline__ bool lane_wait_cluster(uint64_t *bar, uint32_t phase, int *status) {
-  bool ok = mbar_try_wait_cluster(bar, phase);
-  if (!ok) {
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t i = 1; !(ok = mbar_try_wait_cluster(bar, phase)); ++i)
-      if ((i & 255u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) break;
-    if (!ok) set_status(status, HIMUON_ERR_TIMEOUT_DEV);
+// A bounded wait by a whole warp: its lanes agree on the outcome.  CLUSTER:
+// for phases that the pair's other CTA also arrives on.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, int *status) {
+  auto ready = [&] {
+    return __all_sync(0xffffffffu, CLUSTER ? mbar_try_wait_cluster(bar, phase) : mbar_try_wait(bar, phase));
+  };
+  if (ready()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (ready()) return true;
+    if ((i & 255u) == 0 && __any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs)) break;
   }
-  return ok;
+  set_status(status, HIMUON_ERR_TIMEOUT_DEV);
+  return false;
 }
 
 // Bound i of the groups, clamped into 0 .. rows.
@@ -385,166 +396,145 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int stages = min(static_cast<int>(kRing / stage_bytes), kMaxStages);
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t full0 = mapa_shared(smem_u32(full), 0);
-      int s = 0;
-      uint32_t phase = 1;   // parity of the stage's last release; the first round finds it free
-      bool ok = true;
-      int64_t issued = 0;
-      uint32_t was_tail = 0, tail_phase = 0;   // per stage: its last block's kind; tail_full's next parity
-      for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
-        const Tile t = tile_at<GRAD>(a, start, idx);
-        const int32_t len = GRAD ? t.hi - t.lo : a.K;
-        const CUtensorMap *mw = NMAP > 1 ? &a.w[t.e] : &a.w[0];
-        const int32_t z = NMAP > 1 ? 0 : t.e;
-        const int32_t half = t.width / 2;
-        const int32_t m0 = t.m0 + 128 * rank, n0 = t.n0 + half * rank;
-        const int32_t boxes = GRAD ? (half + 63) / 64 : half / 16;
-        const uint32_t bytes = kABytes + boxes * (GRAD ? 8192u : kBoxBytes);
-        for (int32_t k = 0; k < len; k += kElems) {
-          if (!(ok = mbar_wait(empty + s, phase, a.status))) break;
-          uint8_t *As = sm + s * stage_bytes, *Bs = As + kABytes;
-          if (GRAD) {
-            const int32_t y = t.lo + k;
-            const bool tail = len - k < kElems && ((len - k) & 15);
-            was_tail = (was_tail & ~(1u << s)) | (static_cast<uint32_t>(tail) << s);
-            if (tail) {   // lands on this CTA's own barrier: its warp 1 has zeros to write before the MMAs
+    const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+    int s = 0;
+    uint32_t phase = 1;   // parity of the stage's last release; the first round finds it free
+    bool ok = true;
+    int64_t issued = 0;
+    uint32_t was_tail = 0, tail_phase = 0;   // per stage: its last block's kind; tail_full's next parity
+    for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
+      const Tile t = tile_at<GRAD>(a, start, idx);
+      const int32_t len = GRAD ? t.hi - t.lo : a.K;
+      const CUtensorMap *mw = NMAP > 1 ? &a.w[t.e] : &a.w[0];
+      const int32_t z = NMAP > 1 ? 0 : t.e;
+      const int32_t half = t.width / 2;
+      const int32_t m0 = t.m0 + 128 * rank, n0 = t.n0 + half * rank;
+      const int32_t boxes = GRAD ? (half + 63) / 64 : half / 16;
+      const uint32_t bytes = kABytes + boxes * (GRAD ? 8192u : kBoxBytes);
+      for (int32_t k = 0; k < len; k += kElems) {
+        if (!(ok = warp_wait(empty + s, phase, a.status))) break;
+        uint8_t *As = sm + s * stage_bytes, *Bs = As + kABytes;
+        const uint32_t bar = full0 + 8 * s;
+        if (GRAD) {
+          const int32_t y = t.lo + k;
+          const bool tail = len - k < kElems && ((len - k) & 15);
+          was_tail = (was_tail & ~(1u << s)) | (static_cast<uint32_t>(tail) << s);
+          if (tail) {   // lands on this CTA's own barrier: its warp 1 has zeros to write before the MMAs
+            tail_phase ^= 1u << s;
+            if (elect_one()) {
               if (rank == 0) mbar_arrive(full + s);
               mbar_arrive_expect_tx(tail_full + s, bytes);
-              tail_phase ^= 1u << s;
               tma_load_2d(As, &a.w[0], m0, y, tail_full + s);
               tma_load_2d(As + 8192, &a.w[0], m0 + 64, y, tail_full + s);
               for (int32_t j = 0; j < boxes; ++j) tma_load_2d(Bs + 8192 * j, &a.x[0], n0 + 64 * j, y, tail_full + s);
-            } else {
-              if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * bytes);
-              const uint32_t bar = full0 + 8 * s;
-              tma_load_2d_pair(As, &a.w[0], m0, y, bar);
-              tma_load_2d_pair(As + 8192, &a.w[0], m0 + 64, y, bar);
-              for (int32_t j = 0; j < boxes; ++j) tma_load_2d_pair(Bs + 8192 * j, &a.x[0], n0 + 64 * j, y, bar);
             }
-          } else {
+          } else if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * bytes);
-            const uint32_t bar = full0 + 8 * s;
-            if (A_MN) {
-              tma_load_3d_pair(As, mw, m0, k, z, bar);
-              tma_load_3d_pair(As + 8192, mw, m0 + 64, k, z, bar);
-            } else {
-              tma_load_3d_pair(As, mw, k, m0, z, bar);
-            }
-            // this CTA's rows of the tile in at most four boxes, the largest first
-            int32_t at = 0;
-#pragma unroll
-            for (int32_t i = 0; i < 4; ++i)
-              if (boxes & (8 >> i)) {
-                tma_load_2d_pair(Bs + kBoxBytes * at, &a.x[i], k, n0 + 16 * at, bar);
-                at += 8 >> i;
-              }
+            tma_load_2d_pair(As, &a.w[0], m0, y, bar);
+            tma_load_2d_pair(As + 8192, &a.w[0], m0 + 64, y, bar);
+            tma_load_2d_pair(Bs, &a.x[0], n0, y, bar);
+            if (boxes > 1) tma_load_2d_pair(Bs + 8192, &a.x[0], n0 + 64, y, bar);
           }
-          ++issued;
+        } else if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * bytes);
+          if (A_MN) {
+            tma_load_3d_pair(As, mw, m0, k, z, bar);
+            tma_load_3d_pair(As + 8192, mw, m0 + 64, k, z, bar);
+          } else {
+            tma_load_3d_pair(As, mw, k, m0, z, bar);
+          }
+          // this CTA's rows of the tile in at most four boxes, the largest first
+          int32_t at = 0;
+#pragma unroll
+          for (int32_t i = 0; i < 4; ++i)
+            if (boxes & (8 >> i)) {
+              tma_load_2d_pair(Bs + kBoxBytes * at, &a.x[i], k, n0 + 16 * at, bar);
+              at += 8 >> i;
+            }
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == stages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    // the last loads have landed before the CTA ends, also when something gave
+    // up (the even CTA's barriers see both CTAs' loads; the CTAs leave together)
+    for (int64_t i = max((int64_t)0, issued - stages); i < issued; ++i) {
+      const int st = static_cast<int>(i % stages);
+      if ((was_tail >> st) & 1) warp_wait(tail_full + st, ((tail_phase >> st) & 1) ^ 1, a.status);
+      else if (rank == 0) warp_wait(full + st, static_cast<uint32_t>((i / stages) & 1), a.status);
+    }
+  } else if (warp == 1) {
+    if (rank == 0 || GRAD) {
+      const uint32_t ready0 = mapa_shared(smem_u32(tail_ready), 0);
+      // descriptors of stage 0, without the address
+      const uint64_t a_bits = A_MN ? sw128_desc(0, 8192, 1024) : sw128_desc(0, 16, 1024);
+      const uint64_t b_bits = GRAD ? sw128_desc(0, 8192, 1024) : sw128_desc(0, 16, 1024);
+      constexpr uint32_t kStepA = (A_MN ? 2048 : 32) >> 4, kStepB = (GRAD ? 2048 : 32) >> 4;
+      int s = 0;
+      uint32_t phase = 0, tail_phase = 0;
+      int32_t j = 0;
+      bool ok = true;
+      for (int32_t idx = first; idx < n_tiles && ok; idx += step, ++j) {
+        const Tile t = tile_at<GRAD>(a, start, idx);
+        const int32_t len = GRAD ? t.hi - t.lo : a.K;
+        const int b = j & 1;
+        if (rank == 0 && j >= 2) {
+          ok = warp_wait<true>(acc_empty + b, static_cast<uint32_t>(((j >> 1) - 1) & 1), a.status);
+          if (!ok) break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(b * kTileN);
+        const uint32_t idesc = a.idesc | (static_cast<uint32_t>(t.width >> 3) << 17);
+        for (int32_t k = 0; k < len; k += kElems) {
+          const uint32_t as = smem_u32(sm) + s * stage_bytes;
+          const int32_t left = len - k;
+          if (rank == 0 && !(ok = warp_wait(full + s, phase, a.status))) break;
+          if (GRAD && left < kElems && (left & 15)) {
+            // the rows behind the group (other groups' or none) up to the next
+            // multiple of 16 must be zero in both operands: each is 128 bytes
+            // in every 64-column box
+            if (!(ok = warp_wait(tail_full + s, (tail_phase >> s) & 1, a.status))) break;
+            const int32_t pad = 16 - (left & 15), boxes = 2 + (t.width / 2 + 63) / 64;
+            for (int32_t i = lane; i < boxes * pad * 8; i += 32)
+              *reinterpret_cast<uint4 *>(sm + s * stage_bytes + (i / (pad * 8)) * 8192 + (left + (i / 8) % pad) * 128 +
+                                         (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (elect_one()) mbar_arrive_cluster(ready0 + 8 * s);
+            if (rank == 0 && !(ok = warp_wait<true>(tail_ready + s, (tail_phase >> s) & 1, a.status))) break;
+            tail_phase ^= 1u << s;
+          }
+          if (rank == 0) {
+            tc_fence_after();
+            const uint64_t ad = a_bits | (as >> 4), bd = b_bits | ((as + kABytes) >> 4);
+            if (elect_one()) {
+#pragma unroll
+              for (int32_t kk = 0; kk < 4; ++kk) {
+                if (kk > 0 && kk * (kElems / 4) >= left) break;
+                if (KIND) mma_i8_ss_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+                else mma_ss_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+              }
+              mma_commit_pair(empty + s, 3);   // the stage is free in both CTAs once these MMAs have read it
+            }
+            __syncwarp();
+          }
           if (++s == stages) {
             s = 0;
             phase ^= 1;
           }
         }
-      }
-      // the last loads have landed before the CTA ends, also when something
-      // gave up (the even CTA's barriers see both CTAs' loads; the CTAs leave
-      // together)
-      for (int64_t i = max((int64_t)0, issued - stages); i < issued; ++i) {
-        const int st = static_cast<int>(i % stages);
-        if ((was_tail >> st) & 1) mbar_wait(tail_full + st, ((tail_phase >> st) & 1) ^ 1, a.status);
-        else if (rank == 0) mbar_wait(full + st, static_cast<uint32_t>((i / stages) & 1), a.status);
-      }
-    }
-  } else if (warp == 1) {
-    if (rank == 0 || GRAD) {
-      const uint32_t ready0 = mapa_shared(smem_u32(tail_ready), 0);
-      int s = 0;
-      uint32_t phase = 0, tail_phase = 0;
-      int32_t j = 0;
-      bool ok = true;
-      // the MMAs over one stage, K elements k .. of `len` (even CTA, lane 0)
-      auto issue = [&](uint32_t d, uint32_t idesc, int32_t k, int32_t left) {
-        tc_fence_after();
-        const uint32_t as = smem_u32(sm + s * stage_bytes), bs = as + kABytes;
-#pragma unroll
-        for (int32_t kk = 0; kk < 4; ++kk) {
-          if (kk * (kElems / 4) >= left) break;
-          const uint64_t ad = A_MN ? sw128_desc(as + kk * 2048, 8192, 1024) : sw128_desc(as + kk * 32, 16, 1024);
-          const uint64_t bd = GRAD ? sw128_desc(bs + kk * 2048, 8192, 1024) : sw128_desc(bs + kk * 32, 16, 1024);
-          if (KIND) mma_i8_ss_pair(d, ad, bd, idesc, (k > 0 || kk > 0) ? 1u : 0u);
-          else mma_ss_pair(d, ad, bd, idesc, (k > 0 || kk > 0) ? 1u : 0u);
-        }
-        mma_commit_pair(empty + s, 3);   // the stage is free in both CTAs once these MMAs have read it
-      };
-      for (int32_t idx = first; idx < n_tiles; idx += step, ++j) {
-        const Tile t = tile_at<GRAD>(a, start, idx);
-        const int32_t len = GRAD ? t.hi - t.lo : a.K;
-        const int b = j & 1;
-        const uint32_t d = tmem + static_cast<uint32_t>(b * kTileN);
-        const uint32_t idesc = a.idesc | (static_cast<uint32_t>(t.width >> 3) << 17);
-        const bool tail = GRAD && (len & 15);
-        const int32_t whole = tail ? len / kElems * kElems : len;   // up to here lane 0 works alone
-        if (rank == 0 && lane == 0) {
-          if (j >= 2) ok = lane_wait_cluster(acc_empty + b, static_cast<uint32_t>(((j >> 1) - 1) & 1), a.status);
-          tc_fence_after();
-          for (int32_t k = 0; k < whole && ok; k += kElems) {
-            if (!(ok = mbar_wait(full + s, phase, a.status))) break;
-            issue(d, idesc, k, len - k);
-            if (++s == stages) {
-              s = 0;
-              phase ^= 1;
-            }
-          }
-          if (ok && !tail) mma_commit_pair(acc_full + b, 3);
-        }
-        if (!GRAD) {   // (warp-uniform; the other lanes have nothing to do)
-          if (!ok) break;
-          continue;
-        }
-        if (rank != 0) {
-          const int32_t at = s + (whole + kElems - 1) / kElems;   // the stage after them (the ring may have gone round)
-          phase ^= (at / stages) & 1;
-          s = at % stages;
-        }
-        s = __shfl_sync(0xffffffffu, s, 0);
-        phase = __shfl_sync(0xffffffffu, phase, 0);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        if (!tail) continue;
-        // the rows behind the group (other groups' or none) up to the next
-        // multiple of 16 must be zero in both operands: each is 128 bytes in
-        // every 64-column box
-        const int32_t left = len - whole, pad = 16 - (left & 15), boxes = 2 + (t.width / 2 + 63) / 64;
-        uint8_t *As = sm + s * stage_bytes;
-        if (rank == 0) ok = mbar_wait(full + s, phase, a.status);
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(tail_full + s, (tail_phase >> s) & 1, a.status));
-        if (!ok) break;
-        for (int32_t i = lane; i < boxes * pad * 8; i += 32)
-          *reinterpret_cast<uint4 *>(As + (i / (pad * 8)) * 8192 + (left + (i / 8) % pad) * 128 + (i & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
+        if (ok && rank == 0 && elect_one()) mma_commit_pair(acc_full + b, 3);
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_cluster(ready0 + 8 * s);
-          if (rank == 0) {
-            ok = lane_wait_cluster(tail_ready + s, (tail_phase >> s) & 1, a.status);
-            if (ok) {
-              issue(d, idesc, whole, left);
-              mma_commit_pair(acc_full + b, 3);
-            }
-          }
-        }
-        tail_phase ^= 1u << s;
-        if (++s == stages) {
-          s = 0;
-          phase ^= 1;
-        }
-        if (!__all_sync(0xffffffffu, ok)) break;
       }
     }
-    if (rank == 0 && lane == 0) {   // nothing is in flight when the pair leaves and releases its tensor memory
-      mma_commit_pair(done, 1);
-      mbar_wait(done, 0, a.status);
+    if (rank == 0) {   // nothing is in flight when the pair leaves and releases its tensor memory
+      if (elect_one()) mma_commit_pair(done, 1);
+      __syncwarp();
+      warp_wait(done, 0, a.status);
     }
   } else {
     const int q = warp & 3;             // TMEM lanes 32 q .. 32 q + 31
