@@ -168,8 +168,10 @@ struct Tile {
   int32_t lo, hi;   // the group's rows
 };
 
+// Tile `idx` of the launch, found by a whole warp.  `from`: a group not after
+// the tile's (the last one found: a role's tiles come in order).
 template <int GRAD, typename Args>
-__device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int32_t idx) {
+__device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int32_t idx, int32_t from) {
   Tile t;
   const int32_t mt_m = m_tiles(a.M);
   if (GRAD) {
@@ -183,15 +185,15 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int
     t.lo = bound_at(a.offsets, t.e, a.rows);
     t.hi = max(t.lo, bound_at(a.offsets, t.e + 1, a.rows));
   } else {
-    // the group whose row tiles hold row tile idx / mt_m: start[e] <= it < start[e + 1]
-    const int32_t u = idx / mt_m;
-    int32_t lo = 0, hi = a.n - 1;
-    while (lo < hi) {
-      const int32_t mid = (lo + hi + 1) / 2;
-      if (start[mid] <= u) lo = mid;
-      else hi = mid - 1;
+    // the group whose row tiles hold row tile idx / mt_m: the last with start[e] <= it
+    const int32_t u = idx / mt_m, lane = threadIdx.x & 31;
+    for (;; from += 32) {
+      const uint32_t before = __ballot_sync(0xffffffffu, from + 1 + lane < a.n && start[from + 1 + lane] <= u);
+      if (before != 0xffffffffu) {
+        t.e = from + __popc(before);
+        break;
+      }
     }
-    t.e = lo;
     t.lo = bound_at(a.offsets, t.e, a.rows);
     t.hi = max(t.lo, bound_at(a.offsets, t.e + 1, a.rows));
     const int32_t cnt = t.hi - t.lo, mt = row_tiles(cnt);
@@ -402,8 +404,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     int64_t issued = 0;
     uint32_t was_tail = 0, tail_phase = 0;   // per stage: its last block's kind; tail_full's next parity
+    Tile t, next;
+    if (first < n_tiles) next = tile_at<GRAD>(a, start, first, 0);
     for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
-      const Tile t = tile_at<GRAD>(a, start, idx);
+      t = next;
+      const bool more = idx + step < n_tiles;   // the next tile is looked up behind this one's first block
+      if (more && (GRAD && t.hi == t.lo)) next = tile_at<GRAD>(a, start, idx + step, t.e);
       const int32_t len = GRAD ? t.hi - t.lo : a.K;
       const CUtensorMap *mw = NMAP > 1 ? &a.w[t.e] : &a.w[0];
       const int32_t z = NMAP > 1 ? 0 : t.e;
@@ -453,6 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
+        if (k == 0 && more) next = tile_at<GRAD>(a, start, idx + step, t.e);
         ++issued;
         if (++s == stages) {
           s = 0;
@@ -478,8 +485,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, tail_phase = 0;
       int32_t j = 0;
       bool ok = true;
+      Tile t, next;
+      if (first < n_tiles) next = tile_at<GRAD>(a, start, first, 0);
       for (int32_t idx = first; idx < n_tiles && ok; idx += step, ++j) {
-        const Tile t = tile_at<GRAD>(a, start, idx);
+        t = next;
+        const bool more = idx + step < n_tiles;
+        if (more && (GRAD && t.hi == t.lo)) next = tile_at<GRAD>(a, start, idx + step, t.e);
         const int32_t len = GRAD ? t.hi - t.lo : a.K;
         const int b = j & 1;
         if (rank == 0 && j >= 2) {
@@ -522,6 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
           }
+          if (k == 0 && more) next = tile_at<GRAD>(a, start, idx + step, t.e);
           if (++s == stages) {
             s = 0;
             phase ^= 1;
@@ -543,9 +555,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const bool w16 = a.odtype != HIMUON_FP32;
     const int64_t osize = w16 ? 2 : 4, csize = a.cdtype == HIMUON_FP32 ? 4 : 2;
     const uint32_t free0 = mapa_shared(smem_u32(acc_empty), 0);
-    int32_t j = 0;
+    int32_t j = 0, from = 0;
     for (int32_t idx = first; idx < n_tiles; idx += step, ++j) {
-      const Tile t = tile_at<GRAD>(a, start, idx);
+      const Tile t = tile_at<GRAD>(a, start, idx, from);
+      from = t.e;
       const int b = j & 1;
       if (!warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status)) break;
       tc_fence_after();
