@@ -46,17 +46,19 @@ constexpr int kMaxStack = 256;
 //             K = the group's rows (both operands MN-major).
 constexpr uint32_t kABytes = 16384;     // 128 rows (or 2 x 64 MN columns) x 128 bytes of K
 constexpr uint32_t kBoxBytes = 2048;    // 16 rows of X x 128 bytes
-constexpr uint32_t kRing = 196608;      // operand ring
+constexpr uint32_t kData = 229376;      // operand ring and the epilogue's buffers
 constexpr int kMaxStages = 10;
-constexpr uint32_t kStageOut = 4096;    // per epilogue warp: 32 x 32 fp32, swizzled
+constexpr uint32_t kStageOut = 4096;    // an epilogue warp's buffer: 32 x 32 fp32, swizzled
 constexpr int kEpiWarps = 8;
 constexpr int kTileM = 256, kTileN = 256;   // a CTA pair's tile of D
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr uint32_t kBarBytes = 384;
-constexpr uint32_t kSmem = kRing + kEpiWarps * kStageOut + kBarBytes + 4 * (kMaxStack + 4) + 1024;
+constexpr uint32_t kBarBytes = 576;
+constexpr uint32_t kSmem = kData + kBarBytes + 4 * (kMaxStack + 4) + 1024;
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
-template <int NMAP, int NPTR>
+// NMAP, NOUT: tensor maps of W, and of G and C (the product writes Y without
+// one): 1, over matrices at equal distances, or one for each of a list.
+template <int NMAP, int NOUT>
 struct MmaArgs {
   CUtensorMap w[NMAP];     // product: W; gradient: operand A
   CUtensorMap x[4];        // product: X in boxes of 128, 64, 32 and 16 rows; gradient: [0] operand B
@@ -69,12 +71,11 @@ struct MmaArgs {
   int *status;
   const float *x_scale, *w_scale;
   int64_t ld_scale;
-  // outputs: product Y (one matrix), gradient G and C
-  char *out[NPTR];
-  const char *c[NPTR];
-  int64_t out_stride, c_stride;   // NPTR == 1: bytes between consecutive matrices
-  int64_t ldo, ldc;
+  CUtensorMap g[NOUT], c[NOUT];   // gradient: G and C in boxes of 32 rows x 32 columns
+  char *out[NOUT];                // product: Y; gradient: G
+  int64_t ldo, out_stride;        // (NOUT = 1: bytes between consecutive matrices of G)
   int32_t odtype, cdtype, has_c;
+  int32_t buffers;                // of kStageOut per epilogue warp
   float alpha, beta;
 };
 
@@ -237,32 +238,24 @@ __device__ __forceinline__ uint32_t pack2(int32_t dtype, float x, float y) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// A staged 32 x 32 block (row r's 16-byte chunk c at chunk c ^ (r & 7)) to the
-// output: `rows` x `cols` of it are inside.  16-bit outputs: 4 lanes per row,
-// 8 columns each; fp32: 8 lanes per row, 4 columns each, so every row of the
-// block is written as one 64- or 128-byte run.
+// The product's output: a staged 32 x 32 block (row r's 16-byte chunk c at
+// chunk c ^ (r & 7)), `rows` x `cols` of it inside.  16-bit outputs: 4 lanes per
+// row, 8 columns each; fp32: 8 lanes per row, 4 columns each, so every row of
+// the block is written as one 64- or 128-byte run.  (A group's last rows end
+// inside a tile, where a tensor map could not stop.)
 template <int W16>
 __device__ __forceinline__ void write_block(const float *st, int lane, char *out, int32_t odtype, int64_t ldo,
-                                            int32_t rows, int32_t cols, float alpha, const char *c, int32_t cdtype,
-                                            int64_t ldc, float beta, const float *row_scale) {
+                                            int32_t rows, int32_t cols, const float *row_scale) {
   constexpr int kLanes = W16 ? 4 : 8, kCols = W16 ? 8 : 4, kPass = W16 ? 4 : 8;
   const int32_t col = (lane % kLanes) * kCols;
   if (col >= cols) return;
   const bool whole = col + kCols <= cols;
-  float cv[kPass][kCols];
-  if (c) {
+  float scale[kPass];
+  if (row_scale) {
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
       const int32_t r = lane / kLanes + p * (32 / kLanes);
-      if (r >= rows) continue;
-      const int64_t o = r * ldc + col;
-      if (whole) {
-#pragma unroll
-        for (int h = 0; h < kCols; h += 4) ld4_any(c, cdtype, o + h, *reinterpret_cast<float(*)[4]>(&cv[p][h]));
-      } else {
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) cv[p][j] = col + j < cols ? ld_any(c, cdtype, o + j) : 0.f;
-      }
+      scale[p] = r < rows ? row_scale[r] : 0.f;
     }
   }
 #pragma unroll
@@ -276,14 +269,8 @@ __device__ __forceinline__ void write_block(const float *st, int lane, char *out
       v[h] = f.x; v[h + 1] = f.y; v[h + 2] = f.z; v[h + 3] = f.w;
     }
     if (row_scale) {
-      const float s = row_scale[r];
 #pragma unroll
-      for (int j = 0; j < kCols; ++j) v[j] *= s;
-    }
-#pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-      v[j] *= alpha;
-      if (c) v[j] = fmaf(beta, cv[p][j], v[j]);
+      for (int j = 0; j < kCols; ++j) v[j] *= scale[p];
     }
     const int64_t o = r * ldo + col;
     if (whole) {
@@ -301,6 +288,55 @@ __device__ __forceinline__ void write_block(const float *st, int lane, char *out
   }
 }
 
+// The gradient's epilogue buffers hold a 32 x 32 box as TMA moves it: rows of
+// 128 bytes (fp32, 128-byte swizzle) or 64 bytes (16-bit, 64-byte swizzle).
+// A lane owns a row; both patterns are free of bank conflicts.
+__device__ __forceinline__ void box_read(const uint8_t *buf, int lane, int32_t dtype, float (&v)[32]) {
+  if (dtype == HIMUON_FP32) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float4 f = *reinterpret_cast<const float4 *>(buf + lane * 128 + ((k ^ (lane & 7)) << 4));
+      v[4 * k] = f.x; v[4 * k + 1] = f.y; v[4 * k + 2] = f.z; v[4 * k + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(buf + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4));
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const float2 f = dtype == HIMUON_FP16 ? __half22float2(*reinterpret_cast<const __half2 *>(&w[h]))
+                                              : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[h]));
+        v[8 * k + 2 * h] = f.x;
+        v[8 * k + 2 * h + 1] = f.y;
+      }
+    }
+  }
+}
+__device__ __forceinline__ void box_write(uint8_t *buf, int lane, int32_t dtype, const float (&v)[32]) {
+  if (dtype == HIMUON_FP32) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      *reinterpret_cast<float4 *>(buf + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+          make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<uint4 *>(buf + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
+          make_uint4(pack2(dtype, v[8 * k], v[8 * k + 1]), pack2(dtype, v[8 * k + 2], v[8 * k + 3]),
+                     pack2(dtype, v[8 * k + 4], v[8 * k + 5]), pack2(dtype, v[8 * k + 6], v[8 * k + 7]));
+  }
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
 // KIND 0: 16-bit operands (kind::f16); 1: int8 (kind::i8).  A_MN: A is
 // MN-major (W stored K x channels; the gradient's operands).
 //
@@ -313,23 +349,24 @@ __device__ __forceinline__ void write_block(const float *st, int lane, char *out
 // completing on the even CTA's barriers), warp 1 of the even CTA issues each
 // tile's MMAs into one of two accumulators, warps 2..9 of both drain the other
 // one meanwhile.
-template <int KIND, int A_MN, int GRAD, int NMAP, int NPTR>
+template <int KIND, int A_MN, int GRAD, int NMAP, int NOUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    expert_kernel(const __grid_constant__ MmaArgs<NMAP, NPTR> a) {
+    expert_kernel(const __grid_constant__ MmaArgs<NMAP, NOUT> a) {
   constexpr int kElems = KIND ? 128 : 64;   // K elements per stage
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float *out_stage = reinterpret_cast<float *>(sm + kRing);
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm + kRing + kEpiWarps * kStageOut);   // even CTA: both CTAs' loads
+  const uint32_t ring = kData - a.buffers * kEpiWarps * kStageOut;   // (a multiple of 1024)
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + kData);   // even CTA: both CTAs' loads
   uint64_t *empty = full + kMaxStages;        // each CTA: the stage's MMAs have read it
   uint64_t *tail_full = empty + kMaxStages;   // each CTA: its own loads of a block that needs zeros
   uint64_t *tail_ready = tail_full + kMaxStages;   // even CTA: both CTAs have written the zeros
   uint64_t *acc_full = tail_ready + kMaxStages;    // [2] each CTA: accumulator b holds a finished tile
   uint64_t *acc_empty = acc_full + 2;              // [2] even CTA: accumulator b drained by both CTAs
   uint64_t *done = acc_empty + 2;                  // even CTA: every MMA issued has completed
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  uint64_t *c_full = done + 1;                     // [3 per epilogue warp] a box of C has landed
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(c_full + 3 * kEpiWarps);
   int32_t *widest = reinterpret_cast<int32_t *>(tmem_slot + 1);
-  int32_t *start = reinterpret_cast<int32_t *>(sm + kRing + kEpiWarps * kStageOut + kBarBytes);   // [n + 1]
+  int32_t *start = reinterpret_cast<int32_t *>(sm + kData + kBarBytes);   // [n + 1]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t rank = static_cast<int32_t>(cluster_ctarank());
   const int32_t first = static_cast<int32_t>(blockIdx.x >> 1), step = static_cast<int32_t>(gridDim.x >> 1);
@@ -346,6 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(acc_empty + b, 2 * kEpiWarps);
     }
     mbar_init(done, 1);
+    for (int i = 0; i < 3 * kEpiWarps; ++i) mbar_init(c_full + i, 1);
     fence_mbar_init();
     tma_prefetch_desc(&a.x[0]);
   }
@@ -395,7 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t b_bytes =
       GRAD ? (round32(min(a.N, kTileN)) / 2 + 63) / 64 * 8192u : (*widest + 31) / 32 * kBoxBytes;
   const uint32_t stage_bytes = (kABytes + b_bytes + 1023) / 1024 * 1024;
-  const int stages = min(static_cast<int>(kRing / stage_bytes), kMaxStages);
+  const int stages = min(static_cast<int>(ring / stage_bytes), kMaxStages);
 
   if (warp == 0) {
     const uint32_t full0 = mapa_shared(smem_u32(full), 0);
@@ -548,58 +586,163 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       warp_wait(done, 0, a.status);
     }
-  } else {
+  } else if (GRAD) {
+    // This warp's boxes of G, 32 rows x 32 columns, in the order of its tiles
+    // and, inside one, of the columns.  With C, the boxes of C come by TMA up
+    // to two ahead of the one at work, also from the next tile, and the result
+    // takes their place: three buffers, so that a buffer is loaded again one
+    // box after its store was issued.
     const int q = warp & 3;             // TMEM lanes 32 q .. 32 q + 31
     const int half = (warp - 2) >> 2;   // the warp's 32-column groups: half, half + 2, ..
-    float *st = out_stage + (warp - 2) * (kStageOut / 4);
-    const bool w16 = a.odtype != HIMUON_FP32;
-    const int64_t osize = w16 ? 2 : 4, csize = a.cdtype == HIMUON_FP32 ? 4 : 2;
+    uint8_t *buf = sm + ring + (warp - 2) * a.buffers * kStageOut;
+    uint64_t *landed = c_full + 3 * (warp - 2);
     const uint32_t free0 = mapa_shared(smem_u32(acc_empty), 0);
-    int32_t j = 0, from = 0;
-    for (int32_t idx = first; idx < n_tiles; idx += step, ++j) {
-      const Tile t = tile_at<GRAD>(a, start, idx, from);
-      from = t.e;
+    const uint32_t c_bytes = a.cdtype == HIMUON_FP32 ? 4096 : 2048;
+    // A box that reaches over the last column is stored up to the end of that
+    // column's 16 bytes (observed: columns behind it in the row's pitch were
+    // overwritten); where G's width is no multiple of 16 bytes the last boxes
+    // are stored element by element.
+    const bool whole_runs = a.N % (a.odtype == HIMUON_FP32 ? 4 : 8) == 0;
+    struct Box {
+      int32_t idx, i;   // tile, column group; idx >= n_tiles: none left
+      Tile t;
+    };
+    auto groups = [&](const Tile &t) {   // of this tile that are inside G
+      return t.m0 + 128 * rank + 32 * q < a.M ? (t.valid + 31) / 32 : 0;
+    };
+    auto settle = [&](Box &x) {   // to the first box at or after (idx, i)
+      while (x.idx < n_tiles && x.i >= groups(x.t)) {
+        x.idx += step;
+        x.i = half;
+        if (x.idx < n_tiles) x.t = tile_at<GRAD>(a, start, x.idx, 0);
+      }
+    };
+    auto load_c = [&](Box &x, int at) {   // box x into buffer `at`, then on to the next box
+      if (x.idx >= n_tiles) return;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(landed + at, c_bytes);
+        tma_load_3d(buf + at * kStageOut, NOUT > 1 ? &a.c[x.t.e] : &a.c[0], x.t.n0 + 32 * x.i,
+                    x.t.m0 + 128 * rank + 32 * q, NOUT > 1 ? 0 : x.t.e, landed + at);
+      }
+      __syncwarp();
+      x.i += 2;
+      settle(x);
+    };
+    Box ahead{first, half, {}};
+    if (a.has_c && first < n_tiles) {
+      ahead.t = tile_at<GRAD>(a, start, first, 0);
+      settle(ahead);
+      load_c(ahead, 0);
+      load_c(ahead, 1);
+    }
+    int at = 0;                  // buffer of the box at work
+    uint32_t c_phase = 0;        // per buffer
+    bool ok = true;
+    int32_t j = 0;
+    for (int32_t idx = first; idx < n_tiles && ok; idx += step, ++j) {
+      const Tile t = tile_at<GRAD>(a, start, idx, 0);
       const int b = j & 1;
-      if (!warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status)) break;
+      if (!(ok = warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status))) break;
       tc_fence_after();
       const uint32_t taddr = tmem + static_cast<uint32_t>(b * kTileN) + (static_cast<uint32_t>(q * 32) << 16);
-      const int32_t m = t.m0 + 128 * rank + 32 * q;   // this warp's 32 rows of D
-      const int32_t m_in = min(32, a.M - m);
-      const bool empty_sum = GRAD && t.hi == t.lo;
-      char *out = (NPTR > 1 ? a.out[GRAD ? t.e : 0] : a.out[0] + (GRAD ? t.e * a.out_stride : 0));
-      const char *c = !GRAD || !a.has_c ? nullptr : (NPTR > 1 ? a.c[t.e] : a.c[0] + t.e * a.c_stride);
-      float chan = 1.f;
-      if (KIND && lane < m_in) chan = a.w_scale[t.e * a.ld_scale + m + lane];
-#pragma unroll 1
-      for (int32_t i = half; i < (t.valid + 31) / 32 && m_in > 0; i += 2) {
+      const int32_t in = groups(t);
+      for (int32_t i = half; i < in; i += 2) {
         float v[32];
-        if (empty_sum) {
+        if (t.hi == t.lo) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) v[k] = 0.f;
         } else {
           tmem_ld32(taddr + 32 * i, v);
           tmem_wait_ld();
         }
-        __syncwarp();   // the last block's readers are done
-        if (GRAD) {     // lane: row m + lane of G, its 32 columns
+        if (i + 2 >= in) {   // the accumulator is read
+          tc_fence_before();
+          __syncwarp();
+          if (elect_one()) mbar_arrive_cluster(free0 + 8 * b);
+        }
+        if (a.has_c) {
+          if (!(ok = warp_wait(landed + at, (c_phase >> at) & 1, a.status))) break;
+          c_phase ^= 1u << at;
+          float cv[32];
+          box_read(buf + at * kStageOut, lane, a.cdtype, cv);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<float4 *>(st + lane * 32 + ((k ^ (lane & 7)) * 4)) =
-                make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        } else {        // lane: channel m + lane of 32 rows of Y
+          for (int k = 0; k < 32; ++k) v[k] = fmaf(a.beta, cv[k], a.alpha * v[k]);
+        } else {
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            st[k * 32 + (((lane >> 2) ^ (k & 7)) * 4) + (lane & 3)] =
-                KIND ? static_cast<float>(__float_as_int(v[k])) * chan : v[k];
+          for (int k = 0; k < 32; ++k) v[k] *= a.alpha;
+          if (elect_one()) bulk_wait_read<1>();   // two buffers: the store before the last has read this one
         }
         __syncwarp();
-        const int32_t r_in = GRAD ? m_in : min(32, t.valid - 32 * i), c_in = GRAD ? min(32, t.valid - 32 * i) : m_in;
-        const int64_t r0 = GRAD ? m : t.n0 + 32 * i, c0 = GRAD ? t.n0 + 32 * i : m;
-        char *o = out + (r0 * a.ldo + c0) * osize;
-        const char *cc = c ? c + (r0 * a.ldc + c0) * csize : nullptr;
+        const int32_t m = t.m0 + 128 * rank + 32 * q, n0 = t.n0 + 32 * i;
+        const bool by_box = n0 + 32 <= a.N || whole_runs;
+        if (by_box) {
+          box_write(buf + at * kStageOut, lane, a.odtype, v);
+          fence_proxy_async_smem();
+        } else if (m + lane < a.M) {
+          char *o = (NOUT > 1 ? a.out[t.e] : a.out[0] + t.e * a.out_stride);
+          const int64_t at0 = (m + lane) * a.ldo + n0;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (n0 + k < a.N) st_any(o, a.odtype, at0 + k, v[k]);
+        }
+        __syncwarp();
+        if (elect_one()) {
+          if (by_box)
+            tma_store_3d(NOUT > 1 ? &a.g[t.e] : &a.g[0], buf + at * kStageOut, n0, m, NOUT > 1 ? 0 : t.e);
+          bulk_commit();
+          if (a.has_c) bulk_wait_read<1>();   // the store of the box before has read its buffer
+        }
+        __syncwarp();
+        if (a.has_c) load_c(ahead, at == 0 ? 2 : at - 1);
+        at = at + 1 == a.buffers ? 0 : at + 1;
+      }
+      if (in <= half) {   // no box of this warp's in the tile
+        tc_fence_before();
+        __syncwarp();
+        if (elect_one()) mbar_arrive_cluster(free0 + 8 * b);
+      }
+    }
+    if (!ok && a.has_c) {   // gave up: what was loaded ahead lands before the CTA ends (bounded)
+      for (int k = 0; k < 3; ++k) warp_wait(landed + k, (c_phase >> k) & 1, a.status);
+    }
+    if (elect_one()) bulk_wait0();
+  } else {
+    const int q = warp & 3;             // TMEM lanes 32 q .. 32 q + 31
+    const int half = (warp - 2) >> 2;   // the warp's 32-column groups: half, half + 2, ..
+    float *st = reinterpret_cast<float *>(sm + ring + (warp - 2) * kStageOut);
+    const bool w16 = a.odtype != HIMUON_FP32;
+    const int64_t osize = w16 ? 2 : 4;
+    const uint32_t free0 = mapa_shared(smem_u32(acc_empty), 0);
+    int32_t j = 0, from = 0;
+    for (int32_t idx = first; idx < n_tiles; idx += step, ++j) {
+      const Tile t = tile_at<GRAD>(a, start, idx, from);
+      from = t.e;
+      const int b = j & 1;
+      const int32_t m = t.m0 + 128 * rank + 32 * q;   // this warp's 32 channels
+      const int32_t m_in = min(32, a.M - m);
+      float chan = 1.f;
+      if (KIND && lane < m_in) chan = a.w_scale[t.e * a.ld_scale + m + lane];
+      if (!warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + static_cast<uint32_t>(b * kTileN) + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+      for (int32_t i = half; i < (t.valid + 31) / 32 && m_in > 0; i += 2) {
+        float v[32];
+        tmem_ld32(taddr + 32 * i, v);
+        tmem_wait_ld();
+        __syncwarp();   // the last block's readers are done
+        // lane: channel m + lane of 32 rows of Y
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          st[k * 32 + (((lane >> 2) ^ (k & 7)) * 4) + (lane & 3)] =
+              KIND ? static_cast<float>(__float_as_int(v[k])) * chan : v[k];
+        __syncwarp();
+        const int64_t r0 = t.n0 + 32 * i;
+        const int32_t r_in = min(32, t.valid - 32 * i);
+        char *o = a.out[0] + (r0 * a.ldo + m) * osize;
         const float *rs = KIND ? a.x_scale + r0 : nullptr;
-        if (w16) write_block<1>(st, lane, o, a.odtype, a.ldo, r_in, c_in, a.alpha, cc, a.cdtype, a.ldc, a.beta, rs);
-        else write_block<0>(st, lane, o, a.odtype, a.ldo, r_in, c_in, a.alpha, cc, a.cdtype, a.ldc, a.beta, rs);
+        if (w16) write_block<1>(st, lane, o, a.odtype, a.ldo, r_in, m_in, rs);
+        else write_block<0>(st, lane, o, a.odtype, a.ldo, r_in, m_in, rs);
       }
       tc_fence_before();
       __syncwarp();
@@ -919,12 +1062,16 @@ EncodeTiledFn encode_fn() {
 }
 
 // Map over `n` row-major matrices `stride` bytes apart (2-D when n = 0): boxes
-// of 128 bytes of columns x box_rows, 128-byte swizzle, zeros outside.
-bool make_map(CUtensorMap *map, const himuon_mat &m, int32_t n, int64_t stride, uint32_t box_rows) {
+// of box_rows x box_cols (0: as many as make 128 bytes) with the swizzle of the
+// box's width (64 or 128 bytes), zeros outside.
+bool make_map(CUtensorMap *map, const himuon_mat &m, int32_t n, int64_t stride, uint32_t box_rows,
+              uint32_t box_cols = 0) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const int64_t es = static_cast<int64_t>(size_of(m.dtype));
+  if (!box_cols) box_cols = static_cast<uint32_t>(128 / es);
   const CUtensorMapDataType dt = m.dtype == HIMUON_I8     ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                 : m.dtype == HIMUON_FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                  : m.dtype == HIMUON_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   // the pitch of a single row is never used and may be any number
@@ -932,10 +1079,11 @@ bool make_map(CUtensorMap *map, const himuon_mat &m, int32_t n, int64_t stride, 
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(m.cols), static_cast<cuuint64_t>(m.rows),
                         static_cast<cuuint64_t>(n > 0 ? n : 1)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch), static_cast<cuuint64_t>(n > 1 ? stride : pitch * m.rows)};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), box_rows, 1};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
   cuuint32_t es1[3] = {1, 1, 1};
   return enc(map, dt, n > 0 ? 3 : 2, m.data, dims, strides, box, es1, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             box_cols * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -959,9 +1107,9 @@ int sm_count() {
   return sms;
 }
 
-template <int KIND, int A_MN, int GRAD, int NMAP, int NPTR>
-int launch_mma(const MmaArgs<NMAP, NPTR> &a, int64_t most_tiles, cudaStream_t stream) {
-  auto kern = expert_kernel<KIND, A_MN, GRAD, NMAP, NPTR>;
+template <int KIND, int A_MN, int GRAD, int NMAP, int NOUT>
+int launch_mma(const MmaArgs<NMAP, NOUT> &a, int64_t most_tiles, cudaStream_t stream) {
+  auto kern = expert_kernel<KIND, A_MN, GRAD, NMAP, NOUT>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return HIMUON_ERR_CUDA;
   const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(most_tiles, sm_count() / 2));
@@ -970,8 +1118,8 @@ int launch_mma(const MmaArgs<NMAP, NPTR> &a, int64_t most_tiles, cudaStream_t st
   return cudaGetLastError() == cudaSuccess ? HIMUON_OK : HIMUON_ERR_CUDA;
 }
 
-template <int NMAP, int NPTR>
-void common_args(MmaArgs<NMAP, NPTR> &a, const int32_t *offsets, int32_t e0, int32_t n, int64_t rows) {
+template <int NMAP, int NOUT>
+void common_args(MmaArgs<NMAP, NOUT> &a, const int32_t *offsets, int32_t e0, int32_t n, int64_t rows) {
   a.offsets = offsets ? offsets + e0 : nullptr;
   a.rows = rows;
   a.n = n;
@@ -979,7 +1127,8 @@ void common_args(MmaArgs<NMAP, NPTR> &a, const int32_t *offsets, int32_t e0, int
   a.x_scale = a.w_scale = nullptr;
   a.ld_scale = 0;
   a.has_c = 0;
-  a.ldc = a.c_stride = a.out_stride = 0;
+  a.ldo = a.out_stride = 0;
+  a.buffers = 1;
   a.cdtype = HIMUON_FP32;
   a.alpha = 1.f;
   a.beta = 0.f;
@@ -1013,7 +1162,6 @@ int product_launch(const himuon_mat *X, const float *x_scale, const himuon_mat *
     a.ld_scale = w_scale->ld;
   }
   a.out[0] = static_cast<char *>(Y->data);
-  a.c[0] = nullptr;
   a.ldo = Y->ld;
   a.odtype = Y->dtype;
   const int64_t mt_m = (Y->cols + kTileM - 1) / kTileM;
@@ -1037,11 +1185,11 @@ int run_product(const himuon_mat *X, const float *x_scale, const himuon_mat *W, 
   return HIMUON_OK;
 }
 
-template <int NPTR>
+template <int NOUT>
 int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_t n, const int32_t *offsets,
                     float alpha, float beta, const himuon_mat *C, int64_t c_stride, const himuon_mat *G,
                     int64_t g_stride, cudaStream_t stream) {
-  MmaArgs<1, NPTR> a;
+  MmaArgs<1, NOUT> a;
   common_args(a, offsets, e0, n, A->rows);
   if (A->rows == 0) {
     // no row is ever loaded: the maps only have to be valid, and G's memory is
@@ -1061,18 +1209,16 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
   a.alpha = alpha;
   a.beta = beta;
   a.has_c = C != nullptr;
-  for (int32_t i = 0; i < (NPTR > 1 ? n : 1); ++i) {
+  for (int32_t i = 0; i < (NOUT > 1 ? n : 1); ++i) {
+    if (!make_map(&a.g[i], G[e0 + i], NOUT > 1 ? 1 : n, g_stride, 32, 32)) return HIMUON_ERR_CUDA;
     a.out[i] = static_cast<char *>(G[e0 + i].data);
-    a.c[i] = C ? static_cast<const char *>(C[e0 + i].data) : nullptr;
+    if (C && !make_map(&a.c[i], C[e0 + i], NOUT > 1 ? 1 : n, c_stride, 32, 32)) return HIMUON_ERR_CUDA;
   }
-  a.out_stride = g_stride;
-  a.c_stride = c_stride;
   a.ldo = G->ld;
+  a.out_stride = g_stride;
   a.odtype = G->dtype;
-  if (C) {
-    a.ldc = C->ld;
-    a.cdtype = C->dtype;
-  }
+  if (C) a.cdtype = C->dtype;
+  a.buffers = C ? 3 : 2;
   const int64_t most = n * ((A->cols + kTileM - 1) / kTileM) * ((B->cols + kTileN - 1) / kTileN);
   return launch_mma<0, 1, 1>(a, most, stream);
 }
