@@ -5,6 +5,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 #include <vector>
 
 #include "himuon.h"
@@ -1100,10 +1101,16 @@ bool stacked(const himuon_mat *m, int32_t n, int64_t *stride) {
   return true;
 }
 
+// SMs of the current device (looked up once per device).
 int sm_count() {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  int sms = known[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    known[dev].store(sms, std::memory_order_relaxed);
+  }
   return sms;
 }
 
@@ -1276,18 +1283,21 @@ int himuon_expert_gradient(const himuon_mat *A, const himuon_mat *B, int32_t n, 
   if (!is16(A->dtype) || !is_float(G->dtype) || (C && !is_float(C->dtype))) return HIMUON_ERR_UNSUPPORTED;
   if (B->dtype != A->dtype || B->rows != A->rows || G->rows != A->cols || G->cols != B->cols) return HIMUON_ERR_INVALID;
   if (C && (C->rows != G->rows || C->cols != G->cols)) return HIMUON_ERR_INVALID;
-  std::vector<const void *> seen(n);
-  for (int32_t e = 0; e < n; ++e) {
-    seen[e] = G[e].data;
-    if (C && beta != 0.f && C[e].data == G[e].data && (C->ld != G->ld || C->dtype != G->dtype)) return HIMUON_ERR_INVALID;
+  if (C && beta != 0.f && (C->ld != G->ld || C->dtype != G->dtype))
+    for (int32_t e = 0; e < n; ++e)
+      if (C[e].data == G[e].data) return HIMUON_ERR_INVALID;
+  int64_t g_stride, c_stride = 0;
+  const bool g_stacked = stacked(G, n, &g_stride);
+  if (!g_stacked) {   // (stacked ones differ)
+    std::vector<const void *> seen(n);
+    for (int32_t e = 0; e < n; ++e) seen[e] = G[e].data;
+    std::sort(seen.begin(), seen.end());
+    if (std::adjacent_find(seen.begin(), seen.end()) != seen.end()) return HIMUON_ERR_INVALID;
   }
-  std::sort(seen.begin(), seen.end());
-  if (std::adjacent_find(seen.begin(), seen.end()) != seen.end()) return HIMUON_ERR_INVALID;
   rc = device_usable();
   if (rc) return rc;
   if (beta == 0.f) C = nullptr;
-  int64_t g_stride, c_stride = 0;
-  const bool st = stacked(G, n, &g_stride) && (!C || stacked(C, n, &c_stride));
+  const bool st = g_stacked && (!C || stacked(C, n, &c_stride));
   const int32_t cap = st ? kMaxStack : kMaxList;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (int32_t e0 = 0; e0 < n; e0 += cap) {

@@ -101,16 +101,23 @@ def _check(code: int, what: str) -> None:
 
 # ---------------------------------------------------------------- marshalling
 
+_DTYPES: dict = {}
+
+
 def _dtype_code(t) -> int:
-    import torch
-    return {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32, torch.int8: I8}[t.dtype]
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32, torch.int8: I8})
+    return _DTYPES[t.dtype]
 
 
 def mat(t) -> Mat:
     """himuon_mat of a 2-D tensor whose rows are contiguous (stride(1) == 1)."""
-    if t.dim() != 2 or t.stride(1) != 1:
+    stride = t.stride()
+    if len(stride) != 2 or stride[1] != 1:
         raise ValueError("himuon needs 2-D tensors with unit column stride")
-    return Mat(t.data_ptr(), t.shape[0], t.shape[1], t.stride(0), _dtype_code(t))
+    rows, cols = t.shape
+    return Mat(t.data_ptr(), rows, cols, stride[0], _dtype_code(t))
 
 
 def _mats(ts) -> ctypes.Array:
@@ -254,26 +261,23 @@ def momentum_step(W, M, G, mu: float, lr: float, p: Params, splits=None, update_
 
 
 # ---------------------------------------------------------------- expert products
-# himuon_mat as a numpy record: a 3-D tensor of stacked matrices is described
-# by a few array operations instead of one ctypes record per matrix.
-_MAT_RECORD = None
-
-
 def _stack(ts):
     """(himuon_mat array, its address, n) of a list of 2-D tensors or of a 3-D
-    tensor of stacked matrices (unit column stride)."""
-    import numpy as np
+    tensor of stacked matrices (unit column stride).
+
+    The records of stacked matrices are filled as five 64-bit words each (a
+    few array operations instead of one ctypes record per matrix).
+    """
     if hasattr(ts, "dim"):
-        global _MAT_RECORD
-        if ts.dim() != 3 or ts.stride(2) != 1:
+        import numpy as np
+        stride = ts.stride()
+        if len(stride) != 3 or stride[2] != 1:
             raise ValueError("stacked matrices are a 3-D tensor with unit column stride")
-        if _MAT_RECORD is None:
-            _MAT_RECORD = np.dtype([("data", "i8"), ("rows", "i8"), ("cols", "i8"), ("ld", "i8"), ("dtype", "i4"),
-                                    ("pad", "i4")])
         n, rows, cols = ts.shape
-        rec = np.empty(n, _MAT_RECORD)
-        rec[:] = (0, rows, cols, ts.stride(1), _dtype_code(ts), 0)
-        rec["data"] = ts.data_ptr() + np.arange(n) * (ts.stride(0) * ts.element_size())
+        rec = np.empty((n, 5), np.int64)
+        rec[:, 1:] = (rows, cols, stride[1], _dtype_code(ts))
+        base, step = ts.data_ptr(), stride[0] * ts.element_size()
+        rec[:, 0] = np.arange(base, base + n * step, step) if step else base
         return rec, rec.ctypes.data, n
     arr = _mats(ts)
     return arr, ctypes.addressof(arr), len(ts)
@@ -281,22 +285,23 @@ def _stack(ts):
 
 def _row_vector(t) -> Mat:
     """himuon_mat of a contiguous 1-D tensor (a 1 x len matrix)."""
-    if t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1):
+    if t.dim() != 1 or (t.shape[0] > 1 and t.stride(0) != 1):
         raise ValueError("scales are contiguous 1-D tensors")
     return Mat(t.data_ptr(), 1, t.shape[0], max(1, t.shape[0]), _dtype_code(t))
 
 
-def _one_device(*operands):
-    """The CUDA device that every tensor of the operands (tensors, lists of
-    them or None) is on."""
-    dev = None
+def _one_device(*operands) -> int:
+    """The index of the CUDA device that every tensor of the operands (tensors,
+    lists of them or None) is on."""
+    dev = -1
     for op in operands:
         for t in (op if isinstance(op, (list, tuple)) else (op,)):
             if t is None:
                 continue
-            if not t.is_cuda or (dev is not None and t.device != dev):
+            d = t.get_device()
+            if d < 0 or (dev >= 0 and d != dev):
                 raise ValueError("expert products need all their tensors on one CUDA device")
-            dev = t.device
+            dev = d
     return dev
 
 
@@ -313,11 +318,19 @@ def _on_device(dev, name, stream, *args):
     """Calls the entry point with the operands' device current, on `stream` or
     on that device's current stream."""
     import torch
-    if stream is not None and stream.device != dev:
-        raise ValueError("the stream is on another device than the tensors")
-    with torch.cuda.device(dev):
-        s = stream if stream is not None else torch.cuda.current_stream(dev)
-        _check(getattr(load(), name)(*args, s.cuda_stream), name)
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError("the stream is on another device than the tensors")
+        raw = stream.cuda_stream
+    else:
+        raw = torch._C._cuda_getCurrentRawStream(dev)   # (current_stream builds an object: 2 us)
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == dev:
+        code = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, raw)
+    _check(code, name)
 
 
 def expert_product(X, W, Y, offsets=None, w_trans: bool = False, stream=None) -> None:
