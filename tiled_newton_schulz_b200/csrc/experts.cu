@@ -52,7 +52,12 @@ constexpr int kMaxStages = 10;
 constexpr uint32_t kStageOut = 4096;    // an epilogue warp's buffer: 32 x 32 fp32, swizzled
 constexpr int kEpiWarps = 8;
 constexpr int kTileM = 256, kTileN = 256;   // a CTA pair's tile of D
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kThreads = 128 + 32 * kEpiWarps;   // three warpgroups: loads and MMAs (warps 0, 1), epilogue (4..11)
+// fp32 results of 16-bit operands: the tensor core's accumulator truncates at
+// every K = 16 step, which costs an fp32 result about 1e-8 of itself per step
+// (K = 1100: 1.1e-6 against 2.6e-7 for rounded fp32 sums).  Their sums are cut
+// every kChunk stages; the epilogue adds the pieces in fp32 registers.
+constexpr int kChunk = 8;
 constexpr uint32_t kBarBytes = 576;
 constexpr uint32_t kSmem = kData + kBarBytes + 4 * (kMaxStack + 4) + 1024;
 static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -292,12 +297,16 @@ __device__ __forceinline__ void write_block(const float *st, int lane, char *out
 // The gradient's epilogue buffers hold a 32 x 32 box as TMA moves it: rows of
 // 128 bytes (fp32, 128-byte swizzle) or 64 bytes (16-bit, 64-byte swizzle).
 // A lane owns a row; both patterns are free of bank conflicts.
-__device__ __forceinline__ void box_read(const uint8_t *buf, int lane, int32_t dtype, float (&v)[32]) {
+__device__ __forceinline__ void box_combine(const uint8_t *buf, int lane, int32_t dtype, float alpha, float beta,
+                                            float (&v)[32]) {   // v = alpha v + beta (this lane's row)
   if (dtype == HIMUON_FP32) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float4 f = *reinterpret_cast<const float4 *>(buf + lane * 128 + ((k ^ (lane & 7)) << 4));
-      v[4 * k] = f.x; v[4 * k + 1] = f.y; v[4 * k + 2] = f.z; v[4 * k + 3] = f.w;
+      v[4 * k] = fmaf(beta, f.x, alpha * v[4 * k]);
+      v[4 * k + 1] = fmaf(beta, f.y, alpha * v[4 * k + 1]);
+      v[4 * k + 2] = fmaf(beta, f.z, alpha * v[4 * k + 2]);
+      v[4 * k + 3] = fmaf(beta, f.w, alpha * v[4 * k + 3]);
     }
   } else {
 #pragma unroll
@@ -308,8 +317,8 @@ __device__ __forceinline__ void box_read(const uint8_t *buf, int lane, int32_t d
       for (int h = 0; h < 4; ++h) {
         const float2 f = dtype == HIMUON_FP16 ? __half22float2(*reinterpret_cast<const __half2 *>(&w[h]))
                                               : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[h]));
-        v[8 * k + 2 * h] = f.x;
-        v[8 * k + 2 * h + 1] = f.y;
+        v[8 * k + 2 * h] = fmaf(beta, f.x, alpha * v[8 * k + 2 * h]);
+        v[8 * k + 2 * h + 1] = fmaf(beta, f.y, alpha * v[8 * k + 2 * h + 1]);
       }
     }
   }
@@ -338,8 +347,34 @@ __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
+// PREC: an epilogue warp's column groups half, half + 2, .. (below `in`) of
+// accumulator piece p, added to its running sums.
+template <int PREC>
+__device__ __forceinline__ void read_pieces(float (&sum)[PREC ? 4 : 1][32], uint32_t taddr, int half, int32_t in,
+                                            int32_t p) {
+#pragma unroll
+  for (int g = 0; g < (PREC ? 4 : 1); ++g) {
+    const int32_t i = half + 2 * g;
+    if (i >= in) continue;
+    if (p == 0) {
+      tmem_ld32(taddr + 32 * i, sum[g]);
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[16];
+        tmem_ld16(taddr + 32 * i + 16 * h, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sum[g][16 * h + k] += v[k];
+      }
+    }
+  }
+}
+
 // KIND 0: 16-bit operands (kind::f16); 1: int8 (kind::i8).  A_MN: A is
-// MN-major (W stored K x channels; the gradient's operands).
+// MN-major (W stored K x channels; the gradient's operands).  PREC: sums in
+// pieces of kChunk stages (fp32 results).
 //
 // A pair of CTAs (cluster of 2) works on one 256-row tile of D: each CTA holds
 // 128 of its rows (in its tensor memory) and of A's, and half of B's columns;
@@ -348,9 +383,9 @@ __device__ __forceinline__ void bulk_wait_read() {
 // shared memory, more than its 128 bytes per cycle; the pair needs 64 + 64.
 // Persistent: warp 0 streams its CTA's operands through a ring of stages (TMA,
 // completing on the even CTA's barriers), warp 1 of the even CTA issues each
-// tile's MMAs into one of two accumulators, warps 2..9 of both drain the other
+// tile's MMAs into one of two accumulators, warps 4..11 of both drain the other
 // one meanwhile.
-template <int KIND, int A_MN, int GRAD, int NMAP, int NOUT>
+template <int KIND, int A_MN, int GRAD, int NMAP, int NOUT, int PREC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expert_kernel(const __grid_constant__ MmaArgs<NMAP, NOUT> a) {
   constexpr int kElems = KIND ? 128 : 64;   // K elements per stage
@@ -436,7 +471,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t stage_bytes = (kABytes + b_bytes + 1023) / 1024 * 1024;
   const int stages = min(static_cast<int>(ring / stage_bytes), kMaxStages);
 
+  // PREC: the epilogue's running sums take 128 registers per thread: 3 x 168
+  // per thread of the three warpgroups become 56 + 2 x 224
   if (warp == 0) {
+    if (PREC) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     const uint32_t full0 = mapa_shared(smem_u32(full), 0);
     int s = 0;
     uint32_t phase = 1;   // parity of the stage's last release; the first round finds it free
@@ -514,6 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       else if (rank == 0) warp_wait(full + st, static_cast<uint32_t>((i / stages) & 1), a.status);
     }
   } else if (warp == 1) {
+    if (PREC) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (rank == 0 || GRAD) {
       const uint32_t ready0 = mapa_shared(smem_u32(tail_ready), 0);
       // descriptors of stage 0, without the address
@@ -526,22 +565,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       Tile t, next;
       if (first < n_tiles) next = tile_at<GRAD>(a, start, first, 0);
-      for (int32_t idx = first; idx < n_tiles && ok; idx += step, ++j) {
+      for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
         t = next;
         const bool more = idx + step < n_tiles;
         if (more && (GRAD && t.hi == t.lo)) next = tile_at<GRAD>(a, start, idx + step, t.e);
         const int32_t len = GRAD ? t.hi - t.lo : a.K;
-        const int b = j & 1;
-        if (rank == 0 && j >= 2) {
-          ok = warp_wait<true>(acc_empty + b, static_cast<uint32_t>(((j >> 1) - 1) & 1), a.status);
-          if (!ok) break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(b * kTileN);
         const uint32_t idesc = a.idesc | (static_cast<uint32_t>(t.width >> 3) << 17);
+        uint32_t d = 0;
+        // the next accumulator, once the epilogue has drained it
+        auto acquire = [&] {
+          const int b = j & 1;
+          d = tmem + static_cast<uint32_t>(b * kTileN);
+          if (rank != 0) return true;
+          const bool free = j < 2 || warp_wait<true>(acc_empty + b, static_cast<uint32_t>(((j >> 1) - 1) & 1), a.status);
+          tc_fence_after();
+          return free;
+        };
+        auto hand_over = [&] {
+          if (rank == 0 && elect_one()) mma_commit_pair(acc_full + (j & 1), 3);
+          __syncwarp();
+          ++j;
+        };
+        if (GRAD && len == 0) {
+          if (!(ok = acquire())) break;
+          hand_over();
+        }
         for (int32_t k = 0; k < len; k += kElems) {
           const uint32_t as = smem_u32(sm) + s * stage_bytes;
           const int32_t left = len - k;
+          const bool fresh = PREC ? k % (kChunk * kElems) == 0 : k == 0;
+          if (fresh && !(ok = acquire())) break;
           if (rank == 0 && !(ok = warp_wait(full + s, phase, a.status))) break;
           if (GRAD && left < kElems && (left & 15)) {
             // the rows behind the group (other groups' or none) up to the next
@@ -565,21 +618,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int32_t kk = 0; kk < 4; ++kk) {
                 if (kk > 0 && kk * (kElems / 4) >= left) break;
-                if (KIND) mma_i8_ss_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, (k > 0 || kk > 0) ? 1u : 0u);
-                else mma_ss_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, (k > 0 || kk > 0) ? 1u : 0u);
+                if (KIND) mma_i8_ss_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, (!fresh || kk > 0) ? 1u : 0u);
+                else mma_ss_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, (!fresh || kk > 0) ? 1u : 0u);
               }
               mma_commit_pair(empty + s, 3);   // the stage is free in both CTAs once these MMAs have read it
             }
             __syncwarp();
           }
+          if (left <= kElems || (PREC && (k + kElems) % (kChunk * kElems) == 0)) hand_over();
           if (k == 0 && more) next = tile_at<GRAD>(a, start, idx + step, t.e);
           if (++s == stages) {
             s = 0;
             phase ^= 1;
           }
         }
-        if (ok && rank == 0 && elect_one()) mma_commit_pair(acc_full + b, 3);
-        __syncwarp();
       }
     }
     if (rank == 0) {   // nothing is in flight when the pair leaves and releases its tensor memory
@@ -587,16 +639,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       warp_wait(done, 0, a.status);
     }
+  } else if (warp < 4) {
+    if (PREC) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   } else if (GRAD) {
+    if (PREC) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // This warp's boxes of G, 32 rows x 32 columns, in the order of its tiles
     // and, inside one, of the columns.  With C, the boxes of C come by TMA up
     // to two ahead of the one at work, also from the next tile, and the result
     // takes their place: three buffers, so that a buffer is loaded again one
     // box after its store was issued.
     const int q = warp & 3;             // TMEM lanes 32 q .. 32 q + 31
-    const int half = (warp - 2) >> 2;   // the warp's 32-column groups: half, half + 2, ..
-    uint8_t *buf = sm + ring + (warp - 2) * a.buffers * kStageOut;
-    uint64_t *landed = c_full + 3 * (warp - 2);
+    const int half = (warp - 4) >> 2;   // the warp's 32-column groups: half, half + 2, ..
+    uint8_t *buf = sm + ring + (warp - 4) * a.buffers * kStageOut;
+    uint64_t *landed = c_full + 3 * (warp - 4);
     const uint32_t free0 = mapa_shared(smem_u32(acc_empty), 0);
     const uint32_t c_bytes = a.cdtype == HIMUON_FP32 ? 4096 : 2048;
     // A box that reaches over the last column is stored up to the end of that
@@ -640,34 +695,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t c_phase = 0;        // per buffer
     bool ok = true;
     int32_t j = 0;
-    for (int32_t idx = first; idx < n_tiles && ok; idx += step, ++j) {
+    for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
       const Tile t = tile_at<GRAD>(a, start, idx, 0);
-      const int b = j & 1;
-      if (!(ok = warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status))) break;
-      tc_fence_after();
-      const uint32_t taddr = tmem + static_cast<uint32_t>(b * kTileN) + (static_cast<uint32_t>(q * 32) << 16);
       const int32_t in = groups(t);
-      for (int32_t i = half; i < in; i += 2) {
-        float v[32];
-        if (t.hi == t.lo) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = 0.f;
-        } else {
-          tmem_ld32(taddr + 32 * i, v);
-          tmem_wait_ld();
-        }
-        if (i + 2 >= in) {   // the accumulator is read
-          tc_fence_before();
-          __syncwarp();
-          if (elect_one()) mbar_arrive_cluster(free0 + 8 * b);
-        }
+      auto emit = [&](int32_t i, float(&v)[32]) {   // column group i: combine with C, store
         if (a.has_c) {
-          if (!(ok = warp_wait(landed + at, (c_phase >> at) & 1, a.status))) break;
+          if (!(ok = warp_wait(landed + at, (c_phase >> at) & 1, a.status))) return;
           c_phase ^= 1u << at;
-          float cv[32];
-          box_read(buf + at * kStageOut, lane, a.cdtype, cv);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = fmaf(a.beta, cv[k], a.alpha * v[k]);
+          box_combine(buf + at * kStageOut, lane, a.cdtype, a.alpha, a.beta, v);
         } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) v[k] *= a.alpha;
@@ -696,11 +731,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (a.has_c) load_c(ahead, at == 0 ? 2 : at - 1);
         at = at + 1 == a.buffers ? 0 : at + 1;
-      }
-      if (in <= half) {   // no box of this warp's in the tile
-        tc_fence_before();
-        __syncwarp();
-        if (elect_one()) mbar_arrive_cluster(free0 + 8 * b);
+      };
+      const int32_t pieces = PREC ? max(1, (t.hi - t.lo + kChunk * kElems - 1) / (kChunk * kElems)) : 1;
+      float sum[PREC ? 4 : 1][32];
+      for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
+        const int b = j & 1;
+        if (!(ok = warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status))) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem + static_cast<uint32_t>(b * kTileN) + (static_cast<uint32_t>(q * 32) << 16);
+        auto release = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (elect_one()) mbar_arrive_cluster(free0 + 8 * b);
+        };
+        if (PREC && pieces > 1) {
+          read_pieces<PREC>(sum, taddr, half, in, p);
+          release();
+          if (p + 1 == pieces) {
+#pragma unroll
+            for (int g = 0; g < (PREC ? 4 : 1); ++g)
+              if (half + 2 * g < in && ok) emit(half + 2 * g, sum[g]);
+          }
+        } else {
+          for (int32_t i = half; i < in && ok; i += 2) {
+            if (t.hi == t.lo) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) sum[0][k] = 0.f;
+            } else {
+              tmem_ld32(taddr + 32 * i, sum[0]);
+              tmem_wait_ld();
+            }
+            if (i + 2 >= in) release();   // the accumulator is read
+            emit(i, sum[0]);
+          }
+          if (in <= half) release();   // no box of this warp's in the tile
+        }
       }
     }
     if (!ok && a.has_c) {   // gave up: what was loaded ahead lands before the CTA ends (bounded)
@@ -708,29 +773,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (elect_one()) bulk_wait0();
   } else {
+    if (PREC) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int q = warp & 3;             // TMEM lanes 32 q .. 32 q + 31
-    const int half = (warp - 2) >> 2;   // the warp's 32-column groups: half, half + 2, ..
-    float *st = reinterpret_cast<float *>(sm + ring + (warp - 2) * kStageOut);
+    const int half = (warp - 4) >> 2;   // the warp's 32-column groups: half, half + 2, ..
+    float *st = reinterpret_cast<float *>(sm + ring + (warp - 4) * kStageOut);
     const bool w16 = a.odtype != HIMUON_FP32;
     const int64_t osize = w16 ? 2 : 4;
     const uint32_t free0 = mapa_shared(smem_u32(acc_empty), 0);
     int32_t j = 0, from = 0;
-    for (int32_t idx = first; idx < n_tiles; idx += step, ++j) {
+    bool ok = true;
+    for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
       const Tile t = tile_at<GRAD>(a, start, idx, from);
       from = t.e;
-      const int b = j & 1;
       const int32_t m = t.m0 + 128 * rank + 32 * q;   // this warp's 32 channels
       const int32_t m_in = min(32, a.M - m);
       float chan = 1.f;
       if (KIND && lane < m_in) chan = a.w_scale[t.e * a.ld_scale + m + lane];
-      if (!warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status)) break;
-      tc_fence_after();
-      const uint32_t taddr = tmem + static_cast<uint32_t>(b * kTileN) + (static_cast<uint32_t>(q * 32) << 16);
-#pragma unroll 1
-      for (int32_t i = half; i < (t.valid + 31) / 32 && m_in > 0; i += 2) {
-        float v[32];
-        tmem_ld32(taddr + 32 * i, v);
-        tmem_wait_ld();
+      const int32_t in = m_in > 0 ? (t.valid + 31) / 32 : 0;
+      auto emit = [&](int32_t i, const float(&v)[32]) {   // rows 32 i .. of the tile
         __syncwarp();   // the last block's readers are done
         // lane: channel m + lane of 32 rows of Y
 #pragma unroll
@@ -742,12 +802,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int32_t r_in = min(32, t.valid - 32 * i);
         char *o = a.out[0] + (r0 * a.ldo + m) * osize;
         const float *rs = KIND ? a.x_scale + r0 : nullptr;
-        if (w16) write_block<1>(st, lane, o, a.odtype, a.ldo, r_in, m_in, rs);
+        if (!PREC && w16) write_block<1>(st, lane, o, a.odtype, a.ldo, r_in, m_in, rs);
         else write_block<0>(st, lane, o, a.odtype, a.ldo, r_in, m_in, rs);
+      };
+      const int32_t pieces = PREC ? (a.K + kChunk * kElems - 1) / (kChunk * kElems) : 1;
+      float sum[PREC ? 4 : 1][32];
+      for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
+        const int b = j & 1;
+        if (!(ok = warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status))) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem + static_cast<uint32_t>(b * kTileN) + (static_cast<uint32_t>(q * 32) << 16);
+        if (PREC && pieces > 1) {
+          read_pieces<PREC>(sum, taddr, half, in, p);
+        } else {
+#pragma unroll 1
+          for (int32_t i = half; i < in; i += 2) {
+            tmem_ld32(taddr + 32 * i, sum[0]);
+            tmem_wait_ld();
+            emit(i, sum[0]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(free0 + 8 * b);
+        if (PREC && pieces > 1 && p + 1 == pieces) {
+#pragma unroll
+          for (int g = 0; g < (PREC ? 4 : 1); ++g)
+            if (half + 2 * g < in) emit(half + 2 * g, sum[g]);
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(free0 + 8 * b);
     }
   }
   __syncwarp();
@@ -1114,9 +1197,9 @@ int sm_count() {
   return sms;
 }
 
-template <int KIND, int A_MN, int GRAD, int NMAP, int NOUT>
+template <int KIND, int A_MN, int GRAD, int PREC, int NMAP, int NOUT>
 int launch_mma(const MmaArgs<NMAP, NOUT> &a, int64_t most_tiles, cudaStream_t stream) {
-  auto kern = expert_kernel<KIND, A_MN, GRAD, NMAP, NOUT>;
+  auto kern = expert_kernel<KIND, A_MN, GRAD, NMAP, NOUT, PREC>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return HIMUON_ERR_CUDA;
   const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(most_tiles, sm_count() / 2));
@@ -1173,8 +1256,10 @@ int product_launch(const himuon_mat *X, const float *x_scale, const himuon_mat *
   a.odtype = Y->dtype;
   const int64_t mt_m = (Y->cols + kTileM - 1) / kTileM;
   const int64_t most = mt_m * (X->rows / kTileN + std::min<int64_t>(n, X->rows));
-  if (X->dtype == HIMUON_I8) return launch_mma<1, 0, 0>(a, most, stream);
-  return w_trans ? launch_mma<0, 0, 0>(a, most, stream) : launch_mma<0, 1, 0>(a, most, stream);
+  if (X->dtype == HIMUON_I8) return launch_mma<1, 0, 0, 0>(a, most, stream);
+  if (Y->dtype == HIMUON_FP32)
+    return w_trans ? launch_mma<0, 0, 0, 1>(a, most, stream) : launch_mma<0, 1, 0, 1>(a, most, stream);
+  return w_trans ? launch_mma<0, 0, 0, 0>(a, most, stream) : launch_mma<0, 1, 0, 0>(a, most, stream);
 }
 
 int run_product(const himuon_mat *X, const float *x_scale, const himuon_mat *W, const himuon_mat *w_scale, int32_t n,
@@ -1227,7 +1312,7 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
   if (C) a.cdtype = C->dtype;
   a.buffers = C ? 3 : 2;
   const int64_t most = n * ((A->cols + kTileM - 1) / kTileM) * ((B->cols + kTileN - 1) / kTileN);
-  return launch_mma<0, 1, 1>(a, most, stream);
+  return G->dtype == HIMUON_FP32 ? launch_mma<0, 1, 1, 1>(a, most, stream) : launch_mma<0, 1, 1, 0>(a, most, stream);
 }
 
 }  // namespace
