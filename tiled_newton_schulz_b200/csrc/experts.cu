@@ -77,11 +77,12 @@ struct MmaArgs {
   int *status;
   const float *x_scale, *w_scale;
   int64_t ld_scale;
-  CUtensorMap g[NOUT], c[NOUT];   // gradient: G and C in boxes of 32 rows x 32 columns
+  CUtensorMap g[NOUT], c[NOUT];   // gradient: G and C in boxes of 32 rows x box_cols columns
   char *out[NOUT];                // product: Y; gradient: G
   int64_t ldo, out_stride;        // (NOUT = 1: bytes between consecutive matrices of G)
   int32_t odtype, cdtype, has_c;
   int32_t buffers;                // of kStageOut per epilogue warp
+  int32_t box_cols;               // 32, or 64 where G and C are 16-bit
   float alpha, beta;
 };
 
@@ -294,15 +295,20 @@ __device__ __forceinline__ void write_block(const float *st, int lane, char *out
   }
 }
 
-// The gradient's epilogue buffers hold a 32 x 32 box as TMA moves it: rows of
-// 128 bytes (fp32, 128-byte swizzle) or 64 bytes (16-bit, 64-byte swizzle).
-// A lane owns a row; both patterns are free of bank conflicts.
-__device__ __forceinline__ void box_combine(const uint8_t *buf, int lane, int32_t dtype, float alpha, float beta,
-                                            float (&v)[32]) {   // v = alpha v + beta (this lane's row)
+// The gradient's epilogue buffers hold a box as TMA moves it: 32 rows of 128
+// bytes (32 columns of fp32, 64 of 16 bits; 128-byte swizzle) or of 64 bytes (32
+// columns of 16 bits; 64-byte swizzle).  A lane owns a row; both patterns are
+// free of bank conflicts.  Chunk k (16 bytes) of this lane's row:
+__device__ __forceinline__ uint32_t box_at(int lane, int k, bool wide) {
+  return wide ? lane * 128 + ((k ^ (lane & 7)) << 4) : lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4);
+}
+// v = alpha v + beta (32 columns of this lane's row, from the box's chunk k0)
+__device__ __forceinline__ void box_combine(const uint8_t *buf, int lane, int32_t dtype, int k0, bool wide, float alpha,
+                                            float beta, float (&v)[32]) {
   if (dtype == HIMUON_FP32) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float4 f = *reinterpret_cast<const float4 *>(buf + lane * 128 + ((k ^ (lane & 7)) << 4));
+      const float4 f = *reinterpret_cast<const float4 *>(buf + box_at(lane, k, true));
       v[4 * k] = fmaf(beta, f.x, alpha * v[4 * k]);
       v[4 * k + 1] = fmaf(beta, f.y, alpha * v[4 * k + 1]);
       v[4 * k + 2] = fmaf(beta, f.z, alpha * v[4 * k + 2]);
@@ -311,7 +317,7 @@ __device__ __forceinline__ void box_combine(const uint8_t *buf, int lane, int32_
   } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint4 u = *reinterpret_cast<const uint4 *>(buf + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4));
+      const uint4 u = *reinterpret_cast<const uint4 *>(buf + box_at(lane, k0 + k, wide));
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
@@ -323,16 +329,17 @@ __device__ __forceinline__ void box_combine(const uint8_t *buf, int lane, int32_
     }
   }
 }
-__device__ __forceinline__ void box_write(uint8_t *buf, int lane, int32_t dtype, const float (&v)[32]) {
+__device__ __forceinline__ void box_write(uint8_t *buf, int lane, int32_t dtype, int k0, bool wide,
+                                          const float (&v)[32]) {
   if (dtype == HIMUON_FP32) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      *reinterpret_cast<float4 *>(buf + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+      *reinterpret_cast<float4 *>(buf + box_at(lane, k, true)) =
           make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
   } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      *reinterpret_cast<uint4 *>(buf + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
+      *reinterpret_cast<uint4 *>(buf + box_at(lane, k0 + k, wide)) =
           make_uint4(pack2(dtype, v[8 * k], v[8 * k + 1]), pack2(dtype, v[8 * k + 2], v[8 * k + 3]),
                      pack2(dtype, v[8 * k + 4], v[8 * k + 5]), pack2(dtype, v[8 * k + 6], v[8 * k + 7]));
   }
@@ -502,7 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int32_t y = t.lo + k;
           const bool tail = len - k < kElems && ((len - k) & 15);
           was_tail = (was_tail & ~(1u << s)) | (static_cast<uint32_t>(tail) << s);
-          if (tail) {   // lands on this CTA's own barrier: its warp 1 has zeros to write before the MMAs
+          if (tail) {   // lands on this CTA's own barrier: its warp 2 has zeros to write before the MMAs
             tail_phase ^= 1u << s;
             if (elect_one()) {
               if (rank == 0) mbar_arrive(full + s);
@@ -553,8 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (PREC) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (rank == 0 || GRAD) {
-      const uint32_t ready0 = mapa_shared(smem_u32(tail_ready), 0);
+    if (rank == 0) {
       // descriptors of stage 0, without the address
       const uint64_t a_bits = A_MN ? sw128_desc(0, 8192, 1024) : sw128_desc(0, 16, 1024);
       const uint64_t b_bits = GRAD ? sw128_desc(0, 8192, 1024) : sw128_desc(0, 16, 1024);
@@ -576,13 +582,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         auto acquire = [&] {
           const int b = j & 1;
           d = tmem + static_cast<uint32_t>(b * kTileN);
-          if (rank != 0) return true;
           const bool free = j < 2 || warp_wait<true>(acc_empty + b, static_cast<uint32_t>(((j >> 1) - 1) & 1), a.status);
           tc_fence_after();
           return free;
         };
         auto hand_over = [&] {
-          if (rank == 0 && elect_one()) mma_commit_pair(acc_full + (j & 1), 3);
+          if (elect_one()) mma_commit_pair(acc_full + (j & 1), 3);
           __syncwarp();
           ++j;
         };
@@ -595,36 +600,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int32_t left = len - k;
           const bool fresh = PREC ? k % (kChunk * kElems) == 0 : k == 0;
           if (fresh && !(ok = acquire())) break;
-          if (rank == 0 && !(ok = warp_wait(full + s, phase, a.status))) break;
-          if (GRAD && left < kElems && (left & 15)) {
-            // the rows behind the group (other groups' or none) up to the next
-            // multiple of 16 must be zero in both operands: each is 128 bytes
-            // in every 64-column box
-            if (!(ok = warp_wait(tail_full + s, (tail_phase >> s) & 1, a.status))) break;
-            const int32_t pad = 16 - (left & 15), boxes = 2 + (t.width / 2 + 63) / 64;
-            for (int32_t i = lane; i < boxes * pad * 8; i += 32)
-              *reinterpret_cast<uint4 *>(sm + s * stage_bytes + (i / (pad * 8)) * 8192 + (left + (i / 8) % pad) * 128 +
-                                         (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (elect_one()) mbar_arrive_cluster(ready0 + 8 * s);
-            if (rank == 0 && !(ok = warp_wait<true>(tail_ready + s, (tail_phase >> s) & 1, a.status))) break;
+          if (GRAD && left < kElems && (left & 15)) {   // (`full` is completed by the producer alone)
+            if (!(ok = warp_wait<true>(tail_ready + s, (tail_phase >> s) & 1, a.status))) break;
             tail_phase ^= 1u << s;
+          } else if (!(ok = warp_wait(full + s, phase, a.status))) {
+            break;
           }
-          if (rank == 0) {
-            tc_fence_after();
-            const uint64_t ad = a_bits | (as >> 4), bd = b_bits | ((as + kABytes) >> 4);
-            if (elect_one()) {
+          tc_fence_after();
+          const uint64_t ad = a_bits | (as >> 4), bd = b_bits | ((as + kABytes) >> 4);
+          if (elect_one()) {
 #pragma unroll
-              for (int32_t kk = 0; kk < 4; ++kk) {
-                if (kk > 0 && kk * (kElems / 4) >= left) break;
-                if (KIND) mma_i8_ss_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, (!fresh || kk > 0) ? 1u : 0u);
-                else mma_ss_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, (!fresh || kk > 0) ? 1u : 0u);
-              }
-              mma_commit_pair(empty + s, 3);   // the stage is free in both CTAs once these MMAs have read it
+            for (int32_t kk = 0; kk < 4; ++kk) {
+              if (kk > 0 && kk * (kElems / 4) >= left) break;
+              if (KIND) mma_i8_ss_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, (!fresh || kk > 0) ? 1u : 0u);
+              else mma_ss_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, (!fresh || kk > 0) ? 1u : 0u);
             }
-            __syncwarp();
+            mma_commit_pair(empty + s, 3);   // the stage is free in both CTAs once these MMAs have read it
           }
+          __syncwarp();
           if (left <= kElems || (PREC && (k + kElems) % (kChunk * kElems) == 0)) hand_over();
           if (k == 0 && more) next = tile_at<GRAD>(a, start, idx + step, t.e);
           if (++s == stages) {
@@ -633,27 +626,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-    }
-    if (rank == 0) {   // nothing is in flight when the pair leaves and releases its tensor memory
+      // nothing is in flight when the pair leaves and releases its tensor memory
       if (elect_one()) mma_commit_pair(done, 1);
       __syncwarp();
       warp_wait(done, 0, a.status);
     }
   } else if (warp < 4) {
     if (PREC) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (GRAD && warp == 2) {
+      // A group's last stage when its rows are no multiple of 16: the rows
+      // behind the group (other groups' or none) up to the next multiple must
+      // be zero in both operands.  They are contiguous in each 64-column box.
+      const uint32_t ready0 = mapa_shared(smem_u32(tail_ready), 0);
+      uint32_t tail_phase = 0;
+      int s = 0;
+      for (int32_t idx = first; idx < n_tiles; idx += step) {
+        const Tile t = tile_at<GRAD>(a, start, idx, 0);
+        const int32_t len = t.hi - t.lo, left = len % kElems;
+        if (left & 15) {
+          const int st = (s + len / kElems) % stages;
+          if (!warp_wait(tail_full + st, (tail_phase >> st) & 1, a.status)) break;
+          tail_phase ^= 1u << st;
+          const int32_t boxes = 2 + (t.width / 2 + 63) / 64;
+          uint8_t *from = sm + st * stage_bytes + left * 128;
+          for (int32_t x = 0; x < boxes; ++x)
+            for (int32_t i = lane * 16; i < (16 - (left & 15)) * 128; i += 512)
+              *reinterpret_cast<uint4 *>(from + x * 8192 + i) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (elect_one()) mbar_arrive_cluster(ready0 + 8 * st);
+        }
+        s = (s + (len + kElems - 1) / kElems) % stages;
+      }
+    }
   } else if (GRAD) {
     if (PREC) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    // This warp's boxes of G, 32 rows x 32 columns, in the order of its tiles
+    // This warp's boxes of G, 32 rows x 32 or 64 columns, in the order of its tiles
     // and, inside one, of the columns.  With C, the boxes of C come by TMA up
     // to two ahead of the one at work, also from the next tile, and the result
     // takes their place: three buffers, so that a buffer is loaded again one
     // box after its store was issued.
     const int q = warp & 3;             // TMEM lanes 32 q .. 32 q + 31
-    const int half = (warp - 4) >> 2;   // the warp's 32-column groups: half, half + 2, ..
+    const int half = (warp - 4) >> 2;   // the warp's column groups: half, half + 2, ..
+    const int32_t bc = PREC ? 32 : a.box_cols;
     uint8_t *buf = sm + ring + (warp - 4) * a.buffers * kStageOut;
     uint64_t *landed = c_full + 3 * (warp - 4);
     const uint32_t free0 = mapa_shared(smem_u32(acc_empty), 0);
-    const uint32_t c_bytes = a.cdtype == HIMUON_FP32 ? 4096 : 2048;
+    const uint32_t c_bytes = bc * (a.cdtype == HIMUON_FP32 ? 128 : 64);
     // A box that reaches over the last column is stored up to the end of that
     // column's 16 bytes (observed: columns behind it in the row's pitch were
     // overwritten); where G's width is no multiple of 16 bytes the last boxes
@@ -664,7 +683,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       Tile t;
     };
     auto groups = [&](const Tile &t) {   // of this tile that are inside G
-      return t.m0 + 128 * rank + 32 * q < a.M ? (t.valid + 31) / 32 : 0;
+      return t.m0 + 128 * rank + 32 * q < a.M ? (t.valid + bc - 1) / bc : 0;
     };
     auto settle = [&](Box &x) {   // to the first box at or after (idx, i)
       while (x.idx < n_tiles && x.i >= groups(x.t)) {
@@ -677,7 +696,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (x.idx >= n_tiles) return;
       if (elect_one()) {
         mbar_arrive_expect_tx(landed + at, c_bytes);
-        tma_load_3d(buf + at * kStageOut, NOUT > 1 ? &a.c[x.t.e] : &a.c[0], x.t.n0 + 32 * x.i,
+        tma_load_3d(buf + at * kStageOut, NOUT > 1 ? &a.c[x.t.e] : &a.c[0], x.t.n0 + bc * x.i,
                     x.t.m0 + 128 * rank + 32 * q, NOUT > 1 ? 0 : x.t.e, landed + at);
       }
       __syncwarp();
@@ -698,33 +717,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
       const Tile t = tile_at<GRAD>(a, start, idx, 0);
       const int32_t in = groups(t);
-      auto emit = [&](int32_t i, float(&v)[32]) {   // column group i: combine with C, store
+      // column group i: combine with C, store.  fetch(h, v): its 32-column
+      // part h from the accumulator or the running sums.
+      auto emit = [&](int32_t i, auto fetch) {
+        const int32_t m = t.m0 + 128 * rank + 32 * q, n0 = t.n0 + bc * i;
+        const bool by_box = n0 + bc <= a.N || whole_runs;
+        uint8_t *box = buf + at * kStageOut;
+        float v[32];
+        fetch(0, v);
         if (a.has_c) {
           if (!(ok = warp_wait(landed + at, (c_phase >> at) & 1, a.status))) return;
           c_phase ^= 1u << at;
-          box_combine(buf + at * kStageOut, lane, a.cdtype, a.alpha, a.beta, v);
         } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] *= a.alpha;
           if (elect_one()) bulk_wait_read<1>();   // two buffers: the store before the last has read this one
+          __syncwarp();
         }
-        __syncwarp();
-        const int32_t m = t.m0 + 128 * rank + 32 * q, n0 = t.n0 + 32 * i;
-        const bool by_box = n0 + 32 <= a.N || whole_runs;
-        if (by_box) {
-          box_write(buf + at * kStageOut, lane, a.odtype, v);
-          fence_proxy_async_smem();
-        } else if (m + lane < a.M) {
-          char *o = (NOUT > 1 ? a.out[t.e] : a.out[0] + t.e * a.out_stride);
-          const int64_t at0 = (m + lane) * a.ldo + n0;
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (n0 + k < a.N) st_any(o, a.odtype, at0 + k, v[k]);
+        for (int h = 0; h < (PREC ? 1 : 2); ++h) {
+          if (32 * h >= bc) break;
+          if (h > 0) fetch(h, v);
+          if (a.has_c) {
+            box_combine(box, lane, a.cdtype, 4 * h, bc == 64, a.alpha, a.beta, v);
+            if (bc == 32) __syncwarp();   // (G's rows may lie where C's of other lanes did)
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] *= a.alpha;
+          }
+          if (by_box) {
+            box_write(box, lane, a.odtype, 4 * h, bc == 64, v);
+          } else if (m + lane < a.M) {
+            char *o = (NOUT > 1 ? a.out[t.e] : a.out[0] + t.e * a.out_stride);
+            const int64_t at0 = (m + lane) * a.ldo + n0 + 32 * h;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (n0 + 32 * h + k < a.N) st_any(o, a.odtype, at0 + k, v[k]);
+          }
         }
+        fence_proxy_async_smem();
         __syncwarp();
         if (elect_one()) {
-          if (by_box)
-            tma_store_3d(NOUT > 1 ? &a.g[t.e] : &a.g[0], buf + at * kStageOut, n0, m, NOUT > 1 ? 0 : t.e);
+          if (by_box) tma_store_3d(NOUT > 1 ? &a.g[t.e] : &a.g[0], box, n0, m, NOUT > 1 ? 0 : t.e);
           bulk_commit();
           if (a.has_c) bulk_wait_read<1>();   // the store of the box before has read its buffer
         }
@@ -750,19 +782,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (p + 1 == pieces) {
 #pragma unroll
             for (int g = 0; g < (PREC ? 4 : 1); ++g)
-              if (half + 2 * g < in && ok) emit(half + 2 * g, sum[g]);
+              if (half + 2 * g < in && ok)
+                emit(half + 2 * g, [&](int, float(&v)[32]) {
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) v[k] = sum[g][k];
+                });
           }
         } else {
           for (int32_t i = half; i < in && ok; i += 2) {
-            if (t.hi == t.lo) {
+            emit(i, [&](int h, float(&v)[32]) {
+              if (t.hi == t.lo) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) sum[0][k] = 0.f;
-            } else {
-              tmem_ld32(taddr + 32 * i, sum[0]);
-              tmem_wait_ld();
-            }
-            if (i + 2 >= in) release();   // the accumulator is read
-            emit(i, sum[0]);
+                for (int k = 0; k < 32; ++k) v[k] = 0.f;
+              } else {
+                tmem_ld32(taddr + bc * i + 32 * h, v);
+                tmem_wait_ld();
+              }
+              if (i + 2 >= in && 32 * (h + 1) >= bc) release();   // the accumulator is read
+            });
           }
           if (in <= half) release();   // no box of this warp's in the tile
         }
@@ -1219,7 +1256,8 @@ void common_args(MmaArgs<NMAP, NOUT> &a, const int32_t *offsets, int32_t e0, int
   a.has_c = 0;
   a.ldo = a.out_stride = 0;
   a.buffers = 1;
-  a.cdtype = HIMUON_FP32;
+  a.box_cols = 0;
+  a.cdtype = HIMUON_BF16;
   a.alpha = 1.f;
   a.beta = 0.f;
 }
@@ -1301,10 +1339,11 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
   a.alpha = alpha;
   a.beta = beta;
   a.has_c = C != nullptr;
+  a.box_cols = G->dtype == HIMUON_FP32 || (C && C->dtype == HIMUON_FP32) ? 32 : 64;
   for (int32_t i = 0; i < (NOUT > 1 ? n : 1); ++i) {
-    if (!make_map(&a.g[i], G[e0 + i], NOUT > 1 ? 1 : n, g_stride, 32, 32)) return HIMUON_ERR_CUDA;
+    if (!make_map(&a.g[i], G[e0 + i], NOUT > 1 ? 1 : n, g_stride, 32, a.box_cols)) return HIMUON_ERR_CUDA;
     a.out[i] = static_cast<char *>(G[e0 + i].data);
-    if (C && !make_map(&a.c[i], C[e0 + i], NOUT > 1 ? 1 : n, c_stride, 32, 32)) return HIMUON_ERR_CUDA;
+    if (C && !make_map(&a.c[i], C[e0 + i], NOUT > 1 ? 1 : n, c_stride, 32, a.box_cols)) return HIMUON_ERR_CUDA;
   }
   a.ldo = G->ld;
   a.out_stride = g_stride;
