@@ -56,7 +56,7 @@ constexpr int kThreads = 128 + 32 * kEpiWarps;   // three warpgroups: loads and 
 // fp32 results of 16-bit operands: the tensor core's accumulator truncates at
 // every K = 16 step, which costs an fp32 result about 1e-8 of itself per step
 // (K = 1100: 1.1e-6 against 2.6e-7 for rounded fp32 sums).  Their sums are cut
-// every kChunk stages; the epilogue adds the pieces in fp32 registers.
+// every kChunk blocks of 64; the epilogue adds the pieces in fp32 registers.
 constexpr int kChunk = 8;
 constexpr uint32_t kBarBytes = 576;
 constexpr uint32_t kSmem = kData + kBarBytes + 4 * (kMaxStack + 4) + 1024;
@@ -381,7 +381,7 @@ __device__ __forceinline__ void read_pieces(float (&sum)[PREC ? 4 : 1][32], uint
 
 // KIND 0: 16-bit operands (kind::f16); 1: int8 (kind::i8).  A_MN: A is
 // MN-major (W stored K x channels; the gradient's operands).  PREC: sums in
-// pieces of kChunk stages (fp32 results).
+// pieces of kChunk blocks (fp32 results).
 //
 // A pair of CTAs (cluster of 2) works on one 256-row tile of D: each CTA holds
 // 128 of its rows (in its tensor memory) and of A's, and half of B's columns;
@@ -395,7 +395,9 @@ __device__ __forceinline__ void read_pieces(float (&sum)[PREC ? 4 : 1][32], uint
 template <int KIND, int A_MN, int GRAD, int NMAP, int NOUT, int PREC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expert_kernel(const __grid_constant__ MmaArgs<NMAP, NOUT> a) {
-  constexpr int kElems = KIND ? 128 : 64;   // K elements per stage
+  constexpr int kElems = KIND ? 128 : 64;   // K elements per block of 128 bytes
+  constexpr int kSub = GRAD ? 1 : 2;        // blocks per stage
+  constexpr int kStageK = kElems * kSub;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t ring = kData - a.buffers * kEpiWarps * kStageOut;   // (a multiple of 1024)
@@ -475,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // in flight
   const uint32_t b_bytes =
       GRAD ? (round32(min(a.N, kTileN)) / 2 + 63) / 64 * 8192u : (*widest + 31) / 32 * kBoxBytes;
-  const uint32_t stage_bytes = (kABytes + b_bytes + 1023) / 1024 * 1024;
+  const uint32_t block_bytes = (kABytes + b_bytes + 1023) / 1024 * 1024, stage_bytes = kSub * block_bytes;
   const int stages = min(static_cast<int>(ring / stage_bytes), kMaxStages);
 
   // PREC: the epilogue's running sums take 128 registers per thread: 3 x 168
@@ -501,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int32_t m0 = t.m0 + 128 * rank, n0 = t.n0 + half * rank;
       const int32_t boxes = GRAD ? (half + 63) / 64 : half / 16;
       const uint32_t bytes = kABytes + boxes * (GRAD ? 8192u : kBoxBytes);
-      for (int32_t k = 0; k < len; k += kElems) {
+      for (int32_t k = 0; k < len; k += kStageK) {
         if (!(ok = warp_wait(empty + s, phase, a.status))) break;
         uint8_t *As = sm + s * stage_bytes, *Bs = As + kABytes;
         const uint32_t bar = full0 + 8 * s;
@@ -526,21 +528,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (boxes > 1) tma_load_2d_pair(Bs + 8192, &a.x[0], n0 + 64, y, bar);
           }
         } else if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * bytes);
-          if (A_MN) {
-            tma_load_3d_pair(As, mw, m0, k, z, bar);
-            tma_load_3d_pair(As + 8192, mw, m0 + 64, k, z, bar);
-          } else {
-            tma_load_3d_pair(As, mw, k, m0, z, bar);
-          }
-          // this CTA's rows of the tile in at most four boxes, the largest first
-          int32_t at = 0;
+          const bool both = kSub > 1 && k + kElems < len;
+          if (rank == 0) mbar_arrive_expect_tx(full + s, both ? 4 * bytes : 2 * bytes);
 #pragma unroll
-          for (int32_t i = 0; i < 4; ++i)
-            if (boxes & (8 >> i)) {
-              tma_load_2d_pair(Bs + kBoxBytes * at, &a.x[i], k, n0 + 16 * at, bar);
-              at += 8 >> i;
+          for (int u = 0; u < kSub; ++u) {
+            if (u > 0 && !both) break;
+            uint8_t *Au = As + u * block_bytes, *Bu = Bs + u * block_bytes;
+            const int32_t ku = k + u * kElems;
+            if (A_MN) {
+              tma_load_3d_pair(Au, mw, m0, ku, z, bar);
+              tma_load_3d_pair(Au + 8192, mw, m0 + 64, ku, z, bar);
+            } else {
+              tma_load_3d_pair(Au, mw, ku, m0, z, bar);
             }
+            // this CTA's rows of the tile in at most four boxes, the largest first
+            int32_t at = 0;
+#pragma unroll
+            for (int32_t i = 0; i < 4; ++i)
+              if (boxes & (8 >> i)) {
+                tma_load_2d_pair(Bu + kBoxBytes * at, &a.x[i], ku, n0 + 16 * at, bar);
+                at += 8 >> i;
+              }
+          }
         }
         __syncwarp();
         if (k == 0 && more) next = tile_at<GRAD>(a, start, idx + step, t.e);
@@ -595,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!(ok = acquire())) break;
           hand_over();
         }
-        for (int32_t k = 0; k < len; k += kElems) {
+        for (int32_t k = 0; k < len; k += kStageK) {
           const uint32_t as = smem_u32(sm) + s * stage_bytes;
           const int32_t left = len - k;
           const bool fresh = PREC ? k % (kChunk * kElems) == 0 : k == 0;
@@ -610,15 +619,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint64_t ad = a_bits | (as >> 4), bd = b_bits | ((as + kABytes) >> 4);
           if (elect_one()) {
 #pragma unroll
-            for (int32_t kk = 0; kk < 4; ++kk) {
+            for (int32_t kk = 0; kk < 4 * kSub; ++kk) {
               if (kk > 0 && kk * (kElems / 4) >= left) break;
-              if (KIND) mma_i8_ss_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, (!fresh || kk > 0) ? 1u : 0u);
-              else mma_ss_pair(d, ad + kk * kStepA, bd + kk * kStepB, idesc, (!fresh || kk > 0) ? 1u : 0u);
+              const uint32_t off = (kk / 4) * (block_bytes >> 4);
+              const uint64_t au = ad + off + (kk % 4) * kStepA, bu = bd + off + (kk % 4) * kStepB;
+              if (KIND) mma_i8_ss_pair(d, au, bu, idesc, (!fresh || kk > 0) ? 1u : 0u);
+              else mma_ss_pair(d, au, bu, idesc, (!fresh || kk > 0) ? 1u : 0u);
             }
             mma_commit_pair(empty + s, 3);   // the stage is free in both CTAs once these MMAs have read it
           }
           __syncwarp();
-          if (left <= kElems || (PREC && (k + kElems) % (kChunk * kElems) == 0)) hand_over();
+          if (left <= kStageK || (PREC && (k + kStageK) % (kChunk * kElems) == 0)) hand_over();
           if (k == 0 && more) next = tile_at<GRAD>(a, start, idx + step, t.e);
           if (++s == stages) {
             s = 0;
