@@ -58,7 +58,7 @@ constexpr int kThreads = 128 + 32 * kEpiWarps;   // three warpgroups: loads and 
 // (K = 1100: 1.1e-6 against 2.6e-7 for rounded fp32 sums).  Their sums are cut
 // every kChunk blocks of 64; the epilogue adds the pieces in fp32 registers.
 constexpr int kChunk = 8;
-constexpr uint32_t kBarBytes = 576;
+constexpr uint32_t kBarBytes = 640;
 constexpr uint32_t kSmem = kData + kBarBytes + 4 * (kMaxStack + 4) + 1024;
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
@@ -236,61 +236,79 @@ __device__ __forceinline__ void ld4_any(const char *p, int32_t dtype, int64_t i,
     v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
   }
 }
-__device__ __forceinline__ uint32_t pack2(int32_t dtype, float x, float y) {
-  if (dtype == HIMUON_FP16) {
-    const __half2 h = __floats2half2_rn(x, y);
-    return *reinterpret_cast<const uint32_t *>(&h);
-  }
+// The product's output: 32 rows of Y x 32 channels, of which `rows` x `cols`
+// are inside.  A lane comes with one channel of every row and leaves with runs
+// of a row: the block is turned through the warp's buffer (16-byte chunk c of
+// line r at chunk c ^ (r & 7): free of bank conflicts both ways), so that every
+// row is written as one 64- or 128-byte run.  (A group's last rows end inside a
+// tile, where a tensor map could not stop.)
+template <typename T2>
+__device__ __forceinline__ uint32_t two16(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t two16<__half2>(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t two16<__nv_bfloat162>(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-
-// The product's output: a staged 32 x 32 block (row r's 16-byte chunk c at
-// chunk c ^ (r & 7)), `rows` x `cols` of it inside.  16-bit outputs: 4 lanes per
-// row, 8 columns each; fp32: 8 lanes per row, 4 columns each, so every row of
-// the block is written as one 64- or 128-byte run.  (A group's last rows end
-// inside a tile, where a tensor map could not stop.)
-template <int W16>
-__device__ __forceinline__ void write_block(const float *st, int lane, char *out, int32_t odtype, int64_t ldo,
-                                            int32_t rows, int32_t cols, const float *row_scale) {
-  constexpr int kLanes = W16 ? 4 : 8, kCols = W16 ? 8 : 4, kPass = W16 ? 4 : 8;
-  const int32_t col = (lane % kLanes) * kCols;
-  if (col >= cols) return;
-  const bool whole = col + kCols <= cols;
-  float scale[kPass];
-  if (row_scale) {
+// 16-bit: line k holds rows 2 k and 2 k + 1, a 32-bit word per channel.
+template <typename T2>
+__device__ __forceinline__ void put_rows16(uint32_t *st, int lane, const float (&v)[32], uint16_t *out, int64_t ldo,
+                                           int32_t rows, int32_t cols) {
+  __syncwarp();   // the last block's readers are done
 #pragma unroll
-    for (int p = 0; p < kPass; ++p) {
-      const int32_t r = lane / kLanes + p * (32 / kLanes);
-      scale[p] = r < rows ? row_scale[r] : 0.f;
+  for (int k = 0; k < 16; ++k)
+    st[k * 32 + (((lane >> 2) ^ (k & 7)) << 2) + (lane & 3)] = two16<T2>(v[2 * k], v[2 * k + 1]);
+  __syncwarp();
+  const int32_t col = (lane & 3) * 8;
+  uint16_t *o = out + (lane >> 2) * 2 * ldo + col;
+#pragma unroll
+  for (int p = 0; p < 2; ++p, o += 16 * ldo) {
+    const int k = (lane >> 2) + 8 * p;
+    const uint4 x = *reinterpret_cast<const uint4 *>(st + k * 32 + (((col >> 2) ^ (k & 7)) << 2));
+    const uint4 y = *reinterpret_cast<const uint4 *>(st + k * 32 + ((((col >> 2) + 1) ^ (k & 7)) << 2));
+    const uint4 a = make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.z, x.w, 0x5410),
+                               __byte_perm(y.x, y.y, 0x5410), __byte_perm(y.z, y.w, 0x5410));
+    const uint4 b = make_uint4(__byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x7632),
+                               __byte_perm(y.x, y.y, 0x7632), __byte_perm(y.z, y.w, 0x7632));
+    if (col + 8 <= cols) {
+      if (2 * k < rows) *reinterpret_cast<uint4 *>(o) = a;
+      if (2 * k + 1 < rows) *reinterpret_cast<uint4 *>(o + ldo) = b;
+    } else {
+      const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (col + j >= cols) break;
+        if (2 * k < rows) o[j] = static_cast<uint16_t>(wa[j / 2] >> (16 * (j & 1)));
+        if (2 * k + 1 < rows) o[ldo + j] = static_cast<uint16_t>(wb[j / 2] >> (16 * (j & 1)));
+      }
     }
   }
+}
+// fp32: line r holds row r.
+__device__ __forceinline__ void put_rows32(float *st, int lane, const float (&v)[32], float *out, int64_t ldo,
+                                           int32_t rows, int32_t cols) {
+  __syncwarp();
 #pragma unroll
-  for (int p = 0; p < kPass; ++p) {
-    const int32_t r = lane / kLanes + p * (32 / kLanes);
+  for (int k = 0; k < 32; ++k) st[k * 32 + (((lane >> 2) ^ (k & 7)) << 2) + (lane & 3)] = v[k];
+  __syncwarp();
+  const int32_t col = (lane & 7) * 4;
+  float *o = out + (lane >> 3) * ldo + col;
+#pragma unroll
+  for (int p = 0; p < 8; ++p, o += 4 * ldo) {
+    const int r = (lane >> 3) + 4 * p;
+    const float4 f = *reinterpret_cast<const float4 *>(st + r * 32 + (((col >> 2) ^ (r & 7)) << 2));
     if (r >= rows) continue;
-    float v[kCols];
-#pragma unroll
-    for (int h = 0; h < kCols; h += 4) {
-      const float4 f = *reinterpret_cast<const float4 *>(st + r * 32 + (((col + h) >> 2) ^ (r & 7)) * 4);
-      v[h] = f.x; v[h + 1] = f.y; v[h + 2] = f.z; v[h + 3] = f.w;
-    }
-    if (row_scale) {
-#pragma unroll
-      for (int j = 0; j < kCols; ++j) v[j] *= scale[p];
-    }
-    const int64_t o = r * ldo + col;
-    if (whole) {
-      if (W16)
-        *reinterpret_cast<uint4 *>(out + 2 * o) = make_uint4(pack2(odtype, v[0], v[1]), pack2(odtype, v[2], v[3]),
-                                                             pack2(odtype, v[4 % kCols], v[5 % kCols]),
-                                                             pack2(odtype, v[6 % kCols], v[7 % kCols]));
-      else
-        *reinterpret_cast<float4 *>(out + 4 * o) = make_float4(v[0], v[1], v[2], v[3]);
+    if (col + 4 <= cols) {
+      *reinterpret_cast<float4 *>(o) = f;
     } else {
+      const float w[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-      for (int j = 0; j < kCols; ++j)
-        if (col + j < cols) st_any(out, odtype, o + j, v[j]);
+      for (int j = 0; j < 4; ++j)
+        if (col + j < cols) o[j] = w[j];
     }
   }
 }
@@ -329,6 +347,14 @@ __device__ __forceinline__ void box_combine(const uint8_t *buf, int lane, int32_
     }
   }
 }
+template <typename T2>
+__device__ __forceinline__ void box_write16(uint8_t *buf, int lane, int k0, bool wide, const float (&v)[32]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    *reinterpret_cast<uint4 *>(buf + box_at(lane, k0 + k, wide)) =
+        make_uint4(two16<T2>(v[8 * k], v[8 * k + 1]), two16<T2>(v[8 * k + 2], v[8 * k + 3]),
+                   two16<T2>(v[8 * k + 4], v[8 * k + 5]), two16<T2>(v[8 * k + 6], v[8 * k + 7]));
+}
 __device__ __forceinline__ void box_write(uint8_t *buf, int lane, int32_t dtype, int k0, bool wide,
                                           const float (&v)[32]) {
   if (dtype == HIMUON_FP32) {
@@ -336,12 +362,10 @@ __device__ __forceinline__ void box_write(uint8_t *buf, int lane, int32_t dtype,
     for (int k = 0; k < 8; ++k)
       *reinterpret_cast<float4 *>(buf + box_at(lane, k, true)) =
           make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  } else if (dtype == HIMUON_FP16) {
+    box_write16<__half2>(buf, lane, k0, wide, v);
   } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      *reinterpret_cast<uint4 *>(buf + box_at(lane, k0 + k, wide)) =
-          make_uint4(pack2(dtype, v[8 * k], v[8 * k + 1]), pack2(dtype, v[8 * k + 2], v[8 * k + 3]),
-                     pack2(dtype, v[8 * k + 4], v[8 * k + 5]), pack2(dtype, v[8 * k + 6], v[8 * k + 7]));
+    box_write16<__nv_bfloat162>(buf, lane, k0, wide, v);
   }
 }
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int32_t x, int32_t y, int32_t z) {
@@ -407,7 +431,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t *tail_ready = tail_full + kMaxStages;   // even CTA: both CTAs have written the zeros
   uint64_t *acc_full = tail_ready + kMaxStages;    // [2] each CTA: accumulator b holds a finished tile
   uint64_t *acc_empty = acc_full + 2;              // [2] even CTA: accumulator b drained by both CTAs
-  uint64_t *done = acc_empty + 2;                  // even CTA: every MMA issued has completed
+  uint64_t *drained = acc_empty + 2;               // [2] odd CTA: accumulator b drained by its warps
+  uint64_t *done = drained + 2;                    // even CTA: every MMA issued has completed
   uint64_t *c_full = done + 1;                     // [3 per epilogue warp] a box of C has landed
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(c_full + 3 * kEpiWarps);
   int32_t *widest = reinterpret_cast<int32_t *>(tmem_slot + 1);
@@ -425,7 +450,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full + b, 1);
-      mbar_init(acc_empty + b, 2 * kEpiWarps);
+      mbar_init(acc_empty + b, kEpiWarps + 1);
+      mbar_init(drained + b, kEpiWarps);
     }
     mbar_init(done, 1);
     for (int i = 0; i < 3 * kEpiWarps; ++i) mbar_init(c_full + i, 1);
@@ -644,6 +670,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 4) {
     if (PREC) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 3 && rank == 1) {
+      // Passes the odd CTA's "drained" on to the even one.  An arrival there
+      // waits for the thread's earlier stores to be performed (cluster scope,
+      // 1 to 2.5 thousand cycles beside a tile's stores); the epilogue's warps
+      // arrive in their own CTA instead.
+      const uint32_t free0 = mapa_shared(smem_u32(acc_empty), 0);
+      int32_t j = 0, from = 0;
+      bool ok = true;
+      for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
+        int32_t len = a.K;
+        if (GRAD) {
+          const Tile t = tile_at<GRAD>(a, start, idx, from);
+          len = t.hi - t.lo;
+        }
+        const int32_t pieces = PREC ? max(1, (len + kChunk * kElems - 1) / (kChunk * kElems)) : 1;
+        for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
+          const int b = j & 1;
+          ok = warp_wait(drained + b, static_cast<uint32_t>((j >> 1) & 1), a.status);
+          tc_fence_after();
+          tc_fence_before();
+          if (ok && elect_one()) mbar_arrive_cluster(free0 + 8 * b);
+          __syncwarp();
+        }
+      }
+    }
     if (GRAD && warp == 2) {
       // A group's last stage when its rows are no multiple of 16: the rows
       // behind the group (other groups' or none) up to the next multiple must
@@ -682,7 +733,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int32_t bc = PREC ? 32 : a.box_cols;
     uint8_t *buf = sm + ring + (warp - 4) * a.buffers * kStageOut;
     uint64_t *landed = c_full + 3 * (warp - 4);
-    const uint32_t free0 = mapa_shared(smem_u32(acc_empty), 0);
+    uint64_t *freed = rank == 0 ? acc_empty : drained;
     const uint32_t c_bytes = bc * (a.cdtype == HIMUON_FP32 ? 128 : 64);
     // A box that reaches over the last column is stored up to the end of that
     // column's 16 bytes (observed: columns behind it in the row's pitch were
@@ -785,7 +836,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         auto release = [&] {
           tc_fence_before();
           __syncwarp();
-          if (elect_one()) mbar_arrive_cluster(free0 + 8 * b);
+          if (elect_one()) mbar_arrive(freed + b);
         };
         if (PREC && pieces > 1) {
           read_pieces<PREC>(sum, taddr, half, in, p);
@@ -825,9 +876,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int q = warp & 3;             // TMEM lanes 32 q .. 32 q + 31
     const int half = (warp - 4) >> 2;   // the warp's 32-column groups: half, half + 2, ..
     float *st = reinterpret_cast<float *>(sm + ring + (warp - 4) * kStageOut);
-    const bool w16 = a.odtype != HIMUON_FP32;
-    const int64_t osize = w16 ? 2 : 4;
-    const uint32_t free0 = mapa_shared(smem_u32(acc_empty), 0);
+    uint64_t *freed = rank == 0 ? acc_empty : drained;
     int32_t j = 0, from = 0;
     bool ok = true;
     for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
@@ -838,20 +887,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float chan = 1.f;
       if (KIND && lane < m_in) chan = a.w_scale[t.e * a.ld_scale + m + lane];
       const int32_t in = m_in > 0 ? (t.valid + 31) / 32 : 0;
-      auto emit = [&](int32_t i, const float(&v)[32]) {   // rows 32 i .. of the tile
-        __syncwarp();   // the last block's readers are done
-        // lane: channel m + lane of 32 rows of Y
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-          st[k * 32 + (((lane >> 2) ^ (k & 7)) * 4) + (lane & 3)] =
-              KIND ? static_cast<float>(__float_as_int(v[k])) * chan : v[k];
-        __syncwarp();
+      auto emit = [&](int32_t i, float(&v)[32]) {   // rows 32 i .. of the tile
         const int64_t r0 = t.n0 + 32 * i;
         const int32_t r_in = min(32, t.valid - 32 * i);
-        char *o = a.out[0] + (r0 * a.ldo + m) * osize;
-        const float *rs = KIND ? a.x_scale + r0 : nullptr;
-        if (!PREC && w16) write_block<1>(st, lane, o, a.odtype, a.ldo, r_in, m_in, rs);
-        else write_block<0>(st, lane, o, a.odtype, a.ldo, r_in, m_in, rs);
+        if (KIND) {   // int32 sums: scales of this lane's channel and of each row
+          const float mine = lane < r_in ? a.x_scale[r0 + lane] : 0.f;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            v[k] = static_cast<float>(__float_as_int(v[k])) * chan * __shfl_sync(0xffffffffu, mine, k);
+        }
+        const int64_t o = r0 * a.ldo + m;
+        if (PREC || a.odtype == HIMUON_FP32)
+          put_rows32(st, lane, v, reinterpret_cast<float *>(a.out[0]) + o, a.ldo, r_in, m_in);
+        else if (a.odtype == HIMUON_FP16)
+          put_rows16<__half2>(reinterpret_cast<uint32_t *>(st), lane, v, reinterpret_cast<uint16_t *>(a.out[0]) + o,
+                              a.ldo, r_in, m_in);
+        else
+          put_rows16<__nv_bfloat162>(reinterpret_cast<uint32_t *>(st), lane, v,
+                                     reinterpret_cast<uint16_t *>(a.out[0]) + o, a.ldo, r_in, m_in);
       };
       const int32_t pieces = PREC ? (a.K + kChunk * kElems - 1) / (kChunk * kElems) : 1;
       float sum[PREC ? 4 : 1][32];
@@ -872,7 +925,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(free0 + 8 * b);
+        if (elect_one()) mbar_arrive(freed + b);
         if (PREC && pieces > 1 && p + 1 == pieces) {
 #pragma unroll
           for (int g = 0; g < (PREC ? 4 : 1); ++g)
