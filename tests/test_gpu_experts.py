@@ -238,6 +238,42 @@ def test_product_many_tiles_per_cta_pair(hm, trans):
     check_i8(hm, torch.float32, 400, 2056, [257, 513, 1, 0, 700, 64, 31, 1025])
 
 
+@pytest.mark.parametrize("P,Q", [(520, 771), (264, 448), (768, 352), (72, 1000), (2048, 224)])
+def test_gradient_tile_widths(hm, P, Q):
+    """Sizes at which the tiles are narrower than 256 columns."""
+    check_gradient(hm, torch.bfloat16, torch.bfloat16, P, Q, [140, 7, 0, 96, 33], beta=1.0, margin=16)
+    check_gradient(hm, torch.float16, torch.float32, P, Q, [64, 7, 700])
+    check_gradient(hm, torch.float16, torch.float16, P, Q, [65, 130], cdtype=torch.float32, beta=0.5)
+
+
+@pytest.mark.parametrize("counts", [[300] * 5, [1531], [100, 180, 260, 20], [129], [193, 257], [90] * 9])
+def test_product_tile_widths(hm, counts):
+    """Row counts at which the tiles are narrower than 256 rows."""
+    check_product(hm, torch.bfloat16, torch.bfloat16, 520, 2050, counts, False)
+    check_product(hm, torch.bfloat16, torch.float32, 200, 1000, counts, True, start=7, behind=300)
+    check_i8(hm, torch.float32, 600, 520, counts, start=1, behind=300)
+
+
+@pytest.mark.parametrize("counts", [[1], [33], [200], [1, 2], [300, 0]])
+@pytest.mark.parametrize("K,N", [(2048, 264), (4100, 136), (520, 520)])
+def test_product_tiles_shared_by_pairs(hm, K, N, counts):
+    """Few tiles: their sums are cut among the pairs of a cluster, every result type."""
+    for trans in (False, True):
+        for out in TYPES.values():
+            check_product(hm, torch.bfloat16, out, K, N, counts, trans, start=2, behind=40, listed=trans)
+    check_i8(hm, torch.bfloat16, K, N, counts, start=2, behind=40)
+    check_i8(hm, torch.float32, 2 * K, N, counts, full=True)
+
+
+@pytest.mark.parametrize("counts", [[5003], [4, 2000, 0], [65], [777, 1024]])
+@pytest.mark.parametrize("P,Q", [(8, 8), (264, 136), (520, 771)])
+def test_gradient_tiles_shared_by_pairs(hm, P, Q, counts):
+    for out in TYPES.values():
+        check_gradient(hm, torch.bfloat16, out, P, Q, counts, start=3, behind=70)
+        check_gradient(hm, torch.float16, out, P, Q, counts, beta=1.0, cdtype=torch.float32, alpha=0.5, listed=True)
+    check_gradient(hm, torch.bfloat16, torch.bfloat16, P, Q, counts, beta=-1.0, alias=True, margin=8)
+
+
 def test_gradient_long_sum(hm):
     check_gradient(hm, torch.bfloat16, torch.float32, 200, 264, [5003, 1])
     check_gradient(hm, torch.bfloat16, torch.bfloat16, 64, 64, [9001])

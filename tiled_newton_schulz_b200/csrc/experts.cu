@@ -73,6 +73,9 @@ struct MmaArgs {
   int32_t n;
   int32_t K;               // product: length of the sums
   int32_t M, N;            // product: M channels; gradient: G is M x N
+  int32_t mt_m, mt_n;      // tiles along M; gradient: along N
+  int32_t cap;             // gradient: columns of a tile (a multiple of 32); product: log2 of a tile's most rows
+  int32_t split;           // pairs that share a tile's sum (the cluster's)
   uint32_t idesc;          // without the N field
   int *status;
   const float *x_scale, *w_scale;
@@ -157,14 +160,13 @@ __device__ __forceinline__ int32_t bound_at(const int32_t *offsets, int32_t i, i
   return static_cast<int32_t>(min(max((int64_t)offsets[i], (int64_t)0), rows));
 }
 
-__device__ __forceinline__ int32_t m_tiles(int32_t M) { return (M + kTileM - 1) / kTileM; }
 __device__ __forceinline__ int32_t round32(int32_t x) { return (x + 31) / 32 * 32; }
-// A group of cnt rows runs as ceil(cnt / 256) tiles of equal width (a multiple
-// of 32: the pair's CTAs hold half of the rows each, in boxes of 16).
-__device__ __forceinline__ int32_t row_tiles(int32_t cnt) { return (cnt + kTileN - 1) / kTileN; }
-__device__ __forceinline__ int32_t tile_width(int32_t cnt) {
-  const int32_t mt = row_tiles(cnt);
-  return mt == 0 ? 0 : ((cnt + mt - 1) / mt + 31) / 32 * 32;
+// A group of cnt rows runs as ceil(cnt / 2^shift) tiles of equal width (a
+// multiple of 32: the pair's CTAs hold half of the rows each, in boxes of 16).
+__device__ __forceinline__ int32_t row_tiles(int32_t cnt, int32_t shift) { return (cnt + (1 << shift) - 1) >> shift; }
+__device__ __forceinline__ int32_t tile_width(int32_t cnt, int32_t shift) {
+  const int32_t mt = row_tiles(cnt, shift);
+  return mt <= 1 ? round32(cnt) : round32((cnt + mt - 1) / mt);
 }
 
 struct Tile {
@@ -173,25 +175,24 @@ struct Tile {
   int32_t n0;       // product: first row of X; gradient: first column of G
   int32_t width;    // columns of D: a multiple of 32
   int32_t valid;    // of them, inside the output
-  int32_t lo, hi;   // the group's rows
+  int32_t k0, len;  // the sums' stretch: product, of K; gradient, rows (of the slice, where a tile is split)
 };
 
 // Tile `idx` of the launch, found by a whole warp.  `from`: a group not after
 // the tile's (the last one found: a role's tiles come in order).
-template <int GRAD, typename Args>
-__device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int32_t idx, int32_t from) {
+template <int GRAD, int SPLIT, int kElems, typename Args>
+__device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int32_t slice, int32_t idx, int32_t from) {
   Tile t;
-  const int32_t mt_m = m_tiles(a.M);
+  const int32_t mt_m = a.mt_m;
   if (GRAD) {
-    const int32_t mt_n = (a.N + kTileN - 1) / kTileN;
-    t.e = idx / (mt_m * mt_n);
-    const int32_t r = idx - t.e * mt_m * mt_n;
-    t.m0 = (r % mt_m) * kTileM;
-    t.n0 = (r / mt_m) * kTileN;
-    t.valid = min(kTileN, a.N - t.n0);
+    const int32_t u = idx / mt_m;
+    t.e = u / a.mt_n;
+    t.m0 = (idx - u * mt_m) * kTileM;
+    t.n0 = (u - t.e * a.mt_n) * a.cap;
+    t.valid = min(a.cap, a.N - t.n0);
     t.width = round32(t.valid);
-    t.lo = bound_at(a.offsets, t.e, a.rows);
-    t.hi = max(t.lo, bound_at(a.offsets, t.e + 1, a.rows));
+    t.k0 = bound_at(a.offsets, t.e, a.rows);
+    t.len = max(0, bound_at(a.offsets, t.e + 1, a.rows) - t.k0);
   } else {
     // the group whose row tiles hold row tile idx / mt_m: the last with start[e] <= it
     const int32_t u = idx / mt_m, lane = threadIdx.x & 31;
@@ -202,19 +203,26 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int
         break;
       }
     }
-    t.lo = bound_at(a.offsets, t.e, a.rows);
-    t.hi = max(t.lo, bound_at(a.offsets, t.e + 1, a.rows));
-    const int32_t cnt = t.hi - t.lo, mt = row_tiles(cnt);
-    t.width = tile_width(cnt);
+    const int32_t lo = bound_at(a.offsets, t.e, a.rows), hi = max(lo, bound_at(a.offsets, t.e + 1, a.rows));
+    const int32_t cnt = hi - lo, mt = row_tiles(cnt, a.cap);
+    t.width = tile_width(cnt, a.cap);
     // bands of up to 8 row tiles, row tile fastest: the tiles in flight share
     // a few panels of W and of X
     const int32_t r = idx - start[t.e] * mt_m;
-    const int32_t g = r / (8 * mt_m), rr = r % (8 * mt_m);
-    const int32_t gm = min(8, mt - 8 * g);
-    const int32_t tt = 8 * g + rr % gm;
-    t.m0 = (rr / gm) * kTileM;
-    t.n0 = t.lo + tt * t.width;
-    t.valid = min(t.width, t.hi - t.n0);
+    const int32_t g = mt <= 8 ? 0 : r / (8 * mt_m), rr = r - g * 8 * mt_m;
+    const int32_t gm = min(8, mt - 8 * g), mc = gm == 1 ? rr : rr / gm;
+    const int32_t tt = 8 * g + rr - mc * gm;
+    t.m0 = mc * kTileM;
+    t.n0 = lo + tt * t.width;
+    t.valid = min(t.width, hi - t.n0);
+    t.k0 = 0;
+    t.len = a.K;
+  }
+  if (SPLIT) {   // this pair's blocks of the sum
+    const int32_t nb = (t.len + kElems - 1) / kElems;
+    const int32_t b0 = nb * slice / a.split, b1 = nb * (slice + 1) / a.split;
+    t.k0 += b0 * kElems;
+    t.len = min(t.len, b1 * kElems) - b0 * kElems;
   }
   return t;
 }
@@ -378,16 +386,76 @@ __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
+// Reports offsets that decrease or leave 0 .. rows (a whole warp).
+template <typename Args>
+__device__ __forceinline__ void check_offsets(const Args &a, int lane) {
+  if (!a.offsets) return;
+  for (int32_t e = lane; e < a.n; e += 32)
+    if (a.offsets[e] < 0 || a.offsets[e + 1] < a.offsets[e] || a.offsets[e + 1] > a.rows)
+      set_status(a.status, HIMUON_ERR_DEVICE);
+}
+
+// The product's tiles, from the groups' bounds (a whole warp): start[e], the
+// row tiles of the groups before e, and the widest tile.
+template <typename Args>
+__device__ __forceinline__ void plan_rows(const Args &a, int32_t *start, int32_t *widest, int lane) {
+  constexpr int kPer = kMaxStack / 32;
+  int32_t cnt[kPer];   // of group lane + 32 i; all loads in flight together
+  {
+    int32_t o[kPer + 1];
+#pragma unroll
+    for (int i = 0; i <= kPer; ++i) {
+      const int32_t e = lane + 32 * i;
+      o[i] = e > a.n ? 0 : a.offsets ? a.offsets[e] : e == 0 ? 0 : static_cast<int32_t>(a.rows);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      cnt[i] = 0;
+      if (32 * i >= a.n) continue;
+      const int32_t e = lane + 32 * i;
+      const int32_t down = __shfl_down_sync(0xffffffffu, o[i], 1), over = __shfl_sync(0xffffffffu, o[i + 1], 0);
+      const int64_t lo = o[i], hi = lane == 31 ? over : down;
+      if (e < a.n) {
+        if (lo < 0 || hi < lo || hi > a.rows) set_status(a.status, HIMUON_ERR_DEVICE);
+        const int64_t first = min(max(lo, (int64_t)0), a.rows), last = min(max(hi, (int64_t)0), a.rows);
+        cnt[i] = static_cast<int32_t>(max(last - first, (int64_t)0));
+      }
+    }
+  }
+  int32_t base = 0, w = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (32 * i >= a.n) break;
+    w = max(w, tile_width(cnt[i], a.cap));
+    int32_t s = row_tiles(cnt[i], a.cap);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t up = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += up;
+    }
+    if (lane + 32 * i < a.n) start[lane + 32 * i + 1] = base + s;
+    base += __shfl_sync(0xffffffffu, s, 31);
+  }
+  w = __reduce_max_sync(0xffffffffu, w);
+  if (lane == 0) {
+    start[0] = 0;
+    *widest = w;
+  }
+}
+
 // PREC: an epilogue warp's column groups half, half + 2, .. (below `in`) of
 // accumulator piece p, added to its running sums.
 template <int PREC>
 __device__ __forceinline__ void read_pieces(float (&sum)[PREC ? 4 : 1][32], uint32_t taddr, int half, int32_t in,
-                                            int32_t p) {
+                                            int32_t p, bool none) {
 #pragma unroll
   for (int g = 0; g < (PREC ? 4 : 1); ++g) {
     const int32_t i = half + 2 * g;
     if (i >= in) continue;
-    if (p == 0) {
+    if (none) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) sum[g][k] = 0.f;
+    } else if (p == 0) {
       tmem_ld32(taddr + 32 * i, sum[g]);
       tmem_wait_ld();
     } else {
@@ -403,9 +471,61 @@ __device__ __forceinline__ void read_pieces(float (&sum)[PREC ? 4 : 1][32], uint
   }
 }
 
+// SPLIT: adds up the slices' sums of a tile.  Column group g of a warp belongs
+// to the pair g % split; every other pair's warp sends it its part over
+// distributed shared memory, into the ring (free by then: the first cluster
+// barrier follows every pair's last MMA), and the owner adds the parts in the
+// order of the slices, whatever their order of arrival.  4 KB per part: chunk k
+// (16 bytes) of lane l at k * 512 + 16 l.
+template <int KIND, int PREC>
+__device__ __forceinline__ void join_slices(float (&sum)[PREC ? 4 : 1][32], uint8_t *ring, int w, int lane, int half,
+                                            int32_t in, int32_t rank, int32_t slice, int32_t split) {
+  const int per = 4 / split;   // groups that a warp owns
+  __syncwarp();
+  cluster_sync_all();
+#pragma unroll
+  for (int g = 0; g < (PREC ? 4 : 1); ++g) {
+    const int owner = g % split;
+    if (half + 2 * g >= in || owner == slice) continue;
+    const uint32_t to =
+        mapa_shared(smem_u32(ring + ((slice * per + g / split) * kEpiWarps + w) * kStageOut), 2 * owner + rank) + 16 * lane;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      st_cluster_v4(to + 512 * k, make_uint4(__float_as_uint(sum[g][4 * k]), __float_as_uint(sum[g][4 * k + 1]),
+                                             __float_as_uint(sum[g][4 * k + 2]), __float_as_uint(sum[g][4 * k + 3])));
+  }
+  __syncwarp();
+  cluster_sync_all();
+#pragma unroll
+  for (int g = 0; g < (PREC ? 4 : 1); ++g) {
+    if (half + 2 * g >= in || g % split != slice) continue;
+    float total[32];
+    for (int from = 0; from < split; ++from) {
+      const uint8_t *part = ring + ((from * per + g / split) * kEpiWarps + w) * kStageOut + 16 * lane;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float4 f = from == slice ? make_float4(sum[g][4 * k], sum[g][4 * k + 1], sum[g][4 * k + 2], sum[g][4 * k + 3])
+                                       : *reinterpret_cast<const float4 *>(part + 512 * k);
+        const float x[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float &t = total[4 * k + c];
+          if (from == 0) t = x[c];
+          else if (KIND) t = __int_as_float(__float_as_int(t) + __float_as_int(x[c]));
+          else t += x[c];
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k) sum[g][k] = total[k];
+  }
+}
+
 // KIND 0: 16-bit operands (kind::f16); 1: int8 (kind::i8).  A_MN: A is
 // MN-major (W stored K x channels; the gradient's operands).  PREC: sums in
 // pieces of kChunk blocks (fp32 results).
+// SPLIT: the cluster's pairs share one tile, each a stretch of its sum (calls of
+// few tiles); comes with PREC's running sums in registers.
 //
 // A pair of CTAs (cluster of 2) works on one 256-row tile of D: each CTA holds
 // 128 of its rows (in its tensor memory) and of A's, and half of B's columns;
@@ -416,8 +536,8 @@ __device__ __forceinline__ void read_pieces(float (&sum)[PREC ? 4 : 1][32], uint
 // completing on the even CTA's barriers), warp 1 of the even CTA issues each
 // tile's MMAs into one of two accumulators, warps 4..11 of both drain the other
 // one meanwhile.
-template <int KIND, int A_MN, int GRAD, int NMAP, int NOUT, int PREC>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <int KIND, int A_MN, int GRAD, int NMAP, int NOUT, int PREC, int SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
     expert_kernel(const __grid_constant__ MmaArgs<NMAP, NOUT> a) {
   constexpr int kElems = KIND ? 128 : 64;   // K elements per block of 128 bytes
   constexpr int kSub = GRAD ? 1 : 2;        // blocks per stage
@@ -435,74 +555,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t *done = drained + 2;                    // even CTA: every MMA issued has completed
   uint64_t *c_full = done + 1;                     // [3 per epilogue warp] a box of C has landed
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(c_full + 3 * kEpiWarps);
-  int32_t *widest = reinterpret_cast<int32_t *>(tmem_slot + 1);
+  int32_t *widest = reinterpret_cast<int32_t *>(tmem_slot + 1);   // product: columns of the widest tile
   int32_t *start = reinterpret_cast<int32_t *>(sm + kData + kBarBytes);   // [n + 1]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t rank = static_cast<int32_t>(cluster_ctarank());
-  const int32_t first = static_cast<int32_t>(blockIdx.x >> 1), step = static_cast<int32_t>(gridDim.x >> 1);
+  constexpr bool kPieces = PREC && !KIND;   // (int32 sums are exact)
+  const int32_t cta = static_cast<int32_t>(cluster_ctarank());
+  const int32_t rank = cta & 1, even = cta & ~1, slice = SPLIT ? cta >> 1 : 0;
+  const uint16_t pair_mask = static_cast<uint16_t>(3u << even);
+  const int32_t ctas = SPLIT ? 2 * a.split : 2;
+  const int32_t first = static_cast<int32_t>(blockIdx.x) / ctas, step = static_cast<int32_t>(gridDim.x) / ctas;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(full + s, 1);
-      mbar_init(empty + s, 1);
-      mbar_init(tail_full + s, 1);
-      mbar_init(tail_ready + s, 2);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(acc_full + b, 1);
-      mbar_init(acc_empty + b, kEpiWarps + 1);
-      mbar_init(drained + b, kEpiWarps);
-    }
-    mbar_init(done, 1);
-    for (int i = 0; i < 3 * kEpiWarps; ++i) mbar_init(c_full + i, 1);
+  if (warp == 0) {
+    // one barrier per lane and round: full, empty, tail_full, tail_ready, acc_full, acc_empty, drained, done, c_full
+    constexpr int kBars = 4 * kMaxStages + 7 + 3 * kEpiWarps, kAcc = 4 * kMaxStages;
+    for (int i = lane; i < kBars; i += 32)
+      mbar_init(full + i, i >= 3 * kMaxStages && i < kAcc     ? 2
+                          : i >= kAcc + 2 && i < kAcc + 4     ? kEpiWarps + 1
+                          : i >= kAcc + 4 && i < kAcc + 6     ? kEpiWarps
+                                                              : 1);
     fence_mbar_init();
-    tma_prefetch_desc(&a.x[0]);
+    if (lane == 0) tma_prefetch_desc(&a.x[0]);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
   }
-  if (warp == 2) {
-    // start[e]: row tiles of the groups before e; widest: the widest tile
-    int32_t base = 0, w = 0;
-    for (int32_t e0 = 0; e0 < a.n; e0 += 32) {
-      const int32_t e = e0 + lane;
-      int32_t cnt = 0;
-      if (e < a.n) {
-        const int32_t lo = bound_at(a.offsets, e, a.rows), hi = bound_at(a.offsets, e + 1, a.rows);
-        cnt = max(hi - lo, 0);
-        if (a.offsets && (a.offsets[e] < 0 || a.offsets[e + 1] < a.offsets[e] || a.offsets[e + 1] > a.rows))
-          set_status(a.status, HIMUON_ERR_DEVICE);
-      }
-      w = max(w, tile_width(cnt));
-      int32_t s = row_tiles(cnt);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int32_t up = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += up;
-      }
-      if (e < a.n) start[e + 1] = base + s;
-      base += __shfl_sync(0xffffffffu, s, 31);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) w = max(w, __shfl_xor_sync(0xffffffffu, w, o));
-    if (lane == 0) {
-      start[0] = 0;
-      *widest = w;
-    }
-  }
+  if (!GRAD && warp == 2) plan_rows(a, start, widest, lane);
+  if (GRAD && warp == 2) check_offsets(a, lane);
   __syncwarp();
   tc_fence_before();
   cluster_sync_all();   // barriers of both CTAs are ready before either is signalled
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int32_t mt_m = m_tiles(a.M);
-  const int32_t n_tiles = GRAD ? a.n * mt_m * ((a.N + kTileN - 1) / kTileN) : start[a.n] * mt_m;
+  const int32_t all_tiles = (GRAD ? a.n * a.mt_n : start[a.n]) * a.mt_m;
+  const int32_t n_tiles = SPLIT ? min(all_tiles, step) : all_tiles;   // (split: one tile per cluster)
   // a stage holds 128 rows of A and half of the widest tile's columns of B;
   // narrow tiles (few rows per expert) get more stages, so that enough of W is
   // in flight
   const uint32_t b_bytes =
-      GRAD ? (round32(min(a.N, kTileN)) / 2 + 63) / 64 * 8192u : (*widest + 31) / 32 * kBoxBytes;
+      GRAD ? (a.cap / 2 + 63) / 64 * 8192u : (*widest + 31) / 32 * kBoxBytes;
   const uint32_t block_bytes = (kABytes + b_bytes + 1023) / 1024 * 1024, stage_bytes = kSub * block_bytes;
   const int stages = min(static_cast<int>(ring / stage_bytes), kMaxStages);
 
@@ -510,19 +601,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // per thread of the three warpgroups become 56 + 2 x 224
   if (warp == 0) {
     if (PREC) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+    const uint32_t full0 = mapa_shared(smem_u32(full), even);
     int s = 0;
     uint32_t phase = 1;   // parity of the stage's last release; the first round finds it free
     bool ok = true;
     int64_t issued = 0;
     uint32_t was_tail = 0, tail_phase = 0;   // per stage: its last block's kind; tail_full's next parity
     Tile t, next;
-    if (first < n_tiles) next = tile_at<GRAD>(a, start, first, 0);
+    if (first < n_tiles) next = tile_at<GRAD, SPLIT, kElems>(a, start, slice, first, 0);
     for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
       t = next;
       const bool more = idx + step < n_tiles;   // the next tile is looked up behind this one's first block
-      if (more && (GRAD && t.hi == t.lo)) next = tile_at<GRAD>(a, start, idx + step, t.e);
-      const int32_t len = GRAD ? t.hi - t.lo : a.K;
+      if (more && t.len == 0) next = tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx + step, t.e);
+      const int32_t len = t.len;
       const CUtensorMap *mw = NMAP > 1 ? &a.w[t.e] : &a.w[0];
       const int32_t z = NMAP > 1 ? 0 : t.e;
       const int32_t half = t.width / 2;
@@ -534,7 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint8_t *As = sm + s * stage_bytes, *Bs = As + kABytes;
         const uint32_t bar = full0 + 8 * s;
         if (GRAD) {
-          const int32_t y = t.lo + k;
+          const int32_t y = t.k0 + k;
           const bool tail = len - k < kElems && ((len - k) & 15);
           was_tail = (was_tail & ~(1u << s)) | (static_cast<uint32_t>(tail) << s);
           if (tail) {   // lands on this CTA's own barrier: its warp 2 has zeros to write before the MMAs
@@ -560,7 +651,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int u = 0; u < kSub; ++u) {
             if (u > 0 && !both) break;
             uint8_t *Au = As + u * block_bytes, *Bu = Bs + u * block_bytes;
-            const int32_t ku = k + u * kElems;
+            const int32_t ku = t.k0 + k + u * kElems;
             if (A_MN) {
               tma_load_3d_pair(Au, mw, m0, ku, z, bar);
               tma_load_3d_pair(Au + 8192, mw, m0 + 64, ku, z, bar);
@@ -578,7 +669,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-        if (k == 0 && more) next = tile_at<GRAD>(a, start, idx + step, t.e);
+        if (k == 0 && more) next = tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx + step, t.e);
         ++issued;
         if (++s == stages) {
           s = 0;
@@ -605,12 +696,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int32_t j = 0;
       bool ok = true;
       Tile t, next;
-      if (first < n_tiles) next = tile_at<GRAD>(a, start, first, 0);
+      if (first < n_tiles) next = tile_at<GRAD, SPLIT, kElems>(a, start, slice, first, 0);
       for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
         t = next;
         const bool more = idx + step < n_tiles;
-        if (more && (GRAD && t.hi == t.lo)) next = tile_at<GRAD>(a, start, idx + step, t.e);
-        const int32_t len = GRAD ? t.hi - t.lo : a.K;
+        if (more && t.len == 0) next = tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx + step, t.e);
+        const int32_t len = t.len;
         const uint32_t idesc = a.idesc | (static_cast<uint32_t>(t.width >> 3) << 17);
         uint32_t d = 0;
         // the next accumulator, once the epilogue has drained it
@@ -622,18 +713,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           return free;
         };
         auto hand_over = [&] {
-          if (elect_one()) mma_commit_pair(acc_full + (j & 1), 3);
+          if (elect_one()) mma_commit_pair(acc_full + (j & 1), pair_mask);
           __syncwarp();
           ++j;
         };
-        if (GRAD && len == 0) {
+        if (len == 0) {
           if (!(ok = acquire())) break;
           hand_over();
         }
         for (int32_t k = 0; k < len; k += kStageK) {
           const uint32_t as = smem_u32(sm) + s * stage_bytes;
           const int32_t left = len - k;
-          const bool fresh = PREC ? k % (kChunk * kElems) == 0 : k == 0;
+          const bool fresh = kPieces ? k % (kChunk * kElems) == 0 : k == 0;
           if (fresh && !(ok = acquire())) break;
           if (GRAD && left < kElems && (left & 15)) {   // (`full` is completed by the producer alone)
             if (!(ok = warp_wait<true>(tail_ready + s, (tail_phase >> s) & 1, a.status))) break;
@@ -642,7 +733,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint64_t ad = a_bits | (as >> 4), bd = b_bits | ((as + kABytes) >> 4);
+          // (a shared-memory address carries the CTA's rank above the descriptor's field)
+          const uint64_t ad = a_bits | ((as >> 4) & 0x3FFF), bd = b_bits | (((as + kABytes) >> 4) & 0x3FFF);
           if (elect_one()) {
 #pragma unroll
             for (int32_t kk = 0; kk < 4 * kSub; ++kk) {
@@ -652,11 +744,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (KIND) mma_i8_ss_pair(d, au, bu, idesc, (!fresh || kk > 0) ? 1u : 0u);
               else mma_ss_pair(d, au, bu, idesc, (!fresh || kk > 0) ? 1u : 0u);
             }
-            mma_commit_pair(empty + s, 3);   // the stage is free in both CTAs once these MMAs have read it
+            mma_commit_pair(empty + s, pair_mask);   // the stage is free in both CTAs once these MMAs have read it
           }
           __syncwarp();
-          if (left <= kStageK || (PREC && (k + kStageK) % (kChunk * kElems) == 0)) hand_over();
-          if (k == 0 && more) next = tile_at<GRAD>(a, start, idx + step, t.e);
+          if (left <= kStageK || (kPieces && (k + kStageK) % (kChunk * kElems) == 0)) hand_over();
+          if (k == 0 && more) next = tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx + step, t.e);
           if (++s == stages) {
             s = 0;
             phase ^= 1;
@@ -664,7 +756,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       // nothing is in flight when the pair leaves and releases its tensor memory
-      if (elect_one()) mma_commit_pair(done, 1);
+      if (elect_one()) mma_commit_pair(done, static_cast<uint16_t>(1u << even));
       __syncwarp();
       warp_wait(done, 0, a.status);
     }
@@ -675,16 +767,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // waits for the thread's earlier stores to be performed (cluster scope,
       // 1 to 2.5 thousand cycles beside a tile's stores); the epilogue's warps
       // arrive in their own CTA instead.
-      const uint32_t free0 = mapa_shared(smem_u32(acc_empty), 0);
-      int32_t j = 0, from = 0;
+      const uint32_t free0 = mapa_shared(smem_u32(acc_empty), even);
+      const int32_t from = 0;
+      int32_t j = 0;
       bool ok = true;
       for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
-        int32_t len = a.K;
-        if (GRAD) {
-          const Tile t = tile_at<GRAD>(a, start, idx, from);
-          len = t.hi - t.lo;
-        }
-        const int32_t pieces = PREC ? max(1, (len + kChunk * kElems - 1) / (kChunk * kElems)) : 1;
+        const int32_t len = GRAD || SPLIT ? tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx, from).len : a.K;
+        const int32_t pieces = kPieces ? max(1, (len + kChunk * kElems - 1) / (kChunk * kElems)) : 1;
         for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
           const int b = j & 1;
           ok = warp_wait(drained + b, static_cast<uint32_t>((j >> 1) & 1), a.status);
@@ -699,12 +788,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // A group's last stage when its rows are no multiple of 16: the rows
       // behind the group (other groups' or none) up to the next multiple must
       // be zero in both operands.  They are contiguous in each 64-column box.
-      const uint32_t ready0 = mapa_shared(smem_u32(tail_ready), 0);
+      const uint32_t ready0 = mapa_shared(smem_u32(tail_ready), even);
       uint32_t tail_phase = 0;
       int s = 0;
       for (int32_t idx = first; idx < n_tiles; idx += step) {
-        const Tile t = tile_at<GRAD>(a, start, idx, 0);
-        const int32_t len = t.hi - t.lo, left = len % kElems;
+        const Tile t = tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx, 0);
+        const int32_t len = t.len, left = len % kElems;
         if (left & 15) {
           const int st = (s + len / kElems) % stages;
           if (!warp_wait(tail_full + st, (tail_phase >> st) & 1, a.status)) break;
@@ -729,7 +818,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // takes their place: three buffers, so that a buffer is loaded again one
     // box after its store was issued.
     const int q = warp & 3;             // TMEM lanes 32 q .. 32 q + 31
-    const int half = (warp - 4) >> 2;   // the warp's column groups: half, half + 2, ..
+    const int half = (warp - 4) >> 2;   // the warp's column groups: half, half + 2, .. (split: its slice's)
+    const int32_t i0 = SPLIT ? half + 2 * slice : half, di = SPLIT ? 2 * a.split : 2;
     const int32_t bc = PREC ? 32 : a.box_cols;
     uint8_t *buf = sm + ring + (warp - 4) * a.buffers * kStageOut;
     uint64_t *landed = c_full + 3 * (warp - 4);
@@ -750,8 +840,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto settle = [&](Box &x) {   // to the first box at or after (idx, i)
       while (x.idx < n_tiles && x.i >= groups(x.t)) {
         x.idx += step;
-        x.i = half;
-        if (x.idx < n_tiles) x.t = tile_at<GRAD>(a, start, x.idx, 0);
+        x.i = i0;
+        if (x.idx < n_tiles) x.t = tile_at<GRAD, SPLIT, kElems>(a, start, slice, x.idx, 0);
       }
     };
     auto load_c = [&](Box &x, int at) {   // box x into buffer `at`, then on to the next box
@@ -762,12 +852,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     x.t.m0 + 128 * rank + 32 * q, NOUT > 1 ? 0 : x.t.e, landed + at);
       }
       __syncwarp();
-      x.i += 2;
+      x.i += di;
       settle(x);
     };
-    Box ahead{first, half, {}};
+    Box ahead{first, i0, {}};
     if (a.has_c && first < n_tiles) {
-      ahead.t = tile_at<GRAD>(a, start, first, 0);
+      ahead.t = tile_at<GRAD, SPLIT, kElems>(a, start, slice, first, 0);
       settle(ahead);
       load_c(ahead, 0);
       load_c(ahead, 1);
@@ -777,7 +867,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     int32_t j = 0;
     for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
-      const Tile t = tile_at<GRAD>(a, start, idx, 0);
+      const Tile t = tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx, 0);
       const int32_t in = groups(t);
       // column group i: combine with C, store.  fetch(h, v): its 32-column
       // part h from the accumulator or the running sums.
@@ -826,7 +916,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (a.has_c) load_c(ahead, at == 0 ? 2 : at - 1);
         at = at + 1 == a.buffers ? 0 : at + 1;
       };
-      const int32_t pieces = PREC ? max(1, (t.hi - t.lo + kChunk * kElems - 1) / (kChunk * kElems)) : 1;
+      const int32_t pieces = kPieces ? max(1, (t.len + kChunk * kElems - 1) / (kChunk * kElems)) : 1;
       float sum[PREC ? 4 : 1][32];
       for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
         const int b = j & 1;
@@ -838,10 +928,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (elect_one()) mbar_arrive(freed + b);
         };
-        if (PREC && pieces > 1) {
-          read_pieces<PREC>(sum, taddr, half, in, p);
+        if (PREC && (SPLIT || pieces > 1)) {
+          read_pieces<PREC>(sum, taddr, half, in, p, t.len == 0);
           release();
-          if (p + 1 == pieces) {
+          if (!SPLIT && p + 1 == pieces) {
 #pragma unroll
             for (int g = 0; g < (PREC ? 4 : 1); ++g)
               if (half + 2 * g < in && ok)
@@ -853,7 +943,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         } else {
           for (int32_t i = half; i < in && ok; i += 2) {
             emit(i, [&](int h, float(&v)[32]) {
-              if (t.hi == t.lo) {
+              if (t.len == 0) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) v[k] = 0.f;
               } else {
@@ -866,6 +956,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (in <= half) release();   // no box of this warp's in the tile
         }
       }
+      if (SPLIT) {
+        join_slices<KIND, PREC>(sum, sm, warp - 4, lane, half, in, rank, slice, a.split);
+#pragma unroll
+        for (int g = 0; g < (PREC ? 4 : 1); ++g)
+          if (half + 2 * g < in && g % a.split == slice && ok)
+            emit(half + 2 * g, [&](int, float(&v)[32]) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = sum[g][k];
+            });
+      }
+    }
+    if (SPLIT && first >= n_tiles) {   // the cluster has no tile: keep step with its barriers
+      cluster_sync_all();
+      cluster_sync_all();
     }
     if (!ok && a.has_c) {   // gave up: what was loaded ahead lands before the CTA ends (bounded)
       for (int k = 0; k < 3; ++k) warp_wait(landed + k, (c_phase >> k) & 1, a.status);
@@ -880,7 +984,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int32_t j = 0, from = 0;
     bool ok = true;
     for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
-      const Tile t = tile_at<GRAD>(a, start, idx, from);
+      const Tile t = tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx, from);
       from = t.e;
       const int32_t m = t.m0 + 128 * rank + 32 * q;   // this warp's 32 channels
       const int32_t m_in = min(32, a.M - m);
@@ -897,7 +1001,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             v[k] = static_cast<float>(__float_as_int(v[k])) * chan * __shfl_sync(0xffffffffu, mine, k);
         }
         const int64_t o = r0 * a.ldo + m;
-        if (PREC || a.odtype == HIMUON_FP32)
+        if ((PREC && !SPLIT) || a.odtype == HIMUON_FP32)
           put_rows32(st, lane, v, reinterpret_cast<float *>(a.out[0]) + o, a.ldo, r_in, m_in);
         else if (a.odtype == HIMUON_FP16)
           put_rows16<__half2>(reinterpret_cast<uint32_t *>(st), lane, v, reinterpret_cast<uint16_t *>(a.out[0]) + o,
@@ -906,15 +1010,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           put_rows16<__nv_bfloat162>(reinterpret_cast<uint32_t *>(st), lane, v,
                                      reinterpret_cast<uint16_t *>(a.out[0]) + o, a.ldo, r_in, m_in);
       };
-      const int32_t pieces = PREC ? (a.K + kChunk * kElems - 1) / (kChunk * kElems) : 1;
+      const int32_t pieces = kPieces ? (t.len + kChunk * kElems - 1) / (kChunk * kElems) : 1;
       float sum[PREC ? 4 : 1][32];
       for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
         const int b = j & 1;
         if (!(ok = warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status))) break;
         tc_fence_after();
         const uint32_t taddr = tmem + static_cast<uint32_t>(b * kTileN) + (static_cast<uint32_t>(q * 32) << 16);
-        if (PREC && pieces > 1) {
-          read_pieces<PREC>(sum, taddr, half, in, p);
+        if (PREC && (SPLIT || pieces > 1)) {
+          read_pieces<PREC>(sum, taddr, half, in, p, false);
         } else {
 #pragma unroll 1
           for (int32_t i = half; i < in; i += 2) {
@@ -926,13 +1030,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (elect_one()) mbar_arrive(freed + b);
-        if (PREC && pieces > 1 && p + 1 == pieces) {
+        if (PREC && !SPLIT && pieces > 1 && p + 1 == pieces) {
 #pragma unroll
           for (int g = 0; g < (PREC ? 4 : 1); ++g)
             if (half + 2 * g < in) emit(half + 2 * g, sum[g]);
         }
       }
+      if (SPLIT) {
+        join_slices<KIND, PREC>(sum, sm, warp - 4, lane, half, in, rank, slice, a.split);
+#pragma unroll
+        for (int g = 0; g < (PREC ? 4 : 1); ++g)
+          if (half + 2 * g < in && g % a.split == slice) emit(half + 2 * g, sum[g]);
+      }
     }
+    if (SPLIT && first >= n_tiles) {   // the cluster has no tile: keep step with its barriers
+      cluster_sync_all();
+      cluster_sync_all();
+    }
+  }
+  if (SPLIT && warp < 4) {   // the two barriers of join_slices
+    __syncwarp();
+    cluster_sync_all();
+    cluster_sync_all();
   }
   __syncwarp();
   tc_fence_before();
@@ -1298,15 +1417,34 @@ int sm_count() {
   return sms;
 }
 
-template <int KIND, int A_MN, int GRAD, int PREC, int NMAP, int NOUT>
+template <int KIND, int A_MN, int GRAD, int PREC, int SPLIT, int NMAP, int NOUT>
 int launch_mma(const MmaArgs<NMAP, NOUT> &a, int64_t most_tiles, cudaStream_t stream) {
-  auto kern = expert_kernel<KIND, A_MN, GRAD, NMAP, NOUT, PREC>;
+  auto kern = expert_kernel<KIND, A_MN, GRAD, NMAP, NOUT, PREC, SPLIT>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
     return HIMUON_ERR_CUDA;
-  const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(most_tiles, sm_count() / 2));
+  const unsigned ctas = 2 * static_cast<unsigned>(a.split);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas * static_cast<unsigned>(SPLIT ? most_tiles : std::min<int64_t>(most_tiles, sm_count() / 2)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   count_launch();
-  kern<<<grid, kThreads, kSmem, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? HIMUON_OK : HIMUON_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? HIMUON_OK : HIMUON_ERR_CUDA;
+}
+
+// How many pairs share a tile (1, 2 or 4): as many as the call's tiles, at most
+// `tiles`, leave pairs for, each with at least 4 blocks of the longest sum.
+int32_t split_of(int64_t tiles, int64_t blocks) {
+  const int64_t pairs = sm_count() / 2;
+  for (int32_t s = 4; s > 1; s /= 2)
+    if (tiles * s <= pairs && blocks >= 4 * s) return s;
+  return 1;
 }
 
 template <int NMAP, int NOUT>
@@ -1321,6 +1459,7 @@ void common_args(MmaArgs<NMAP, NOUT> &a, const int32_t *offsets, int32_t e0, int
   a.ldo = a.out_stride = 0;
   a.buffers = 1;
   a.box_cols = 0;
+  a.split = 1;
   a.cdtype = HIMUON_BF16;
   a.alpha = 1.f;
   a.beta = 0.f;
@@ -1356,12 +1495,31 @@ int product_launch(const himuon_mat *X, const float *x_scale, const himuon_mat *
   a.out[0] = static_cast<char *>(Y->data);
   a.ldo = Y->ld;
   a.odtype = Y->dtype;
-  const int64_t mt_m = (Y->cols + kTileM - 1) / kTileM;
-  const int64_t most = mt_m * (X->rows / kTileN + std::min<int64_t>(n, X->rows));
-  if (X->dtype == HIMUON_I8) return launch_mma<1, 0, 0, 0>(a, most, stream);
-  if (Y->dtype == HIMUON_FP32)
-    return w_trans ? launch_mma<0, 0, 0, 1>(a, most, stream) : launch_mma<0, 1, 0, 1>(a, most, stream);
-  return w_trans ? launch_mma<0, 0, 0, 0>(a, most, stream) : launch_mma<0, 1, 0, 0>(a, most, stream);
+  // Row tiles of up to 256 rows move the fewest bytes.  Where even tiles of up to
+  // 128 (below that a tile's loads of W bound it) cannot fill the pairs once,
+  // whatever the groups' sizes, they are taken, and what pairs are left then
+  // share the tiles' sums.  (One group of 512 rows, 4096 -> 4096: 28.7 us
+  // with 256 rows, 20.5 with 128; where the cap lengthens the last round instead,
+  // it costs: 1024 rows 28.7 us with 256, 32.9 with 128.)
+  const int64_t mt_m = (Y->cols + kTileM - 1) / kTileM, pairs = sm_count() / 2;
+  auto most_tiles = [&](int64_t cap) {
+    return mt_m * (n == 1 ? (X->rows + cap - 1) / cap : X->rows / cap + std::min<int64_t>(n, X->rows));
+  };
+  a.cap = most_tiles(128) <= pairs ? 7 : 8;
+  const int64_t most = most_tiles(1 << a.cap);
+  a.mt_m = static_cast<int32_t>(mt_m);
+  a.mt_n = 0;
+  a.split = split_of(most, (X->cols * static_cast<int64_t>(size_of(X->dtype)) + 127) / 128);
+  const bool fp32 = Y->dtype == HIMUON_FP32;
+  if (X->dtype == HIMUON_I8)
+    return a.split > 1 ? launch_mma<1, 0, 0, 1, 1>(a, most, stream) : launch_mma<1, 0, 0, 0, 0>(a, most, stream);
+  if (w_trans)
+    return a.split > 1 ? launch_mma<0, 0, 0, 1, 1>(a, most, stream)
+           : fp32      ? launch_mma<0, 0, 0, 1, 0>(a, most, stream)
+                       : launch_mma<0, 0, 0, 0, 0>(a, most, stream);
+  return a.split > 1 ? launch_mma<0, 1, 0, 1, 1>(a, most, stream)
+         : fp32      ? launch_mma<0, 1, 0, 1, 0>(a, most, stream)
+                     : launch_mma<0, 1, 0, 0, 0>(a, most, stream);
 }
 
 int run_product(const himuon_mat *X, const float *x_scale, const himuon_mat *W, const himuon_mat *w_scale, int32_t n,
@@ -1403,7 +1561,28 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
   a.alpha = alpha;
   a.beta = beta;
   a.has_c = C != nullptr;
-  a.box_cols = G->dtype == HIMUON_FP32 || (C && C->dtype == HIMUON_FP32) ? 32 : 64;
+  // Columns of a tile: as few tiles as 256 columns allow, or more of equal
+  // width where that fills the last round of the pairs better (a tile costs its
+  // columns and about as much as 64 more), in whole boxes of the epilogue.
+  const bool wide = G->dtype == HIMUON_FP32 || (C && C->dtype == HIMUON_FP32);
+  a.box_cols = wide ? 32 : 64;
+  const int64_t m_tiles = n * ((A->cols + kTileM - 1) / kTileM), pairs = sm_count() / 2;
+  const int64_t fewest = (B->cols + kTileN - 1) / kTileN;
+  int64_t best = INT64_MAX, most = 0;
+  for (int64_t c = fewest; c <= 4 * fewest; ++c) {
+    const int64_t w = ((B->cols + c - 1) / c + a.box_cols - 1) / a.box_cols * a.box_cols;
+    const int64_t tiles = m_tiles * ((B->cols + w - 1) / w), cost = (tiles + pairs - 1) / pairs * (w + 64);
+    if (cost < best) {
+      best = cost;
+      most = tiles;
+      a.cap = static_cast<int32_t>(w);
+      a.mt_n = static_cast<int32_t>(tiles / m_tiles);
+    }
+    if (tiles >= 6 * pairs) break;
+  }
+  a.mt_m = static_cast<int32_t>(m_tiles / n);
+  a.split = split_of(most, (A->rows + 63) / 64);
+  if (a.split > 1) a.box_cols = 32;
   for (int32_t i = 0; i < (NOUT > 1 ? n : 1); ++i) {
     if (!make_map(&a.g[i], G[e0 + i], NOUT > 1 ? 1 : n, g_stride, 32, a.box_cols)) return HIMUON_ERR_CUDA;
     a.out[i] = static_cast<char *>(G[e0 + i].data);
@@ -1414,8 +1593,8 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
   a.odtype = G->dtype;
   if (C) a.cdtype = C->dtype;
   a.buffers = C ? 3 : 2;
-  const int64_t most = n * ((A->cols + kTileM - 1) / kTileM) * ((B->cols + kTileN - 1) / kTileN);
-  return G->dtype == HIMUON_FP32 ? launch_mma<0, 1, 1, 1>(a, most, stream) : launch_mma<0, 1, 1, 0>(a, most, stream);
+  if (a.split > 1) return launch_mma<0, 1, 1, 1, 1>(a, most, stream);
+  return G->dtype == HIMUON_FP32 ? launch_mma<0, 1, 1, 1, 0>(a, most, stream) : launch_mma<0, 1, 1, 0, 0>(a, most, stream);
 }
 
 }  // namespace
