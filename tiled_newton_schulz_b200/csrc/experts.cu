@@ -1069,37 +1069,31 @@ struct QuantArgs {
   int32_t dim;
 };
 
-// code = round(127 x / top), ties to even.  x and top are first multiplied by a
-// power of two (exact) that keeps 127 x and 1 / top in range; 127 x is then
-// exact for 16-bit x.  127 x times inv = 1 / top is off from the quotient by
-// less than 127 * 3 * 2^-24 < 3e-5, so it decides every code whose distance to
-// the next tie is more than that; nearer ones (about 1 in 5000) take the
-// correctly rounded division, which meets ties of 16-bit x exactly.  Adding
-// 1.5 * 2^23 rounds to an integer (ties to even) and leaves it in the low bits.
-// (The plain division for every element bounded the kernel by its
-// instructions: 8192 x 11008 bf16 in 464 us.)
+// code = round(127 x / top), ties to even.  With 127 / top = hi + lo (two fp32
+// numbers, the second the division's remainder), x hi + x lo summed without
+// losing the first product's low part is the quotient rounded once: ties of
+// 16-bit x, which are short numbers, come out exactly.  Adding 1.5 * 2^23 then
+// rounds to an integer and leaves it in the low bits.  Five operations per
+// element: the kernel is bound by its instructions (the plain division took 464
+// us for 8192 x 11008 bf16).  A maximum so small or large that hi or x hi could
+// leave fp32's range takes the division, scaled by a power of two.
 struct Coder {
-  float k, top, inv;
+  float hi, lo, top;
   __device__ explicit Coder(float t) {
-    const float mul = t > 0x1p100f ? 0x1p-100f : t < 0x1p-100f ? 0x1p100f : 1.f;
-    top = t * mul;
-    k = 127.f * mul;
-    inv = __fdiv_rn(1.f, top);
+    top = t;
+    hi = __fdiv_rn(127.f, t);
+    lo = __fdiv_rn(fmaf(-t, hi, 127.f), t);
   }
-  // the code in the low byte; `far`: the largest distance to the code so far
-  __device__ __forceinline__ uint32_t near_code(float x, float &far) const {
-    const float r = x * k, t = fmaf(r, inv, 12582912.f);
-    far = fmaxf(far, fabsf(fmaf(r, inv, -(t - 12582912.f))));
-    return __float_as_uint(t);
+  __device__ __forceinline__ bool in_range() const { return top >= 0x1p-60f && top <= 0x1p60f; }
+  __device__ __forceinline__ uint32_t near_code(float x) const {   // the code in the low byte
+    const float p = x * hi;
+    return __float_as_uint(p + fmaf(x, lo, fmaf(x, hi, -p)) + 12582912.f);
   }
-  __device__ __forceinline__ uint32_t exact_code(float x) const {
-    return __float_as_uint(__fdiv_rn(x * k, top) + 12582912.f);
+  __device__ __forceinline__ uint32_t far_code(float x) const {
+    const float mul = top > 1.f ? 0x1p-100f : 0x1p100f;
+    return __float_as_uint(__fdiv_rn(127.f * (x * mul), top * mul) + 12582912.f);
   }
-  __device__ __forceinline__ uint32_t operator()(float x) const {
-    float far = 0.f;
-    const uint32_t c = near_code(x, far);
-    return far <= 0.4999f ? c : exact_code(x);
-  }
+  __device__ __forceinline__ uint32_t operator()(float x) const { return in_range() ? near_code(x) : far_code(x); }
 };
 __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
@@ -1124,26 +1118,30 @@ __device__ __forceinline__ void ld8_any(const void *p, int32_t dtype, int64_t i,
 // the two passes (kHold runs of 8 elements per thread, all loads in flight
 // together; longer rows are read again, from L2).  HBM-bound: 3 bytes per
 // 16-bit element.
-template <int F32>
-struct Run8;   // 8 consecutive elements as loaded
-template <>
-struct Run8<0> {
+__device__ __forceinline__ uint32_t max_s16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.s16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <int DT>
+struct Run8 {   // 8 consecutive elements as loaded (16 bits)
   uint4 u;
   __device__ __forceinline__ void load(const char *p, int64_t i) { u = *reinterpret_cast<const uint4 *>(p + 16 * i); }
   // |x| of 16-bit floats orders as an integer: two maxima at a time
   __device__ __forceinline__ uint32_t top() const {
     const uint32_t m = 0x7fff7fffu;
-    return __vmaxu2(__vmaxu2(u.x & m, u.y & m), __vmaxu2(u.z & m, u.w & m));
+    return max_s16x2(max_s16x2(u.x & m, u.y & m), max_s16x2(u.z & m, u.w & m));
   }
-  __device__ __forceinline__ float get(int j, int32_t dtype) const {
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max_s16x2(a, b); }
+  __device__ __forceinline__ float get(int j) const {
     const uint32_t w = j < 2 ? u.x : j < 4 ? u.y : j < 6 ? u.z : u.w;
-    if (dtype == HIMUON_BF16) return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
+    if (DT == HIMUON_BF16) return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
     const __half2 h = *reinterpret_cast<const __half2 *>(&w);
     return j & 1 ? __high2float(h) : __low2float(h);
   }
 };
 template <>
-struct Run8<1> {
+struct Run8<HIMUON_FP32> {
   float4 a, b;
   __device__ __forceinline__ void load(const char *p, int64_t i) {
     a = *reinterpret_cast<const float4 *>(p + 32 * i);
@@ -1153,46 +1151,48 @@ struct Run8<1> {
     return max(max(max(abs_bits(a.x), abs_bits(a.y)), max(abs_bits(a.z), abs_bits(a.w))),
                max(max(abs_bits(b.x), abs_bits(b.y)), max(abs_bits(b.z), abs_bits(b.w))));
   }
-  __device__ __forceinline__ float get(int j, int32_t) const {
+  static __device__ __forceinline__ uint32_t larger(uint32_t x, uint32_t y) { return max(x, y); }
+  __device__ __forceinline__ float get(int j) const {
     const float4 &f = j < 4 ? a : b;
     return (j & 3) == 0 ? f.x : (j & 3) == 1 ? f.y : (j & 3) == 2 ? f.z : f.w;
   }
 };
-template <int F32>
-constexpr int kHold = F32 ? 4 : 8;
+template <int DT>
+constexpr int kHold = DT == HIMUON_FP32 ? 4 : 8;
 
-template <int F32, int TPR>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constant__ QuantArgs a) {
+template <int DT, int TPR>
+__global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const __grid_constant__ QuantArgs a) {
   __shared__ uint32_t part[8];
   const int32_t z = blockIdx.y;
+  if (a.dtype[z] != DT) return;
   const int64_t row = blockIdx.x * static_cast<int64_t>(256 / TPR) + threadIdx.x / TPR;
   const int t = threadIdx.x % TPR;
-  const int32_t dt = a.dtype[z];
-  const int64_t cols = a.cols[z], runs = cols / 8;
-  const bool live = row < a.rows[z] && (dt == HIMUON_FP32) == (F32 == 1);
-  const char *in = static_cast<const char *>(a.in[z]) + (live ? row * a.ld[z] : 0) * (F32 ? 4 : 2);
-  Run8<F32> v[kHold<F32>];
-  uint32_t top = 0;   // F32: bits of the maximum; else two 16-bit maxima
+  const int64_t cols = a.cols[z];
+  const int32_t runs = static_cast<int32_t>(cols / 8);
+  const bool live = row < a.rows[z];
+  const char *in = static_cast<const char *>(a.in[z]) + (live ? row * a.ld[z] : 0) * (DT == HIMUON_FP32 ? 4 : 2);
+  Run8<DT> v[kHold<DT>];
+  uint32_t top = 0;   // fp32: bits of the maximum; else two 16-bit maxima
   if (live) {
 #pragma unroll
-    for (int h = 0; h < kHold<F32>; ++h)
+    for (int h = 0; h < kHold<DT>; ++h)
       if (t + h * TPR < runs) v[h].load(in, t + h * TPR);
 #pragma unroll
-    for (int h = 0; h < kHold<F32>; ++h)
-      if (t + h * TPR < runs) top = F32 ? max(top, v[h].top()) : __vmaxu2(top, v[h].top());
-    for (int64_t i = t + static_cast<int64_t>(kHold<F32>) * TPR; i < runs; i += TPR) {
-      Run8<F32> w;
+    for (int h = 0; h < kHold<DT>; ++h)
+      if (t + h * TPR < runs) top = Run8<DT>::larger(top, v[h].top());
+    for (int32_t i = t + kHold<DT> * TPR; i < runs; i += TPR) {
+      Run8<DT> w;
       w.load(in, i);
-      top = F32 ? max(top, w.top()) : __vmaxu2(top, w.top());
+      top = Run8<DT>::larger(top, w.top());
     }
   }
-  if (!F32) {   // the 16-bit maximum as an fp32's bits
+  if (DT != HIMUON_FP32) {   // the 16-bit maximum as an fp32's bits
     const uint32_t m = max(top >> 16, top & 0xffffu);
     const uint16_t h = static_cast<uint16_t>(m);
-    top = dt == HIMUON_FP16 ? abs_bits(__half2float(*reinterpret_cast<const __half *>(&h))) : m << 16;
+    top = DT == HIMUON_FP16 ? abs_bits(__half2float(*reinterpret_cast<const __half *>(&h))) : m << 16;
   }
   if (live)
-    for (int64_t i = 8 * runs + t; i < cols; i += TPR) top = max(top, abs_bits(ld_any(in, dt, i)));
+    for (int64_t i = 8ll * runs + t; i < cols; i += TPR) top = max(top, abs_bits(ld_any(in, DT, i)));
   top = __reduce_max_sync(0xffffffffu, top);
   if (TPR > 32) {
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
@@ -1207,41 +1207,39 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const __grid_constan
   int8_t *out = a.codes[z] + row * a.ldq[z];
   const bool ok = line_ok(top);
   const Coder code(ok ? __uint_as_float(top) : 1.f);
-  auto put8 = [&](int64_t i, const Run8<F32> &x) {
+  if (!ok || !code.in_range()) {   // (rare: one element at a time)
+    for (int64_t i = t; i < cols; i += TPR) out[i] = ok ? static_cast<int8_t>(code.far_code(ld_any(in, DT, i))) : 0;
+    return;
+  }
+  auto put8 = [&](int32_t i, const Run8<DT> &x) {
     uint32_t u[8];
-    float far = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = code.near_code(x.get(j, dt), far);
-    if (!(far <= 0.4999f)) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] = code.exact_code(x.get(j, dt));
-    }
-    *reinterpret_cast<uint2 *>(out + 8 * i) =
-        ok ? make_uint2(bytes4(u[0], u[1], u[2], u[3]), bytes4(u[4], u[5], u[6], u[7])) : make_uint2(0, 0);
+    for (int j = 0; j < 8; ++j) u[j] = code.near_code(x.get(j));
+    *reinterpret_cast<uint2 *>(out + 8 * i) = make_uint2(bytes4(u[0], u[1], u[2], u[3]), bytes4(u[4], u[5], u[6], u[7]));
   };
 #pragma unroll
-  for (int h = 0; h < kHold<F32>; ++h)
+  for (int h = 0; h < kHold<DT>; ++h)
     if (t + h * TPR < runs) put8(t + h * TPR, v[h]);
-  for (int64_t i = t + static_cast<int64_t>(kHold<F32>) * TPR; i < runs; i += TPR) {
-    Run8<F32> w;
+  for (int32_t i = t + kHold<DT> * TPR; i < runs; i += TPR) {
+    Run8<DT> w;
     w.load(in, i);
     put8(i, w);
   }
-  for (int64_t i = 8 * runs + t; i < cols; i += TPR) out[i] = ok ? static_cast<int8_t>(code(ld_any(in, dt, i))) : 0;
+  for (int64_t i = 8ll * runs + t; i < cols; i += TPR) out[i] = static_cast<int8_t>(code.near_code(ld_any(in, DT, i)));
 }
 
 // Rows of at most `widest` columns: the fewest threads per row that hold it.
-template <int F32>
+template <int DT>
 void quantize_rows(const QuantArgs &a, int64_t most, int64_t widest, unsigned zs, cudaStream_t st) {
-  const int64_t per = 8 * kHold<F32>;
+  const int64_t per = 8 * kHold<DT>;
   auto go = [&](auto kern, int tpr) {
     count_launch();
     kern<<<dim3(static_cast<unsigned>((most + 256 / tpr - 1) / (256 / tpr)), zs), 256, 0, st>>>(a);
   };
-  if (widest <= 32 * per) go(quantize_rows_kernel<F32, 32>, 32);
-  else if (widest <= 64 * per) go(quantize_rows_kernel<F32, 64>, 64);
-  else if (widest <= 128 * per) go(quantize_rows_kernel<F32, 128>, 128);
-  else go(quantize_rows_kernel<F32, 256>, 256);
+  if (widest <= 32 * per) go(quantize_rows_kernel<DT, 32>, 32);
+  else if (widest <= 64 * per) go(quantize_rows_kernel<DT, 64>, 64);
+  else if (widest <= 128 * per) go(quantize_rows_kernel<DT, 128>, 128);
+  else go(quantize_rows_kernel<DT, 256>, 256);
 }
 
 // One scale per column, codes transposed: a CTA takes 64 columns (128 bytes of
@@ -1696,7 +1694,7 @@ int himuon_quantize(const himuon_mat *in, int32_t n, int32_t dim, const himuon_m
     QuantArgs a;
     a.dim = dim;
     int64_t most = 0, widest = 0;
-    bool any16 = false, any32 = false;
+    bool any[3] = {false, false, false};
     for (int32_t e = 0; e < cnt; ++e) {
       const himuon_mat &m = in[e0 + e];
       a.in[e] = m.data;
@@ -1709,7 +1707,7 @@ int himuon_quantize(const himuon_mat *in, int32_t n, int32_t dim, const himuon_m
       a.dtype[e] = m.dtype;
       most = std::max(most, dim ? m.cols : m.rows);
       widest = std::max(widest, m.cols);
-      (m.dtype == HIMUON_FP32 ? any32 : any16) = true;
+      any[m.dtype] = true;
     }
     if (most == 0) continue;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1717,9 +1715,10 @@ int himuon_quantize(const himuon_mat *in, int32_t n, int32_t dim, const himuon_m
     if (dim) {
       count_launch();
       quantize_cols_kernel<<<dim3(static_cast<unsigned>((most + 63) / 64), zs), 256, 0, st>>>(a);
-    } else {   // one launch per storage width among the call's matrices
-      if (any16) quantize_rows<0>(a, most, widest, zs, st);
-      if (any32) quantize_rows<1>(a, most, widest, zs, st);
+    } else {   // one launch per storage type among the call's matrices
+      if (any[HIMUON_BF16]) quantize_rows<HIMUON_BF16>(a, most, widest, zs, st);
+      if (any[HIMUON_FP16]) quantize_rows<HIMUON_FP16>(a, most, widest, zs, st);
+      if (any[HIMUON_FP32]) quantize_rows<HIMUON_FP32>(a, most, widest, zs, st);
     }
     if (cudaGetLastError() != cudaSuccess) return HIMUON_ERR_CUDA;
   }
