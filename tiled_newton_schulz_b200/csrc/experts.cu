@@ -127,6 +127,13 @@ __device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *m
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar_cluster)
       : "memory");
 }
+// Launches of this file follow one another without a gap: a kernel lets the next
+// one start as soon as its CTAs have (its first part, which touches no memory of
+// the stream's, runs under this one's end), and waits for everything before it
+// in the stream to have completed ahead of its first access.
+__device__ __forceinline__ void grid_start_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // One thread of the converged warp (the same one every time).  The loops that
 // issue copies and MMAs are run by whole warps, with only the instruction
 // itself in the elected thread's branch: their addresses and descriptors then
@@ -564,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint16_t pair_mask = static_cast<uint16_t>(3u << even);
   const int32_t ctas = SPLIT ? 2 * a.split : 2;
   const int32_t first = static_cast<int32_t>(blockIdx.x) / ctas, step = static_cast<int32_t>(gridDim.x) / ctas;
+  grid_start_next();
 
   if (warp == 0) {
     // one barrier per lane and round: full, empty, tail_full, tail_ready, acc_full, acc_empty, drained, done, c_full
@@ -580,6 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
   }
+  grid_wait();   // nothing above reads or writes what earlier work of the stream does
   if (!GRAD && warp == 2) plan_rows(a, start, widest, lane);
   if (GRAD && warp == 2) check_offsets(a, lane);
   __syncwarp();
@@ -1163,6 +1172,8 @@ constexpr int kHold = DT == HIMUON_FP32 ? 4 : 8;
 template <int DT, int TPR>
 __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const __grid_constant__ QuantArgs a) {
   __shared__ uint32_t part[8];
+  grid_start_next();
+  grid_wait();
   const int32_t z = blockIdx.y;
   if (a.dtype[z] != DT) return;
   const int64_t row = blockIdx.x * static_cast<int64_t>(256 / TPR) + threadIdx.x / TPR;
@@ -1228,13 +1239,27 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const __grid_cons
   for (int64_t i = 8ll * runs + t; i < cols; i += TPR) out[i] = static_cast<int8_t>(code.near_code(ld_any(in, DT, i)));
 }
 
+template <typename Kern>
+void launch_quant(Kern kern, dim3 grid, const QuantArgs &a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  count_launch();
+  cudaLaunchKernelEx(&cfg, kern, a);   // (its error is read by the caller)
+}
+
 // Rows of at most `widest` columns: the fewest threads per row that hold it.
 template <int DT>
 void quantize_rows(const QuantArgs &a, int64_t most, int64_t widest, unsigned zs, cudaStream_t st) {
   const int64_t per = 8 * kHold<DT>;
   auto go = [&](auto kern, int tpr) {
-    count_launch();
-    kern<<<dim3(static_cast<unsigned>((most + 256 / tpr - 1) / (256 / tpr)), zs), 256, 0, st>>>(a);
+    launch_quant(kern, dim3(static_cast<unsigned>((most + 256 / tpr - 1) / (256 / tpr)), zs), a, st);
   };
   if (widest <= 32 * per) go(quantize_rows_kernel<DT, 32>, 32);
   else if (widest <= 64 * per) go(quantize_rows_kernel<DT, 64>, 64);
@@ -1248,6 +1273,8 @@ void quantize_rows(const QuantArgs &a, int64_t most, int64_t widest, unsigned zs
 __global__ void __launch_bounds__(256) quantize_cols_kernel(const __grid_constant__ QuantArgs a) {
   __shared__ uint32_t tops[8][64];
   __shared__ __align__(16) int8_t turn[64][128 + 16];
+  grid_start_next();
+  grid_wait();
   const int32_t z = blockIdx.y;
   const int64_t c0 = blockIdx.x * 64ll;
   const int64_t rows = a.rows[z], cols = a.cols[z], ld = a.ld[z];
@@ -1426,12 +1453,14 @@ int launch_mma(const MmaArgs<NMAP, NOUT> &a, int64_t most_tiles, cudaStream_t st
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = ctas;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   count_launch();
   return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? HIMUON_OK : HIMUON_ERR_CUDA;
 }
@@ -1713,8 +1742,7 @@ int himuon_quantize(const himuon_mat *in, int32_t n, int32_t dim, const himuon_m
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const unsigned zs = static_cast<unsigned>(cnt);
     if (dim) {
-      count_launch();
-      quantize_cols_kernel<<<dim3(static_cast<unsigned>((most + 63) / 64), zs), 256, 0, st>>>(a);
+      launch_quant(quantize_cols_kernel, dim3(static_cast<unsigned>((most + 63) / 64), zs), a, st);
     } else {   // one launch per storage type among the call's matrices
       if (any[HIMUON_BF16]) quantize_rows<HIMUON_BF16>(a, most, widest, zs, st);
       if (any[HIMUON_FP16]) quantize_rows<HIMUON_FP16>(a, most, widest, zs, st);
