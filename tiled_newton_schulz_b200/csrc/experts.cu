@@ -890,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = warp_wait(landed + at, (c_phase >> at) & 1, a.status))) return;
           c_phase ^= 1u << at;
         } else {
-          if (elect_one()) bulk_wait_read<1>();   // two buffers: the store before the last has read this one
+          if (elect_one()) bulk_wait_read<0>();   // (the last box's store has read the buffer)
           __syncwarp();
         }
 #pragma unroll
@@ -1619,7 +1619,7 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
   a.out_stride = g_stride;
   a.odtype = G->dtype;
   if (C) a.cdtype = C->dtype;
-  a.buffers = C ? 3 : 2;
+  a.buffers = C ? 3 : 1;
   if (a.split > 1) return launch_mma<0, 1, 1, 1, 1>(a, most, stream);
   return G->dtype == HIMUON_FP32 ? launch_mma<0, 1, 1, 1, 0>(a, most, stream) : launch_mma<0, 1, 1, 0, 0>(a, most, stream);
 }
