@@ -58,7 +58,7 @@ constexpr int kThreads = 128 + 32 * kEpiWarps;   // three warpgroups: loads and 
 // (K = 1100: 1.1e-6 against 2.6e-7 for rounded fp32 sums).  Their sums are cut
 // every kChunk blocks of 64; the epilogue adds the pieces in fp32 registers.
 constexpr int kChunk = 8;
-constexpr uint32_t kBarBytes = 640;
+constexpr uint32_t kBarBytes = 448;
 constexpr uint32_t kSmem = kData + kBarBytes + 4 * (kMaxStack + 4) + 1024;
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
@@ -67,7 +67,9 @@ static_assert(kSmem <= 232448, "shared memory of one CTA");
 template <int NMAP, int NOUT>
 struct MmaArgs {
   CUtensorMap w[NMAP];     // product: W; gradient: operand A
-  CUtensorMap x[4];        // product: X in boxes of 128, 64, 32 and 16 rows; gradient: [0] operand B
+  // product: X in boxes of 128, 64, 32 and 16 rows; gradient: operand B, and the
+  // windows (make_window_map) of B and A
+  CUtensorMap x[4];
   const int32_t *offsets;
   int64_t rows;
   int32_t n;
@@ -554,9 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t ring = kData - a.buffers * kEpiWarps * kStageOut;   // (a multiple of 1024)
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + kData);   // even CTA: both CTAs' loads
   uint64_t *empty = full + kMaxStages;        // each CTA: the stage's MMAs have read it
-  uint64_t *tail_full = empty + kMaxStages;   // each CTA: its own loads of a block that needs zeros
-  uint64_t *tail_ready = tail_full + kMaxStages;   // even CTA: both CTAs have written the zeros
-  uint64_t *acc_full = tail_ready + kMaxStages;    // [2] each CTA: accumulator b holds a finished tile
+  uint64_t *acc_full = empty + kMaxStages;    // [2] each CTA: accumulator b holds a finished tile
   uint64_t *acc_empty = acc_full + 2;              // [2] even CTA: accumulator b drained by both CTAs
   uint64_t *drained = acc_empty + 2;               // [2] odd CTA: accumulator b drained by its warps
   uint64_t *done = drained + 2;                    // even CTA: every MMA issued has completed
@@ -574,13 +574,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_start_next();
 
   if (warp == 0) {
-    // one barrier per lane and round: full, empty, tail_full, tail_ready, acc_full, acc_empty, drained, done, c_full
-    constexpr int kBars = 4 * kMaxStages + 7 + 3 * kEpiWarps, kAcc = 4 * kMaxStages;
+    // one barrier per lane and round: full, empty, acc_full, acc_empty, drained, done, c_full
+    constexpr int kAcc = 2 * kMaxStages, kBars = kAcc + 7 + 3 * kEpiWarps;
     for (int i = lane; i < kBars; i += 32)
-      mbar_init(full + i, i >= 3 * kMaxStages && i < kAcc     ? 2
-                          : i >= kAcc + 2 && i < kAcc + 4     ? kEpiWarps + 1
-                          : i >= kAcc + 4 && i < kAcc + 6     ? kEpiWarps
-                                                              : 1);
+      mbar_init(full + i, i >= kAcc + 2 && i < kAcc + 4   ? kEpiWarps + 1
+                          : i >= kAcc + 4 && i < kAcc + 6 ? kEpiWarps
+                                                          : 1);
     fence_mbar_init();
     if (lane == 0) tma_prefetch_desc(&a.x[0]);
   }
@@ -615,7 +614,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 1;   // parity of the stage's last release; the first round finds it free
     bool ok = true;
     int64_t issued = 0;
-    uint32_t was_tail = 0, tail_phase = 0;   // per stage: its last block's kind; tail_full's next parity
     Tile t, next;
     if (first < n_tiles) next = tile_at<GRAD, SPLIT, kElems>(a, start, slice, first, 0);
     for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
@@ -634,24 +632,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t *As = sm + s * stage_bytes, *Bs = As + kABytes;
         const uint32_t bar = full0 + 8 * s;
         if (GRAD) {
-          const int32_t y = t.k0 + k;
-          const bool tail = len - k < kElems && ((len - k) & 15);
-          was_tail = (was_tail & ~(1u << s)) | (static_cast<uint32_t>(tail) << s);
-          if (tail) {   // lands on this CTA's own barrier: its warp 2 has zeros to write before the MMAs
-            tail_phase ^= 1u << s;
-            if (elect_one()) {
-              if (rank == 0) mbar_arrive(full + s);
-              mbar_arrive_expect_tx(tail_full + s, bytes);
-              tma_load_2d(As, &a.w[0], m0, y, tail_full + s);
-              tma_load_2d(As + 8192, &a.w[0], m0 + 64, y, tail_full + s);
-              for (int32_t j = 0; j < boxes; ++j) tma_load_2d(Bs + 8192 * j, &a.x[0], n0 + 64 * j, y, tail_full + s);
-            }
-          } else if (elect_one()) {
+          // a group's last rows, fewer than a block: they go to the block's end,
+          // behind rows of zeros (rows -(64 - left) .. of their window), so that
+          // no row of another group, whatever it holds, meets the MMAs
+          const int32_t y = t.k0 + k, left = len - k;
+          if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * bytes);
-            tma_load_2d_pair(As, &a.w[0], m0, y, bar);
-            tma_load_2d_pair(As + 8192, &a.w[0], m0 + 64, y, bar);
-            tma_load_2d_pair(Bs, &a.x[0], n0, y, bar);
-            if (boxes > 1) tma_load_2d_pair(Bs + 8192, &a.x[0], n0 + 64, y, bar);
+            if (left < kElems) {
+              tma_load_3d_pair(As, &a.x[2], m0, left - kElems, y, bar);
+              tma_load_3d_pair(As + 8192, &a.x[2], m0 + 64, left - kElems, y, bar);
+              tma_load_3d_pair(Bs, &a.x[1], n0, left - kElems, y, bar);
+              if (boxes > 1) tma_load_3d_pair(Bs + 8192, &a.x[1], n0 + 64, left - kElems, y, bar);
+            } else {
+              tma_load_2d_pair(As, &a.w[0], m0, y, bar);
+              tma_load_2d_pair(As + 8192, &a.w[0], m0 + 64, y, bar);
+              tma_load_2d_pair(Bs, &a.x[0], n0, y, bar);
+              if (boxes > 1) tma_load_2d_pair(Bs + 8192, &a.x[0], n0 + 64, y, bar);
+            }
           }
         } else if (elect_one()) {
           const bool both = kSub > 1 && k + kElems < len;
@@ -688,11 +685,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // the last loads have landed before the CTA ends, also when something gave
     // up (the even CTA's barriers see both CTAs' loads; the CTAs leave together)
-    for (int64_t i = max((int64_t)0, issued - stages); i < issued; ++i) {
-      const int st = static_cast<int>(i % stages);
-      if ((was_tail >> st) & 1) warp_wait(tail_full + st, ((tail_phase >> st) & 1) ^ 1, a.status);
-      else if (rank == 0) warp_wait(full + st, static_cast<uint32_t>((i / stages) & 1), a.status);
-    }
+    if (rank == 0)
+      for (int64_t i = max((int64_t)0, issued - stages); i < issued; ++i)
+        warp_wait(full + i % stages, static_cast<uint32_t>((i / stages) & 1), a.status);
   } else if (warp == 1) {
     if (PREC) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (rank == 0) {
@@ -701,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t b_bits = GRAD ? sw128_desc(0, 8192, 1024) : sw128_desc(0, 16, 1024);
       constexpr uint32_t kStepA = (A_MN ? 2048 : 32) >> 4, kStepB = (GRAD ? 2048 : 32) >> 4;
       int s = 0;
-      uint32_t phase = 0, tail_phase = 0;
+      uint32_t phase = 0;
       int32_t j = 0;
       bool ok = true;
       Tile t, next;
@@ -735,23 +730,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t left = len - k;
           const bool fresh = kPieces ? k % (kChunk * kElems) == 0 : k == 0;
           if (fresh && !(ok = acquire())) break;
-          if (GRAD && left < kElems && (left & 15)) {   // (`full` is completed by the producer alone)
-            if (!(ok = warp_wait<true>(tail_ready + s, (tail_phase >> s) & 1, a.status))) break;
-            tail_phase ^= 1u << s;
-          } else if (!(ok = warp_wait(full + s, phase, a.status))) {
-            break;
-          }
+          if (!(ok = warp_wait(full + s, phase, a.status))) break;
           tc_fence_after();
           // (a shared-memory address carries the CTA's rank above the descriptor's field)
           const uint64_t ad = a_bits | ((as >> 4) & 0x3FFF), bd = b_bits | (((as + kABytes) >> 4) & 0x3FFF);
+          const int32_t begin = GRAD ? (kElems - min(left, kElems)) / 16 : 0;
           if (elect_one()) {
 #pragma unroll
             for (int32_t kk = 0; kk < 4 * kSub; ++kk) {
-              if (kk > 0 && kk * (kElems / 4) >= left) break;
+              // 16 (int8: 32) elements of K at a time: the product's lie at the
+              // stage's start, the gradient's at its end
+              if (!GRAD && kk > 0 && kk * (kElems / 4) >= left) break;
+              if (GRAD && kk < begin) continue;
               const uint32_t off = (kk / 4) * (block_bytes >> 4);
               const uint64_t au = ad + off + (kk % 4) * kStepA, bu = bd + off + (kk % 4) * kStepB;
-              if (KIND) mma_i8_ss_pair(d, au, bu, idesc, (!fresh || kk > 0) ? 1u : 0u);
-              else mma_ss_pair(d, au, bu, idesc, (!fresh || kk > 0) ? 1u : 0u);
+              const uint32_t add = !fresh || kk > begin ? 1u : 0u;
+              if (KIND) mma_i8_ss_pair(d, au, bu, idesc, add);
+              else mma_ss_pair(d, au, bu, idesc, add);
             }
             mma_commit_pair(empty + s, pair_mask);   // the stage is free in both CTAs once these MMAs have read it
           }
@@ -791,32 +786,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && elect_one()) mbar_arrive_cluster(free0 + 8 * b);
           __syncwarp();
         }
-      }
-    }
-    if (GRAD && warp == 2) {
-      // A group's last stage when its rows are no multiple of 16: the rows
-      // behind the group (other groups' or none) up to the next multiple must
-      // be zero in both operands.  They are contiguous in each 64-column box.
-      const uint32_t ready0 = mapa_shared(smem_u32(tail_ready), even);
-      uint32_t tail_phase = 0;
-      int s = 0;
-      for (int32_t idx = first; idx < n_tiles; idx += step) {
-        const Tile t = tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx, 0);
-        const int32_t len = t.len, left = len % kElems;
-        if (left & 15) {
-          const int st = (s + len / kElems) % stages;
-          if (!warp_wait(tail_full + st, (tail_phase >> st) & 1, a.status)) break;
-          tail_phase ^= 1u << st;
-          const int32_t boxes = 2 + (t.width / 2 + 63) / 64;
-          uint8_t *from = sm + st * stage_bytes + left * 128;
-          for (int32_t x = 0; x < boxes; ++x)
-            for (int32_t i = lane * 16; i < (16 - (left & 15)) * 128; i += 512)
-              *reinterpret_cast<uint4 *>(from + x * 8192 + i) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (elect_one()) mbar_arrive_cluster(ready0 + 8 * st);
-        }
-        s = (s + (len + kElems - 1) / kElems) % stages;
       }
     }
   } else if (GRAD) {
@@ -1416,6 +1385,24 @@ bool make_map(CUtensorMap *map, const himuon_mat &m, int32_t n, int64_t stride, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A row operand as overlapping windows: coordinates (column, r, row) are row `row`
+// + r, r < 64, so that a box that begins at r = left - 64 holds 64 - left rows of
+// zeros and then rows row .. row + left - 1.
+bool make_window_map(CUtensorMap *map, const himuon_mat &m) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const int64_t es = static_cast<int64_t>(size_of(m.dtype));
+  const CUtensorMapDataType dt =
+      m.dtype == HIMUON_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint64_t pitch = static_cast<cuuint64_t>(m.rows > 1 ? m.ld * es : (m.cols * es + 15) / 16 * 16);
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(m.cols), 64, static_cast<cuuint64_t>(m.rows)};
+  cuuint64_t strides[2] = {pitch, pitch};
+  cuuint32_t box[3] = {64, 64, 1};
+  cuuint32_t es1[3] = {1, 1, 1};
+  return enc(map, dt, 3, m.data, dims, strides, box, es1, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Do the matrices lie at equal, positive distances (a multiple of 16 bytes, in
 // a tensor map's range)?  `stride`: that distance.
 bool stacked(const himuon_mat *m, int32_t n, int64_t *stride) {
@@ -1577,8 +1564,9 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
     any.rows = 1;
     any.cols = 8;
     if (!make_map(&a.w[0], any, 0, 0, 64)) return HIMUON_ERR_CUDA;
-    a.x[0] = a.w[0];
-  } else if (!make_map(&a.w[0], *A, 0, 0, 64) || !make_map(&a.x[0], *B, 0, 0, 64)) {
+    a.x[0] = a.x[1] = a.x[2] = a.w[0];
+  } else if (!make_map(&a.w[0], *A, 0, 0, 64) || !make_map(&a.x[0], *B, 0, 0, 64) ||
+             !make_window_map(&a.x[1], *B) || !make_window_map(&a.x[2], *A)) {
     return HIMUON_ERR_CUDA;
   }
   a.K = 0;
