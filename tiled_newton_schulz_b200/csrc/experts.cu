@@ -549,7 +549,7 @@ template <int KIND, int A_MN, int GRAD, int NMAP, int NOUT, int PREC, int SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_kernel(const __grid_constant__ MmaArgs<NMAP, NOUT> a) {
   constexpr int kElems = KIND ? 128 : 64;   // K elements per block of 128 bytes
-  constexpr int kSub = GRAD ? 1 : 2;        // blocks per stage
+  constexpr int kSub = GRAD && PREC ? 1 : 2;   // blocks per stage
   constexpr int kStageK = kElems * kSub;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -635,19 +635,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           // a group's last rows, fewer than a block: they go to the block's end,
           // behind rows of zeros (rows -(64 - left) .. of their window), so that
           // no row of another group, whatever it holds, meets the MMAs
-          const int32_t y = t.k0 + k, left = len - k;
           if (elect_one()) {
-            if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * bytes);
-            if (left < kElems) {
-              tma_load_3d_pair(As, &a.x[2], m0, left - kElems, y, bar);
-              tma_load_3d_pair(As + 8192, &a.x[2], m0 + 64, left - kElems, y, bar);
-              tma_load_3d_pair(Bs, &a.x[1], n0, left - kElems, y, bar);
-              if (boxes > 1) tma_load_3d_pair(Bs + 8192, &a.x[1], n0 + 64, left - kElems, y, bar);
-            } else {
-              tma_load_2d_pair(As, &a.w[0], m0, y, bar);
-              tma_load_2d_pair(As + 8192, &a.w[0], m0 + 64, y, bar);
-              tma_load_2d_pair(Bs, &a.x[0], n0, y, bar);
-              if (boxes > 1) tma_load_2d_pair(Bs + 8192, &a.x[0], n0 + 64, y, bar);
+            const bool both = kSub > 1 && k + kElems < len;
+            if (rank == 0) mbar_arrive_expect_tx(full + s, both ? 4 * bytes : 2 * bytes);
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+              if (u > 0 && !both) break;
+              uint8_t *Au = As + u * block_bytes, *Bu = Bs + u * block_bytes;
+              const int32_t y = t.k0 + k + u * kElems, left = len - k - u * kElems;
+              if (left < kElems) {
+                tma_load_3d_pair(Au, &a.x[2], m0, left - kElems, y, bar);
+                tma_load_3d_pair(Au + 8192, &a.x[2], m0 + 64, left - kElems, y, bar);
+                tma_load_3d_pair(Bu, &a.x[1], n0, left - kElems, y, bar);
+                if (boxes > 1) tma_load_3d_pair(Bu + 8192, &a.x[1], n0 + 64, left - kElems, y, bar);
+              } else {
+                tma_load_2d_pair(Au, &a.w[0], m0, y, bar);
+                tma_load_2d_pair(Au + 8192, &a.w[0], m0 + 64, y, bar);
+                tma_load_2d_pair(Bu, &a.x[0], n0, y, bar);
+                if (boxes > 1) tma_load_2d_pair(Bu + 8192, &a.x[0], n0 + 64, y, bar);
+              }
             }
           }
         } else if (elect_one()) {
@@ -738,10 +744,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) {
 #pragma unroll
             for (int32_t kk = 0; kk < 4 * kSub; ++kk) {
-              // 16 (int8: 32) elements of K at a time: the product's lie at the
-              // stage's start, the gradient's at its end
-              if (!GRAD && kk > 0 && kk * (kElems / 4) >= left) break;
-              if (GRAD && kk < begin) continue;
+              // 16 (int8: 32) elements of K at a time; of a block that is not
+              // full, the product's lie at its start, the gradient's at its end
+              if (kk > 0 && (GRAD ? kk / 4 * kElems : kk * (kElems / 4)) >= left) break;
+              if (GRAD && kk % 4 < (kElems - min(left - kk / 4 * kElems, kElems)) / 16) continue;
               const uint32_t off = (kk / 4) * (block_bytes >> 4);
               const uint64_t au = ad + off + (kk % 4) * kStepA, bu = bd + off + (kk % 4) * kStepB;
               const uint32_t add = !fresh || kk > begin ? 1u : 0u;
