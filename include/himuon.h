@@ -280,7 +280,9 @@ HIMUON_API int64_t himuon_plan_tiles(const himuon_mat *mats, int32_t n, const hi
  * matrices of one argument have the same shape, ld and dtype.  Outputs must not overlap inputs (except C and G
  * below) or each other.  The calls keep nothing between them and take no
  * workspace; results do not depend on timing, and calls on several streams may
- * overlap.
+ * overlap.  The first call on a device loads the kernels: make it before any
+ * stream capture.  No side of an operand is longer than 2^27, and n is at most
+ * 65536 (HIMUON_ERR_UNSUPPORTED, HIMUON_ERR_INVALID).
  */
 
 /*

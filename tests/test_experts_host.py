@@ -56,6 +56,8 @@ def product(lib, X=None, W=None, Y=None, n=2, offsets=P, trans=0):
     (dict(Y=M(10, 32, dtype=hm.I8)), UNSUPPORTED),
     (dict(X=M(10, 64, dtype=7)), UNSUPPORTED),
     (dict(X=M((1 << 30) + 1, 64), Y=M((1 << 30) + 1, 32)), UNSUPPORTED),
+    (dict(X=M((1 << 27) + 8, 64), Y=M((1 << 27) + 8, 32)), UNSUPPORTED),   # longer than the bounded waits allow
+    (dict(n=65537), INVALID),
     (dict(X=M(10, 64, data=P + 8)), ALIGNMENT),
     (dict(Y=M(10, 32, ld=36)), ALIGNMENT),
     (dict(W=arr(M(64, 32, data=P + 2), M(64, 32))), ALIGNMENT),

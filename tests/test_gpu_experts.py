@@ -136,6 +136,77 @@ def test_product_one_group_without_offsets_and_empty_operands(hm):
     assert hm.device_status() == 0
 
 
+@pytest.mark.parametrize("trans", [False, True])
+def test_product_all_groups_empty_and_column_blocks(hm, trans):
+    """No row in any group; and matrices that are column blocks of one fused matrix, as a list and as a 3-D view."""
+    g = gen(21)
+    n, K, N = 3, 64, 40
+    X = matrix((50, K), torch.bfloat16, g)
+    fused = matrix((N if trans else K, n * (K if trans else N)), torch.bfloat16, g)
+    blocks = list(fused.split(K if trans else N, dim=1))
+    W3 = fused.reshape(fused.shape[0], n, -1).transpose(0, 1)
+    assert W3.data_ptr() == fused.data_ptr()
+    Y = torch.full((50, N), -7.0, device=DEV)
+    for off in (offsets([0, 0, 0]), offsets([0, 0, 0], start=50)):
+        hm.expert_product(X, blocks, Y, off, w_trans=trans)
+        assert (Y == -7).all()
+    off = offsets([20, 0, 30])
+    for W in (blocks, W3):
+        Y.fill_(-7)
+        hm.expert_product(X, W, Y, off, w_trans=trans)
+        for e, (a, b) in enumerate(groups(off)):
+            x, w = X[a:b].double(), (blocks[e].double().T if trans else blocks[e].double())
+            close(Y[a:b], x @ w, x.abs() @ w.abs(), K, torch.float32)
+    assert hm.device_status() == 0
+
+
+def test_gradient_into_column_blocks(hm):
+    g = gen(22)
+    n, P, Q = 4, 72, 48
+    A, B = matrix((90, P), torch.bfloat16, g), matrix((90, Q), torch.bfloat16, g)
+    off = offsets([30, 0, 25, 35])
+    for out in (torch.bfloat16, torch.float32):
+        fused = torch.full((P, n * Q), 2.0, device=DEV).to(out)
+        for G in (list(fused.split(Q, dim=1)), fused.reshape(P, n, Q).transpose(0, 1)):
+            fused.fill_(2)
+            hm.expert_gradient(A, B, G, off, beta=1.0, C=G)
+            for e, (a, b) in enumerate(groups(off)):
+                x, y = A[a:b].double(), B[a:b].double()
+                close(G[e], 2 + x.T @ y, 2 + x.abs().T @ y.abs(), b - a, out)
+    assert hm.device_status() == 0
+
+
+def test_first_run_of_a_variant_inside_a_capture(hm):
+    """After one call on the device, a call whose kernel has not run yet can be captured and replayed."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from tiled_newton_schulz_b200 import himuon as hm
+x = torch.randn(40, 64, device="cuda").bfloat16()
+w = torch.randn(1, 64, 48, device="cuda").bfloat16()
+y = torch.zeros(40, 48, device="cuda", dtype=torch.bfloat16)
+hm.expert_product(x, w, y)
+a, b = torch.randn(3000, 64, device="cuda").bfloat16(), torch.randn(3000, 48, device="cuda").bfloat16()
+G = torch.zeros(1, 64, 48, device="cuda")
+q, s = torch.zeros(40, 64, device="cuda", dtype=torch.int8), torch.zeros(40, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    hm.expert_gradient(a, b, G)
+    hm.quantize([x], [q], [s])
+g.replay()
+torch.cuda.synchronize()
+ref = a.double().T @ b.double()
+assert (G[0].double() - ref).norm() <= 1e-5 * ref.norm()
+assert q.abs().amax(1).eq(127).all()
+assert hm.device_status() == 0
+print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-2000:]
+
+
 def test_product_shared_matrix_and_nonfinite_rows(hm):
     """One matrix for two groups; a row with an infinity or a NaN changes no other row."""
     g = gen(4)

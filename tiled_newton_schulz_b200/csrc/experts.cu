@@ -581,7 +581,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                           : i >= kAcc + 4 && i < kAcc + 6 ? kEpiWarps
                                                           : 1);
     fence_mbar_init();
-    if (lane == 0) tma_prefetch_desc(&a.x[0]);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -1229,6 +1228,15 @@ void launch_quant(Kern kern, dim3 grid, const QuantArgs &a, cudaStream_t st) {
   cudaLaunchKernelEx(&cfg, kern, a);   // (its error is read by the caller)
 }
 
+template <int DT>
+bool load_rows_kernels() {
+  cudaFuncAttributes f;
+  return cudaFuncGetAttributes(&f, quantize_rows_kernel<DT, 32>) == cudaSuccess &&
+         cudaFuncGetAttributes(&f, quantize_rows_kernel<DT, 64>) == cudaSuccess &&
+         cudaFuncGetAttributes(&f, quantize_rows_kernel<DT, 128>) == cudaSuccess &&
+         cudaFuncGetAttributes(&f, quantize_rows_kernel<DT, 256>) == cudaSuccess;
+}
+
 // Rows of at most `widest` columns: the fewest threads per row that hold it.
 template <int DT>
 void quantize_rows(const QuantArgs &a, int64_t most, int64_t widest, unsigned zs, cudaStream_t st) {
@@ -1317,12 +1325,17 @@ size_t size_of(int32_t dt) { return dt == HIMUON_FP32 ? 4 : dt == HIMUON_I8 ? 1 
 bool is16(int32_t dt) { return dt == HIMUON_BF16 || dt == HIMUON_FP16; }
 bool is_float(int32_t dt) { return dt >= HIMUON_BF16 && dt <= HIMUON_FP32; }
 
+// Longest side of an operand: a sum of that length still ends well inside the
+// kernels' bounded waits (two seconds).
+constexpr int64_t kMaxSide = (int64_t)1 << 27;
+constexpr int32_t kMaxGroups = 1 << 16;
+
 // A matrix operand: shape, pointer and 16-byte alignment of its rows.
 // `min_rows` 0: a row operand, which may be empty (its pointer is not used).
 int check_operand(const himuon_mat &m, int64_t min_rows) {
   if (m.rows < min_rows || m.cols < 1 || m.ld < m.cols || (m.rows > 0 && !m.data)) return HIMUON_ERR_INVALID;
   if (m.dtype < HIMUON_BF16 || m.dtype > HIMUON_I8) return HIMUON_ERR_UNSUPPORTED;
-  if (m.rows > (int64_t)1 << 30 || m.cols > (int64_t)1 << 30 || m.ld > (int64_t)1 << 36) return HIMUON_ERR_UNSUPPORTED;
+  if (m.rows > kMaxSide || m.cols > kMaxSide || m.ld > (int64_t)1 << 36) return HIMUON_ERR_UNSUPPORTED;
   if (m.rows > 0 && reinterpret_cast<uintptr_t>(m.data) % 16 != 0) return HIMUON_ERR_ALIGNMENT;
   // (the pitch of a single row is never used)
   if (m.rows > 1 && (m.ld * static_cast<int64_t>(size_of(m.dtype))) % 16 != 0) return HIMUON_ERR_ALIGNMENT;
@@ -1409,13 +1422,15 @@ bool make_window_map(CUtensorMap *map, const himuon_mat &m) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Do the matrices lie at equal, positive distances (a multiple of 16 bytes, in
-// a tensor map's range)?  `stride`: that distance.
+// Do the matrices lie one behind the other at equal distances, a multiple of
+// their pitch in a tensor map's range?  `stride`: that distance.  (Anything else,
+// such as column blocks of one fused matrix, runs as a list.)
 bool stacked(const himuon_mat *m, int32_t n, int64_t *stride) {
   *stride = 0;
   if (n == 1) return true;
   const int64_t d = static_cast<const char *>(m[1].data) - static_cast<const char *>(m[0].data);
-  if (d <= 0 || d % 16 != 0 || d >= (int64_t)1 << 39) return false;
+  const int64_t pitch = m->ld * static_cast<int64_t>(size_of(m->dtype));
+  if (d < pitch * m->rows || d % pitch != 0 || pitch % 16 != 0 || d >= (int64_t)1 << 39) return false;
   for (int32_t e = 1; e < n; ++e)
     if (static_cast<const char *>(m[e].data) - static_cast<const char *>(m[e - 1].data) != d) return false;
   *stride = d;
@@ -1435,11 +1450,41 @@ int sm_count() {
   return sms;
 }
 
+// Every variant of the kernel is loaded, and allowed its shared memory, at the
+// first call on a device: a call captured into a graph later loads nothing.
+template <int KIND, int A_MN, int GRAD, int PREC, int SPLIT>
+bool load_variant() {
+  return cudaFuncSetAttribute(expert_kernel<KIND, A_MN, GRAD, 1, 1, PREC, SPLIT>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess &&
+         cudaFuncSetAttribute(expert_kernel<KIND, A_MN, GRAD, GRAD ? 1 : kMaxList, GRAD ? kMaxList : 1, PREC, SPLIT>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess;
+}
+bool load_kernels() {
+  static std::atomic<uint64_t> loaded{0};   // a bit per device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (loaded.load(std::memory_order_relaxed) & bit) return true;
+  cudaFuncAttributes f;
+  const bool ok =
+      load_variant<0, 0, 0, 0, 0>() && load_variant<0, 0, 0, 1, 0>() && load_variant<0, 0, 0, 1, 1>() &&
+      load_variant<0, 1, 0, 0, 0>() && load_variant<0, 1, 0, 1, 0>() && load_variant<0, 1, 0, 1, 1>() &&
+      load_variant<1, 0, 0, 0, 0>() && load_variant<1, 0, 0, 1, 1>() && load_variant<0, 1, 1, 0, 0>() &&
+      load_variant<0, 1, 1, 1, 0>() && load_variant<0, 1, 1, 1, 1>() && device_status_word() != nullptr &&
+      cudaFuncGetAttributes(&f, quantize_cols_kernel) == cudaSuccess && load_rows_kernels<HIMUON_BF16>() &&
+      load_rows_kernels<HIMUON_FP16>() && load_rows_kernels<HIMUON_FP32>();
+  if (ok) loaded.fetch_or(bit, std::memory_order_relaxed);
+  return ok;
+}
+int expert_device() {
+  const int rc = device_usable();
+  if (rc) return rc;
+  return load_kernels() ? HIMUON_OK : HIMUON_ERR_CUDA;
+}
+
 template <int KIND, int A_MN, int GRAD, int PREC, int SPLIT, int NMAP, int NOUT>
 int launch_mma(const MmaArgs<NMAP, NOUT> &a, int64_t most_tiles, cudaStream_t stream) {
   auto kern = expert_kernel<KIND, A_MN, GRAD, NMAP, NOUT, PREC, SPLIT>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-    return HIMUON_ERR_CUDA;
   const unsigned ctas = 2 * static_cast<unsigned>(a.split);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas * static_cast<unsigned>(SPLIT ? most_tiles : std::min<int64_t>(most_tiles, sm_count() / 2)));
@@ -1501,8 +1546,10 @@ int product_launch(const himuon_mat *X, const float *x_scale, const himuon_mat *
   const uint32_t w_rows = w_trans ? 128 : 64;
   for (int32_t i = 0; i < (NMAP > 1 ? n : 1); ++i)
     if (!make_map(&a.w[i], W[e0 + i], NMAP > 1 ? 1 : n, stride, w_rows)) return HIMUON_ERR_CUDA;
+  // (boxes of more rows than half of the widest tile are never loaded)
+  const int64_t half = (std::min<int64_t>(X->rows, kTileN) + 31) / 32 * 16;
   for (int i = 0; i < 4; ++i)
-    if (!make_map(&a.x[i], *X, 0, 0, 128 >> i)) return HIMUON_ERR_CUDA;
+    if ((128 >> i) <= half && !make_map(&a.x[i], *X, 0, 0, 128 >> i)) return HIMUON_ERR_CUDA;
   a.K = static_cast<int32_t>(X->cols);
   a.M = static_cast<int32_t>(Y->cols);
   a.N = 0;
@@ -1627,7 +1674,7 @@ extern "C" {
 
 int himuon_expert_product(const himuon_mat *X, const himuon_mat *W, int32_t n, const int32_t *offsets, int32_t w_trans,
                           const himuon_mat *Y, void *stream) {
-  if (!X || !W || !Y || n < 1 || (!offsets && n != 1) || (w_trans != 0 && w_trans != 1)) return HIMUON_ERR_INVALID;
+  if (!X || !W || !Y || n < 1 || n > kMaxGroups || (!offsets && n != 1) || (w_trans != 0 && w_trans != 1)) return HIMUON_ERR_INVALID;
   int rc = check_operand(*X, 0);
   if (!rc) rc = check_operand(*Y, 0);
   if (!rc) rc = check_list(W, n);
@@ -1635,7 +1682,7 @@ int himuon_expert_product(const himuon_mat *X, const himuon_mat *W, int32_t n, c
   if (!is16(X->dtype) || !is_float(Y->dtype)) return HIMUON_ERR_UNSUPPORTED;
   if (W->dtype != X->dtype || Y->rows != X->rows) return HIMUON_ERR_INVALID;
   if ((w_trans ? W->cols : W->rows) != X->cols || (w_trans ? W->rows : W->cols) != Y->cols) return HIMUON_ERR_INVALID;
-  rc = device_usable();
+  rc = expert_device();
   if (rc) return rc;
   return run_product(X, nullptr, W, nullptr, n, offsets, w_trans, Y, static_cast<cudaStream_t>(stream));
 }
@@ -1643,7 +1690,7 @@ int himuon_expert_product(const himuon_mat *X, const himuon_mat *W, int32_t n, c
 int himuon_expert_product_i8(const himuon_mat *X, const himuon_mat *x_scale, const himuon_mat *W,
                              const himuon_mat *w_scale, int32_t n, const int32_t *offsets, const himuon_mat *Y,
                              void *stream) {
-  if (!X || !W || !Y || n < 1 || (!offsets && n != 1)) return HIMUON_ERR_INVALID;
+  if (!X || !W || !Y || n < 1 || n > kMaxGroups || (!offsets && n != 1)) return HIMUON_ERR_INVALID;
   int rc = check_operand(*X, 0);
   if (!rc) rc = check_operand(*Y, 0);
   if (!rc) rc = check_list(W, n);
@@ -1653,7 +1700,7 @@ int himuon_expert_product_i8(const himuon_mat *X, const himuon_mat *x_scale, con
   if (X->dtype != HIMUON_I8 || W->dtype != HIMUON_I8 || !is_float(Y->dtype)) return HIMUON_ERR_UNSUPPORTED;
   if (W->cols != X->cols || W->rows != Y->cols || Y->rows != X->rows) return HIMUON_ERR_INVALID;
   if (X->cols > 131071) return HIMUON_ERR_UNSUPPORTED;   // 2^14 per term: the sum stays inside int32
-  rc = device_usable();
+  rc = expert_device();
   if (rc) return rc;
   return run_product(X, static_cast<const float *>(x_scale->data), W, w_scale, n, offsets, 1, Y,
                      static_cast<cudaStream_t>(stream));
@@ -1661,7 +1708,7 @@ int himuon_expert_product_i8(const himuon_mat *X, const himuon_mat *x_scale, con
 
 int himuon_expert_gradient(const himuon_mat *A, const himuon_mat *B, int32_t n, const int32_t *offsets, float alpha,
                            float beta, const himuon_mat *C, const himuon_mat *G, void *stream) {
-  if (!A || !B || !G || n < 1 || (!offsets && n != 1)) return HIMUON_ERR_INVALID;
+  if (!A || !B || !G || n < 1 || n > kMaxGroups || (!offsets && n != 1)) return HIMUON_ERR_INVALID;
   if (!isfinite(alpha) || !isfinite(beta) || (!C && beta != 0.f)) return HIMUON_ERR_INVALID;
   int rc = check_operand(*A, 0);
   if (!rc) rc = check_operand(*B, 0);
@@ -1682,7 +1729,7 @@ int himuon_expert_gradient(const himuon_mat *A, const himuon_mat *B, int32_t n, 
     std::sort(seen.begin(), seen.end());
     if (std::adjacent_find(seen.begin(), seen.end()) != seen.end()) return HIMUON_ERR_INVALID;
   }
-  rc = device_usable();
+  rc = expert_device();
   if (rc) return rc;
   if (beta == 0.f) C = nullptr;
   const bool st = g_stacked && (!C || stacked(C, n, &c_stride));
@@ -1710,7 +1757,7 @@ int himuon_quantize(const himuon_mat *in, int32_t n, int32_t dim, const himuon_m
     if (codes[e].rows != (dim ? in[e].cols : in[e].rows) || codes[e].cols != (dim ? in[e].rows : in[e].cols))
       return HIMUON_ERR_INVALID;
   }
-  const int rc = device_usable();
+  const int rc = expert_device();
   if (rc) return rc;
   for (int32_t e0 = 0; e0 < n; e0 += kMaxList) {
     const int32_t cnt = std::min(n - e0, kMaxList);

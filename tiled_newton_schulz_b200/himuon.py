@@ -9,6 +9,7 @@ the built library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Sequence
 
@@ -261,26 +262,30 @@ def momentum_step(W, M, G, mu: float, lr: float, p: Params, splits=None, update_
 
 
 # ---------------------------------------------------------------- expert products
+@functools.lru_cache(maxsize=256)
+def _stack_layout(n: int, rows: int, cols: int, ld: int, dtype: int, step: int):
+    """The records of n matrices `step` bytes apart as five 64-bit words each,
+    the first matrix at address 0."""
+    import numpy as np
+    rec = np.empty((n, 5), np.int64)
+    rec[:, 0] = np.arange(n) * step
+    rec[:, 1:] = (rows, cols, ld, dtype)
+    return rec
+
+
 def _stack(ts):
     """(himuon_mat array, its address, n) of a list of 2-D tensors or of a 3-D
-    tensor of stacked matrices (unit column stride).
-
-    The records of stacked matrices are filled as five 64-bit words each (a
-    few array operations instead of one ctypes record per matrix).
-    """
-    if hasattr(ts, "dim"):
-        import numpy as np
-        stride = ts.stride()
-        if len(stride) != 3 or stride[2] != 1:
-            raise ValueError("stacked matrices are a 3-D tensor with unit column stride")
-        n, rows, cols = ts.shape
-        rec = np.empty((n, 5), np.int64)
-        rec[:, 1:] = (rows, cols, stride[1], _dtype_code(ts))
-        base, step = ts.data_ptr(), stride[0] * ts.element_size()
-        rec[:, 0] = np.arange(base, base + n * step, step) if step else base
-        return rec, rec.ctypes.data, n
-    arr = _mats(ts)
-    return arr, ctypes.addressof(arr), len(ts)
+    tensor of stacked matrices (unit column stride)."""
+    if isinstance(ts, (list, tuple)):
+        arr = _mats(ts)
+        return arr, ctypes.addressof(arr), len(ts)
+    stride = ts.stride()
+    if len(stride) != 3 or stride[2] != 1:
+        raise ValueError("stacked matrices are a 3-D tensor with unit column stride")
+    n, rows, cols = ts.shape
+    rec = _stack_layout(n, rows, cols, stride[1], _dtype_code(ts), stride[0] * ts.element_size()).copy()
+    rec[:, 0] += ts.data_ptr()
+    return rec, rec.ctypes.data, n
 
 
 def _row_vector(t) -> Mat:
@@ -293,23 +298,23 @@ def _row_vector(t) -> Mat:
 def _one_device(*operands) -> int:
     """The index of the CUDA device that every tensor of the operands (tensors,
     lists of them or None) is on."""
-    dev = -1
+    devs = set()
     for op in operands:
-        for t in (op if isinstance(op, (list, tuple)) else (op,)):
-            if t is None:
-                continue
-            d = t.get_device()
-            if d < 0 or (dev >= 0 and d != dev):
-                raise ValueError("expert products need all their tensors on one CUDA device")
-            dev = d
+        if isinstance(op, (list, tuple)):
+            devs.update([t.get_device() for t in op])
+        elif op is not None:
+            devs.add(op.get_device())
+    dev = devs.pop() if len(devs) == 1 else -1
+    if dev < 0:
+        raise ValueError("expert products need all their tensors on one CUDA device")
     return dev
 
 
 def _offsets(offsets, n):
-    import torch
     if offsets is None:
         return None
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() != n + 1 or not offsets.is_contiguous():
+    import torch
+    if offsets.dtype is not torch.int32 or offsets.shape != (n + 1,) or not offsets.is_contiguous():
         raise ValueError(f"offsets are a contiguous int32 tensor of n + 1 = {n + 1} entries")
     return offsets.data_ptr()
 
