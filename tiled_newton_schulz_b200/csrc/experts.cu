@@ -170,12 +170,14 @@ __device__ __forceinline__ int32_t bound_at(const int32_t *offsets, int32_t i, i
 }
 
 __device__ __forceinline__ int32_t round32(int32_t x) { return (x + 31) / 32 * 32; }
-// A group of cnt rows runs as ceil(cnt / 2^shift) tiles of equal width (a
-// multiple of 32: the pair's CTAs hold half of the rows each, in boxes of 16).
+// A group of cnt rows runs as ceil(cnt / 2^shift) tiles, its units of 32 rows
+// (the pair's CTAs hold half of them each, in boxes of 16) dealt out as evenly
+// as they go: tiles of equal width would pad up to 31 rows each (16381 rows of 61
+// experts, 1024 -> 4096, a tenth of the MMAs' columns).
 __device__ __forceinline__ int32_t row_tiles(int32_t cnt, int32_t shift) { return (cnt + (1 << shift) - 1) >> shift; }
-__device__ __forceinline__ int32_t tile_width(int32_t cnt, int32_t shift) {
-  const int32_t mt = row_tiles(cnt, shift);
-  return mt <= 1 ? round32(cnt) : round32((cnt + mt - 1) / mt);
+__device__ __forceinline__ int32_t tile_width(int32_t cnt, int32_t shift) {   // the widest
+  const int32_t mt = row_tiles(cnt, shift), units = (cnt + 31) / 32;
+  return 32 * (mt <= 1 ? units : (units + mt - 1) / mt);
 }
 
 struct Tile {
@@ -214,7 +216,6 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int
     }
     const int32_t lo = bound_at(a.offsets, t.e, a.rows), hi = max(lo, bound_at(a.offsets, t.e + 1, a.rows));
     const int32_t cnt = hi - lo, mt = row_tiles(cnt, a.cap);
-    t.width = tile_width(cnt, a.cap);
     // bands of up to 8 row tiles, row tile fastest: the tiles in flight share
     // a few panels of W and of X
     const int32_t r = idx - start[t.e] * mt_m;
@@ -222,7 +223,9 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int
     const int32_t gm = min(8, mt - 8 * g), mc = gm == 1 ? rr : rr / gm;
     const int32_t tt = 8 * g + rr - mc * gm;
     t.m0 = mc * kTileM;
-    t.n0 = lo + tt * t.width;
+    const int32_t units = (cnt + 31) / 32, each = mt <= 1 ? units : units / mt, more = units - each * mt;
+    t.width = 32 * (each + (tt < more ? 1 : 0));
+    t.n0 = lo + 32 * (tt * each + min(tt, more));
     t.valid = min(t.width, hi - t.n0);
     t.k0 = 0;
     t.len = a.K;
