@@ -239,23 +239,6 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int
   return t;
 }
 
-__device__ __forceinline__ void ld4_any(const char *p, int32_t dtype, int64_t i, float (&v)[4]) {
-  if (dtype == HIMUON_FP32) {
-    const float4 f = *reinterpret_cast<const float4 *>(p + 4 * i);
-    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-  } else {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p + 2 * i);
-    float2 a, b;
-    if (dtype == HIMUON_FP16) {
-      a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
-      b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
-    } else {
-      a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.x));
-      b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.y));
-    }
-    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-  }
-}
 // The product's output: 32 rows of Y x 32 channels, of which `rows` x `cols`
 // are inside.  A lane comes with one channel of every row and leaves with runs
 // of a row: the block is turned through the warp's buffer (16-byte chunk c of
@@ -1046,6 +1029,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
+// SMs of the current device (looked up once per device).
+int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  int sms = known[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    known[dev].store(sms, std::memory_order_relaxed);
+  }
+  return sms;
+}
+
 struct QuantArgs {
   const void *in[kMaxList];
   int8_t *codes[kMaxList];
@@ -1063,6 +1059,10 @@ struct QuantArgs {
 // element: the kernel is bound by its instructions (the plain division took 464
 // us for 8192 x 11008 bf16).  A maximum so small or large that hi or x hi could
 // leave fp32's range takes the division, scaled by a power of two.
+__device__ __forceinline__ uint32_t near_code(float x, float hi, float lo) {   // the code in the low byte
+  const float p = x * hi;
+  return __float_as_uint(p + fmaf(x, lo, fmaf(x, hi, -p)) + 12582912.f);
+}
 struct Coder {
   float hi, lo, top;
   __device__ explicit Coder(float t) {
@@ -1071,15 +1071,11 @@ struct Coder {
     lo = __fdiv_rn(fmaf(-t, hi, 127.f), t);
   }
   __device__ __forceinline__ bool in_range() const { return top >= 0x1p-60f && top <= 0x1p60f; }
-  __device__ __forceinline__ uint32_t near_code(float x) const {   // the code in the low byte
-    const float p = x * hi;
-    return __float_as_uint(p + fmaf(x, lo, fmaf(x, hi, -p)) + 12582912.f);
-  }
   __device__ __forceinline__ uint32_t far_code(float x) const {
     const float mul = top > 1.f ? 0x1p-100f : 0x1p100f;
     return __float_as_uint(__fdiv_rn(127.f * (x * mul), top * mul) + 12582912.f);
   }
-  __device__ __forceinline__ uint32_t operator()(float x) const { return in_range() ? near_code(x) : far_code(x); }
+  __device__ __forceinline__ uint32_t operator()(float x) const { return in_range() ? near_code(x, hi, lo) : far_code(x); }
 };
 __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
@@ -1093,12 +1089,6 @@ __device__ __forceinline__ float line_scale(uint32_t top_bits) {
   return top_bits < 0x7f800000u ? __fdiv_rn(__uint_as_float(top_bits), 127.f) : __uint_as_float(0x7fffffffu);
 }
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
-// 8 consecutive elements (16-byte aligned for 16-bit types, 32 for fp32)
-__device__ __forceinline__ void ld8_any(const void *p, int32_t dtype, int64_t i, float (&v)[8]) {
-  ld4_any(static_cast<const char *>(p), dtype, i, *reinterpret_cast<float(*)[4]>(&v[0]));
-  ld4_any(static_cast<const char *>(p), dtype, i + 4, *reinterpret_cast<float(*)[4]>(&v[4]));
-}
 
 // One scale per row: TPR threads per row.  The row stays in registers between
 // the two passes (kHold runs of 8 elements per thread, all loads in flight
@@ -1125,6 +1115,29 @@ struct Run8 {   // 8 consecutive elements as loaded (16 bits)
     const __half2 h = *reinterpret_cast<const __half2 *>(&w);
     return j & 1 ? __high2float(h) : __low2float(h);
   }
+  __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load_some(const char *p, int64_t i, int n) {   // n < 8 elements from element i on
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) w[j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[i + j]) << (16 * (j & 1));
+    u = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // the 8 columns' maxima, in pairs until unpack()
+  __device__ __forceinline__ void tops(uint32_t (&t)[8]) const {
+    const uint32_t m = 0x7fff7fffu;
+    t[0] = max_s16x2(t[0], u.x & m);
+    t[1] = max_s16x2(t[1], u.y & m);
+    t[2] = max_s16x2(t[2], u.z & m);
+    t[3] = max_s16x2(t[3], u.w & m);
+  }
+  static __device__ __forceinline__ void unpack(uint32_t (&t)[8]) {
+#pragma unroll
+    for (int j = 7; j >= 0; --j) {
+      const uint16_t h = static_cast<uint16_t>(j & 1 ? t[j / 2] >> 16 : t[j / 2] & 0xffffu);
+      t[j] = DT == HIMUON_FP16 ? abs_bits(__half2float(*reinterpret_cast<const __half *>(&h))) : uint32_t(h) << 16;
+    }
+  }
 };
 template <>
 struct Run8<HIMUON_FP32> {
@@ -1142,6 +1155,19 @@ struct Run8<HIMUON_FP32> {
     const float4 &f = j < 4 ? a : b;
     return (j & 3) == 0 ? f.x : (j & 3) == 1 ? f.y : (j & 3) == 2 ? f.z : f.w;
   }
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load_some(const char *p, int64_t i, int n) {
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = j < n ? reinterpret_cast<const float *>(p)[i + j] : 0.f;
+    a = make_float4(w[0], w[1], w[2], w[3]);
+    b = make_float4(w[4], w[5], w[6], w[7]);
+  }
+  __device__ __forceinline__ void tops(uint32_t (&t)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = max(t[j], abs_bits(get(j)));
+  }
+  static __device__ __forceinline__ void unpack(uint32_t (&)[8]) {}
 };
 template <int DT>
 constexpr int kHold = DT == HIMUON_FP32 ? 4 : 8;
@@ -1202,7 +1228,7 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const __grid_cons
   auto put8 = [&](int32_t i, const Run8<DT> &x) {
     uint32_t u[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = code.near_code(x.get(j));
+    for (int j = 0; j < 8; ++j) u[j] = near_code(x.get(j), code.hi, code.lo);
     *reinterpret_cast<uint2 *>(out + 8 * i) = make_uint2(bytes4(u[0], u[1], u[2], u[3]), bytes4(u[4], u[5], u[6], u[7]));
   };
 #pragma unroll
@@ -1213,31 +1239,151 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const __grid_cons
     w.load(in, i);
     put8(i, w);
   }
-  for (int64_t i = 8ll * runs + t; i < cols; i += TPR) out[i] = static_cast<int8_t>(code.near_code(ld_any(in, DT, i)));
+  for (int64_t i = 8ll * runs + t; i < cols; i += TPR) out[i] = static_cast<int8_t>(near_code(ld_any(in, DT, i), code.hi, code.lo));
+}
+
+// One scale per column, codes transposed.  A cluster takes 64 columns (128 bytes
+// of a 16-bit row) and deals their rows, 128 at a time, over its CTAs (up to
+// eight: a matrix of 4096 x 1024 has only 16 such column blocks).  The first pass
+// finds the columns' maxima, joined over distributed shared memory; the second,
+// from L2, codes the same rows: a thread takes 8 columns of 4 rows, packs each
+// column's four codes into a word and the words are turned through shared
+// memory, so that a warp stores 128 rows of a column at once.
+constexpr int kTurnPitch = 33;   // words; with the columns' rotation below free of bank conflicts
+template <int DT>
+__global__ void __launch_bounds__(256) quantize_cols_kernel(const __grid_constant__ QuantArgs a) {
+  __shared__ uint32_t tops[64];
+  __shared__ uint32_t turn[64 * kTurnPitch];
+  grid_start_next();
+  grid_wait();
+  const int32_t z = blockIdx.z;
+  if (a.dtype[z] != DT) return;   // (the same for the whole cluster)
+  const int64_t c0 = blockIdx.x * 64ll;
+  const int64_t rows = a.rows[z], cols = a.cols[z], ld = a.ld[z];
+  if (c0 >= cols) return;
+  const int32_t part = blockIdx.y, parts = gridDim.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c8 = lane & 7, rg = warp * 4 + (lane >> 3);   // 8 columns, rows 4 rg .. 4 rg + 3 of a block
+  const int64_t c = c0 + 8 * c8;
+  const bool whole = c + 8 <= cols;
+  const char *in = static_cast<const char *>(a.in[z]) + c * (DT == HIMUON_FP32 ? 4 : 2);
+  auto load = [&](int64_t r, Run8<DT> &x) {   // (zeros where there is nothing)
+    if (r >= rows) x.clear();
+    else if (whole) x.load(in + r * ld * (DT == HIMUON_FP32 ? 4 : 2), 0);
+    else x.load_some(static_cast<const char *>(a.in[z]), r * ld + c, static_cast<int>(cols - c));
+  };
+  if (threadIdx.x < 64) tops[threadIdx.x] = 0;
+  __syncthreads();
+  {
+    uint32_t top[8] = {};   // 16 bits: pairs of columns in the first four
+    for (int64_t b = part * 128ll; b < rows; b += parts * 128ll) {
+      Run8<DT> x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) load(b + 4 * rg + k, x[k]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k].tops(top);
+    }
+    Run8<DT>::unpack(top);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 8));
+      top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
+      if (lane < 8) atomicMax(&tops[8 * c8 + j], top[j]);
+    }
+  }
+  cluster_sync_all();
+  uint32_t mine = 0;
+  if (threadIdx.x < 64)
+    for (int32_t p = 0; p < parts; ++p) {
+      uint32_t v;
+      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(&tops[threadIdx.x]), p)));
+      mine = max(mine, v);
+    }
+  cluster_sync_all();
+  if (threadIdx.x < 64) {
+    tops[threadIdx.x] = mine;
+    if (part == 0 && c0 + threadIdx.x < cols) a.scale[z][c0 + threadIdx.x] = line_scale(mine);
+  }
+  __syncthreads();
+  float hi[8], lo[8];
+  bool near = true;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t top = tops[8 * c8 + j];
+    const Coder code(line_ok(top) ? __uint_as_float(top) : 1.f);
+    hi[j] = code.hi;
+    lo[j] = code.lo;
+    near = near && (line_ok(top) || top == 0) && code.in_range();   // (top 0: all zeros, whose codes are 0)
+  }
+  for (int64_t b = part * 128ll; b < rows; b += parts * 128ll) {
+    Run8<DT> x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) load(b + 4 * rg + k, x[k]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t u[4];
+      if (near) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[k] = near_code(x[k].get(j), hi[j], lo[j]);
+      } else {
+        const uint32_t top = tops[8 * c8 + j];
+        const Coder code(line_ok(top) ? __uint_as_float(top) : 1.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[k] = line_ok(top) ? code(x[k].get(j)) : 0;
+      }
+      turn[(8 * c8 + j) * kTurnPitch + ((rg + 4 * (c8 >> 2)) & 31)] = bytes4(u[0], u[1], u[2], u[3]);
+    }
+    __syncthreads();
+    const int64_t r = b + 4 * lane;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = 8 * warp + j;
+      const uint32_t w = turn[col * kTurnPitch + ((lane + 4 * (warp >> 2)) & 31)];
+      if (c0 + col >= cols || r >= rows) continue;
+      int8_t *out = a.codes[z] + (c0 + col) * a.ldq[z] + r;
+      if (r + 4 <= rows) *reinterpret_cast<uint32_t *>(out) = w;
+      else
+        for (int k = 0; r + k < rows; ++k) out[k] = static_cast<int8_t>(w >> (8 * k));
+    }
+    __syncthreads();
+  }
 }
 
 template <typename Kern>
-void launch_quant(Kern kern, dim3 grid, const QuantArgs &a, cudaStream_t st) {
+void launch_quant(Kern kern, dim3 grid, unsigned cluster_y, const QuantArgs &a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(256);
   cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = attr[1].val.clusterDim.z = 1;
+  attr[1].val.clusterDim.y = cluster_y;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   count_launch();
   cudaLaunchKernelEx(&cfg, kern, a);   // (its error is read by the caller)
 }
 
+// Columns of matrices of at most `most` columns and `tallest` rows.
 template <int DT>
-bool load_rows_kernels() {
+void quantize_cols(const QuantArgs &a, int64_t most, int64_t tallest, unsigned zs, cudaStream_t st) {
+  // rows are dealt out only as far as the column blocks leave SMs without work
+  unsigned parts = 1;
+  while (parts < 8 && parts * 128ll < tallest && (most + 63) / 64 * zs * parts < 4 * sm_count()) parts *= 2;
+  launch_quant(quantize_cols_kernel<DT>, dim3(static_cast<unsigned>((most + 63) / 64), parts, zs), parts, a, st);
+}
+
+template <int DT>
+bool load_quant_kernels() {
   cudaFuncAttributes f;
   return cudaFuncGetAttributes(&f, quantize_rows_kernel<DT, 32>) == cudaSuccess &&
          cudaFuncGetAttributes(&f, quantize_rows_kernel<DT, 64>) == cudaSuccess &&
          cudaFuncGetAttributes(&f, quantize_rows_kernel<DT, 128>) == cudaSuccess &&
-         cudaFuncGetAttributes(&f, quantize_rows_kernel<DT, 256>) == cudaSuccess;
+         cudaFuncGetAttributes(&f, quantize_rows_kernel<DT, 256>) == cudaSuccess &&
+         cudaFuncGetAttributes(&f, quantize_cols_kernel<DT>) == cudaSuccess;
 }
 
 // Rows of at most `widest` columns: the fewest threads per row that hold it.
@@ -1245,82 +1391,12 @@ template <int DT>
 void quantize_rows(const QuantArgs &a, int64_t most, int64_t widest, unsigned zs, cudaStream_t st) {
   const int64_t per = 8 * kHold<DT>;
   auto go = [&](auto kern, int tpr) {
-    launch_quant(kern, dim3(static_cast<unsigned>((most + 256 / tpr - 1) / (256 / tpr)), zs), a, st);
+    launch_quant(kern, dim3(static_cast<unsigned>((most + 256 / tpr - 1) / (256 / tpr)), zs), 1, a, st);
   };
   if (widest <= 32 * per) go(quantize_rows_kernel<DT, 32>, 32);
   else if (widest <= 64 * per) go(quantize_rows_kernel<DT, 64>, 64);
   else if (widest <= 128 * per) go(quantize_rows_kernel<DT, 128>, 128);
   else go(quantize_rows_kernel<DT, 256>, 256);
-}
-
-// One scale per column, codes transposed: a CTA takes 64 columns (128 bytes of
-// a 16-bit row); the first pass finds the columns' maxima, the second (from
-// L2) codes blocks of 128 rows and turns them through shared memory.
-__global__ void __launch_bounds__(256) quantize_cols_kernel(const __grid_constant__ QuantArgs a) {
-  __shared__ uint32_t tops[8][64];
-  __shared__ __align__(16) int8_t turn[64][128 + 16];
-  grid_start_next();
-  grid_wait();
-  const int32_t z = blockIdx.y;
-  const int64_t c0 = blockIdx.x * 64ll;
-  const int64_t rows = a.rows[z], cols = a.cols[z], ld = a.ld[z];
-  if (c0 >= cols) return;
-  const int32_t dt = a.dtype[z];
-  const int c8 = threadIdx.x & 7, r0 = threadIdx.x >> 3;   // 8 columns, 32 rows at a time
-  const int64_t c = c0 + 8 * c8;
-  const bool whole = c + 8 <= cols;
-  auto load = [&](int64_t r, float(&x)[8]) {
-    if (whole) ld8_any(a.in[z], dt, r * ld + c, x);
-    else
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = c + j < cols ? ld_any(a.in[z], dt, r * ld + c + j) : 0.f;
-  };
-  uint32_t top[8] = {};
-#pragma unroll 4
-  for (int64_t r = r0; r < rows; r += 32) {
-    float x[8];
-    load(r, x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top[j] = max(top[j], abs_bits(x[j]));
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 8));
-    top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
-    if ((threadIdx.x & 31) < 8) tops[threadIdx.x >> 5][8 * c8 + j] = top[j];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-#pragma unroll
-    for (int w = 0; w < 8; ++w) top[j] = max(top[j], tops[w][8 * c8 + j]);
-    if (r0 == 0 && c + j < cols) a.scale[z][c + j] = line_scale(top[j]);
-  }
-  for (int64_t b = 0; b < rows; b += 128) {
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t r = b + r0 + 32 * k;
-      if (r >= rows) continue;
-      float x[8];
-      load(r, x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bool ok = line_ok(top[j]);
-        turn[8 * c8 + j][r0 + 32 * k] = ok ? static_cast<int8_t>(Coder(__uint_as_float(top[j]))(x[j])) : 0;
-      }
-    }
-    __syncthreads();
-    const int64_t in = min(rows - b, (int64_t)128);
-    for (int i = threadIdx.x; i < 64 * 8; i += 256) {   // 16 rows of a column at a time
-      const int col = i >> 3, r = (i & 7) * 16;
-      if (c0 + col >= cols || r >= in) continue;
-      int8_t *out = a.codes[z] + (c0 + col) * a.ldq[z] + b + r;
-      if (r + 16 <= in) *reinterpret_cast<uint4 *>(out) = *reinterpret_cast<const uint4 *>(&turn[col][r]);
-      else
-        for (int k = 0; r + k < in; ++k) out[k] = turn[col][r + k];
-    }
-  }
 }
 
 // ---------------------------------------------------------------- argument checks
@@ -1440,19 +1516,6 @@ bool stacked(const himuon_mat *m, int32_t n, int64_t *stride) {
   return true;
 }
 
-// SMs of the current device (looked up once per device).
-int sm_count() {
-  static std::atomic<int> known[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  int sms = known[dev].load(std::memory_order_relaxed);
-  if (sms == 0) {
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    known[dev].store(sms, std::memory_order_relaxed);
-  }
-  return sms;
-}
-
 // Every variant of the kernel is loaded, and allowed its shared memory, at the
 // first call on a device: a call captured into a graph later loads nothing.
 template <int KIND, int A_MN, int GRAD, int PREC, int SPLIT>
@@ -1468,14 +1531,12 @@ bool load_kernels() {
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (loaded.load(std::memory_order_relaxed) & bit) return true;
-  cudaFuncAttributes f;
   const bool ok =
       load_variant<0, 0, 0, 0, 0>() && load_variant<0, 0, 0, 1, 0>() && load_variant<0, 0, 0, 1, 1>() &&
       load_variant<0, 1, 0, 0, 0>() && load_variant<0, 1, 0, 1, 0>() && load_variant<0, 1, 0, 1, 1>() &&
       load_variant<1, 0, 0, 0, 0>() && load_variant<1, 0, 0, 1, 1>() && load_variant<0, 1, 1, 0, 0>() &&
       load_variant<0, 1, 1, 1, 0>() && load_variant<0, 1, 1, 1, 1>() && device_status_word() != nullptr &&
-      cudaFuncGetAttributes(&f, quantize_cols_kernel) == cudaSuccess && load_rows_kernels<HIMUON_BF16>() &&
-      load_rows_kernels<HIMUON_FP16>() && load_rows_kernels<HIMUON_FP32>();
+      load_quant_kernels<HIMUON_BF16>() && load_quant_kernels<HIMUON_FP16>() && load_quant_kernels<HIMUON_FP32>();
   if (ok) loaded.fetch_or(bit, std::memory_order_relaxed);
   return ok;
 }
@@ -1766,7 +1827,7 @@ int himuon_quantize(const himuon_mat *in, int32_t n, int32_t dim, const himuon_m
     const int32_t cnt = std::min(n - e0, kMaxList);
     QuantArgs a;
     a.dim = dim;
-    int64_t most = 0, widest = 0;
+    int64_t most = 0, widest = 0, tallest = 0;
     bool any[3] = {false, false, false};
     for (int32_t e = 0; e < cnt; ++e) {
       const himuon_mat &m = in[e0 + e];
@@ -1780,14 +1841,18 @@ int himuon_quantize(const himuon_mat *in, int32_t n, int32_t dim, const himuon_m
       a.dtype[e] = m.dtype;
       most = std::max(most, dim ? m.cols : m.rows);
       widest = std::max(widest, m.cols);
+      tallest = std::max(tallest, m.rows);
       any[m.dtype] = true;
     }
     if (most == 0) continue;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const unsigned zs = static_cast<unsigned>(cnt);
+    // one launch per storage type among the call's matrices
     if (dim) {
-      launch_quant(quantize_cols_kernel, dim3(static_cast<unsigned>((most + 63) / 64), zs), a, st);
-    } else {   // one launch per storage type among the call's matrices
+      if (any[HIMUON_BF16]) quantize_cols<HIMUON_BF16>(a, most, tallest, zs, st);
+      if (any[HIMUON_FP16]) quantize_cols<HIMUON_FP16>(a, most, tallest, zs, st);
+      if (any[HIMUON_FP32]) quantize_cols<HIMUON_FP32>(a, most, tallest, zs, st);
+    } else {
       if (any[HIMUON_BF16]) quantize_rows<HIMUON_BF16>(a, most, widest, zs, st);
       if (any[HIMUON_FP16]) quantize_rows<HIMUON_FP16>(a, most, widest, zs, st);
       if (any[HIMUON_FP32]) quantize_rows<HIMUON_FP32>(a, most, widest, zs, st);
