@@ -504,6 +504,37 @@ def test_product_i8_edges(hm):
 
 
 # ---------------------------------------------------------------- how they are called
+@pytest.mark.parametrize("op", ["product", "product_few_tiles", "gradient", "gradient_few_tiles"])
+def test_device_timeout_is_reported_and_the_next_call_is_right(hm, op):
+    """HIMUON_TEST_STALL=1 makes the first pair's MMA warp wait on a barrier that nothing arrives on: every other wait
+    of its cluster then runs out too (two seconds), the kernel ends, and the status says so."""
+    import os
+    g = gen(31)
+    few = op.endswith("few_tiles")
+    K, N, rows = 1024, 256 if few else 8192, 300
+    X, W, dY = (matrix(s, torch.bfloat16, g) for s in ((rows, K), (1, K, N), (rows, N)))
+    Y, C = torch.zeros(rows, N, device=DEV), matrix((1, K, N), torch.float32, g)
+    G = torch.zeros(1, K, N, device=DEV)
+    run = (lambda: hm.expert_product(X, W, Y)) if op.startswith("product") else \
+        (lambda: hm.expert_gradient(X, dY, G, beta=1.0, C=C))
+    assert hm.device_status() == 0
+    os.environ["HIMUON_TEST_STALL"] = "1"
+    try:
+        run()
+        status = hm.device_status()
+    finally:
+        del os.environ["HIMUON_TEST_STALL"]
+    assert status == -6                                                          # HIMUON_ERR_TIMEOUT
+    assert hm.device_status() == 0
+    run()
+    x, w, dy = X.double(), W[0].double(), dY.double()
+    if op.startswith("product"):
+        close(Y, x @ w, x.abs() @ w.abs(), K, torch.float32)
+    else:
+        close(G[0], x.T @ dy + C[0].double(), x.abs().T @ dy.abs() + C[0].double().abs(), rows, torch.float32)
+    assert hm.device_status() == 0
+
+
 def test_bad_offsets_are_reported_and_stay_in_bounds(hm):
     g = gen(11)
     X, W = matrix((40, 64), torch.bfloat16, g), matrix((3, 64, 32), torch.bfloat16, g)
