@@ -448,6 +448,21 @@ def test_quantize_lists_and_nonfinite(hm):
     hm.quantize([tiny[:0]], [q[:0]], [s[:0]])
 
 
+@pytest.mark.parametrize("dim", [0, 1])
+def test_quantize_stacked(hm, dim):
+    """Stacked matrices, codes and scales give what the lists give."""
+    x = matrix((5, 96, 136), torch.bfloat16, gen(41), margin=8)
+    L, n = (136, 96) if dim else (96, 136)
+    q, q2 = (torch.full((5, L, -(-n // 16) * 16 + 16), 99, dtype=torch.int8, device=DEV)[:, :, :n] for _ in range(2))
+    s, s2 = (torch.zeros(5, L + 4, device=DEV)[:, :L] for _ in range(2))
+    hm.quantize(x, q, s, dim=dim)
+    hm.quantize(list(x), list(q2), list(s2), dim=dim)
+    assert torch.equal(q, q2) and torch.equal(s, s2) and (s > 0).all()
+    for e in range(5):
+        want, top = exact_codes(x[e].T if dim else x[e])
+        assert torch.equal(q[e].double(), want.round()) and torch.equal(s[e], (top / 127).float())
+
+
 def check_i8(hm, out, K, N, counts, start=0, behind=0, listed=False, full=False, seed=0):
     g = gen(seed)
     n, off = len(counts), offsets(counts, start)
@@ -604,6 +619,40 @@ def test_streams_and_graph_replay_with_new_offsets(hm):
         for y, gr in (*outs, (y2, g2)):
             assert torch.equal(y, w[0]) and torch.equal(gr, w[1])
     assert hm.device_status() == 0
+
+
+def test_calls_from_several_host_threads(hm):
+    """Each thread on its own stream, calls of every kind at once."""
+    import threading
+    g = gen(42)
+    X, W = matrix((700, 256), torch.bfloat16, g), matrix((6, 256, 320), torch.bfloat16, g)
+    off = offsets([100, 0, 255, 45, 299, 1])
+    want = torch.zeros(700, 320, device=DEV)
+    hm.expert_product(X, W, want, off)
+    want_g = torch.zeros(6, 256, 256, device=DEV)
+    hm.expert_gradient(X, X, want_g, off)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            y, gr = torch.zeros(700, 320, device=DEV), torch.zeros(6, 256, 256, device=DEV)
+            q, qs = torch.zeros(700, 256, dtype=torch.int8, device=DEV), torch.zeros(700, device=DEV)
+            for _ in range(20):
+                hm.expert_product(X, list(W), y, off)
+                hm.expert_gradient(X, X, gr, off)
+                hm.quantize([X], [q], [qs])
+            s.synchronize()
+            if not (torch.equal(y, want) and torch.equal(gr, want_g) and bool(q.abs().amax(1).eq(127).all())):
+                bad.append(1)
+
+    ts = [threading.Thread(target=work) for _ in range(4)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad and hm.device_status() == 0
 
 
 def test_results_do_not_depend_on_other_groups_or_repeat(hm):

@@ -371,15 +371,21 @@ def quantize(inputs, codes, scales, dim: int = 0, stream=None) -> None:
     """8-bit codes of each matrix: one scale per row (dim 0), or per column
     with the codes transposed (dim 1).
 
-    inputs: list of 2-D float tensors; codes: int8 tensors (transposed shape
-    for dim 1); scales: 1-D fp32 tensors.
+    inputs: list of 2-D float tensors, or a 3-D tensor of stacked matrices;
+    codes: int8, likewise (transposed shape for dim 1); scales: list of 1-D fp32
+    tensors, or a 2-D tensor with a row per matrix.
     """
     if not len(inputs) == len(codes) == len(scales):
         raise ValueError("inputs, codes and scales differ in length")
-    dev = _one_device(list(inputs), list(codes), list(scales))
-    n = len(inputs)
-    sc = (Mat * max(1, n))(*[_row_vector(s) for s in scales])
-    _on_device(dev, "himuon_quantize", stream, _mats(inputs), n, int(dim), _mats(codes), sc)
+    dev = _one_device(inputs, codes, scales)
+    keep_i, i, n = _stack(inputs)
+    keep_c, c, _ = _stack(codes)
+    if isinstance(scales, (list, tuple)):
+        keep_s = (Mat * max(1, n))(*[_row_vector(s) for s in scales])
+        s = ctypes.addressof(keep_s)
+    else:
+        keep_s, s, _ = _stack(scales.unsqueeze(1))
+    _on_device(dev, "himuon_quantize", stream, i, n, int(dim), c, s)
 
 
 def expert_product_i8(X, x_scale, W, w_scale, Y, offsets=None, stream=None) -> None:
