@@ -216,6 +216,8 @@ def test_product_shared_matrix_and_nonfinite_rows(hm):
     Y = torch.empty(50, 96, device=DEV, dtype=torch.bfloat16)
     hm.expert_product(X, [W1, W1], Y, off)
     want = Y.clone()
+    hm.expert_product(X, W1.expand(2, -1, -1), Y, off)
+    assert torch.equal(Y, want)
     X[7, 3], X[20, 159] = float("nan"), float("inf")
     hm.expert_product(X, [W1, W1], Y, off)
     keep = [r for r in range(50) if r not in (7, 20)]
@@ -618,6 +620,56 @@ def test_streams_and_graph_replay_with_new_offsets(hm):
         torch.cuda.synchronize()
         for y, gr in (*outs, (y2, g2)):
             assert torch.equal(y, w[0]) and torch.equal(gr, w[1])
+    assert hm.device_status() == 0
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_launches_wait_for_work_of_other_streams_and_of_torch(hm, captured):
+    """A launch may start under the end of the one before it, but not ahead of what its stream waits for: inputs that
+    another stream, a torch kernel or a copy writes between two calls, and outputs that a torch kernel reads."""
+    g = gen(43)
+    src = [matrix((512, 512), torch.bfloat16, g, fill=0.0) for _ in range(4)]
+    big = torch.randn(3000, 3000, generator=g, device=DEV)
+    X, W = torch.zeros(512, 512, dtype=torch.bfloat16, device=DEV), matrix((2, 512, 256), torch.bfloat16, g)
+    off = offsets([200, 312])
+    Y = torch.zeros(512, 256, device=DEV)
+    keep = [torch.zeros(512, 256, device=DEV) for _ in range(8)]
+    slow = torch.zeros(3000, 3000, device=DEV)
+    other = torch.cuda.Stream()
+
+    def work():
+        main = torch.cuda.current_stream()
+        for i in range(8):
+            other.wait_stream(main)
+            with torch.cuda.stream(other):
+                torch.mm(big, big, out=slow)          # long enough for a call that does not wait to be early
+                if i % 2:
+                    X.copy_(src[i % 4])
+                else:
+                    torch.add(src[i % 4], 0, out=X)
+            hm.expert_product(src[0], W, Y, off)      # the launch before, with nothing to wait for
+            main.wait_stream(other)
+            hm.expert_product(X, W, Y, off)
+            keep[i].copy_(Y)
+
+    if captured:
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            work()
+        torch.cuda.synchronize()
+        for k in keep:
+            k.zero_()
+        gph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gph):
+            work()
+        gph.replay()
+    else:
+        work()
+    torch.cuda.synchronize()
+    for i in range(8):
+        want = torch.zeros(512, 256, device=DEV)
+        hm.expert_product(src[i % 4], W, want, off)
+        assert torch.equal(keep[i], want), i
     assert hm.device_status() == 0
 
 
