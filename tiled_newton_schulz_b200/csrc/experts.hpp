@@ -69,11 +69,6 @@ __device__ __forceinline__ float ld_any(const void *p, int32_t dtype, int64_t i)
   if (dtype == HIMUON_FP16) return __half2float(static_cast<const __half *>(p)[i]);
   return static_cast<const float *>(p)[i];
 }
-__device__ __forceinline__ void st_any(void *p, int32_t dtype, int64_t i, float v) {
-  if (dtype == HIMUON_BF16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
-  else if (dtype == HIMUON_FP16) static_cast<__half *>(p)[i] = __float2half_rn(v);
-  else static_cast<float *>(p)[i] = v;
-}
 
 // The expert entry points' launches follow one another without a gap: a kernel
 // lets the next one start as soon as its CTAs have (its first part, which touches no memory of

@@ -341,6 +341,29 @@ __device__ __forceinline__ void box_write(uint8_t *buf, int lane, int32_t dtype,
     box_write16<__nv_bfloat162>(buf, lane, k0, wide, v);
   }
 }
+// A box to memory by the warp, `rows` x `cols` of it: runs of 16 bytes, and single
+// elements in the last column's run.
+__device__ __forceinline__ void box_copy(const uint8_t *buf, int lane, int32_t dtype, int32_t box_cols, char *out,
+                                         int64_t at, int64_t ld, int32_t rows, int32_t cols) {
+  const int es = dtype == HIMUON_FP32 ? 4 : 2, per = 16 / es, runs = box_cols * es / 16;   // 4 or 8 runs per row
+  const int run = lane % runs, have = min(per, cols - run * per);
+  if (have <= 0) return;
+  for (int r = lane / runs; r < rows; r += 32 / runs) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(buf + box_at(r, run, runs == 8));
+    char *o = out + (at + r * ld + run * per) * es;
+    if (have == per) {
+      *reinterpret_cast<uint4 *>(o) = u;
+    } else {
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j >= have) break;
+        if (es == 4) reinterpret_cast<uint32_t *>(o)[j] = w[j & 3];
+        else reinterpret_cast<uint16_t *>(o)[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+      }
+    }
+  }
+}
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int32_t x, int32_t y, int32_t z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
                "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
@@ -769,8 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t c_bytes = bc * (a.cdtype == HIMUON_FP32 ? 128 : 64);
     // A box that reaches over the last column is stored up to the end of that
     // column's 16 bytes (observed: columns behind it in the row's pitch were
-    // overwritten); where G's width is no multiple of 16 bytes the last boxes
-    // are stored element by element.
+    // overwritten); where G's width is no multiple of 16 bytes the warp copies
+    // the last boxes itself.
     const bool whole_runs = a.N % (a.odtype == HIMUON_FP32 ? 4 : 8) == 0;
     struct Box {
       int32_t idx, i;   // tile, column group; idx >= n_tiles: none left
@@ -837,15 +860,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] *= a.alpha;
           }
-          if (by_box) {
-            box_write(box, lane, a.odtype, 4 * h, bc == 64, v);
-          } else if (m + lane < a.M) {
-            char *o = (NOUT > 1 ? a.out[t.e] : a.out[0] + t.e * a.out_stride);
-            const int64_t at0 = (m + lane) * a.ldo + n0 + 32 * h;
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (n0 + 32 * h + k < a.N) st_any(o, a.odtype, at0 + k, v[k]);
-          }
+          box_write(box, lane, a.odtype, 4 * h, bc == 64, v);
+        }
+        if (!by_box) {
+          __syncwarp();
+          box_copy(box, lane, a.odtype, bc, (NOUT > 1 ? a.out[t.e] : a.out[0] + t.e * a.out_stride), m * a.ldo + n0,
+                   a.ldo, min(32, a.M - m), a.N - n0);
         }
         fence_proxy_async_smem();
         __syncwarp();
