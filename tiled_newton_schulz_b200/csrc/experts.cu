@@ -110,6 +110,35 @@ bool load_variant() {
          cudaFuncSetAttribute(expert_kernel<KIND, A_MN, GRAD, GRAD ? 1 : kMaxList, GRAD ? kMaxList : 1, PREC, SPLIT>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess;
 }
+// How many clusters of `split` pairs run at once: fewer than the pairs would
+// make, since a cluster lives inside one of the device's processor clusters
+// (148 SMs hold 74 pairs, but not 37 clusters of four SMs or 18 of eight).
+// A property of the device; 0 if it cannot be had.
+std::atomic<int32_t> cluster_room[64][2];
+int32_t clusters_at_once(int32_t split) {
+  if (split == 1) return sm_count() / 2;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::atomic<int32_t> *known = dev < 64 ? &cluster_room[dev][split / 4] : nullptr;
+  if (known && known->load(std::memory_order_relaxed)) return known->load(std::memory_order_relaxed);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * split);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2 * split;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int room = 0;
+  if (cudaOccupancyMaxActiveClusters(&room, expert_kernel<0, 0, 0, 1, 1, 1, 1>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (known) known->store(room, std::memory_order_relaxed);
+  return room;
+}
 bool load_kernels() {
   static std::atomic<uint64_t> loaded{0};   // a bit per device
   int dev = 0;
@@ -121,7 +150,7 @@ bool load_kernels() {
       load_variant<0, 1, 0, 0, 0>() && load_variant<0, 1, 0, 1, 0>() && load_variant<0, 1, 0, 1, 1>() &&
       load_variant<1, 0, 0, 0, 0>() && load_variant<1, 0, 0, 1, 1>() && load_variant<0, 1, 1, 0, 0>() &&
       load_variant<0, 1, 1, 1, 0>() && load_variant<0, 1, 1, 1, 1>() && device_status_word() != nullptr &&
-      load_quantize();
+      load_quantize() && clusters_at_once(2) >= 0 && clusters_at_once(4) >= 0;
   if (ok) loaded.fetch_or(bit, std::memory_order_relaxed);
   return ok;
 }
@@ -146,13 +175,15 @@ int launch_mma(const MmaArgs<NMAP, NOUT> &a, int64_t most_tiles, cudaStream_t st
   return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? HIMUON_OK : HIMUON_ERR_CUDA;
 }
 
-// How many pairs share a tile (1, 2 or 4): as many as the call's tiles, at most
-// `tiles`, leave pairs for, each with at least 4 blocks of the longest sum.
-int32_t split_of(int64_t tiles, int64_t blocks) {
-  const int64_t pairs = sm_count() / 2;
-  for (int32_t s = 4; s > 1; s /= 2)
-    if (tiles * s <= pairs && blocks >= 4 * s) return s;
-  return 1;
+// What a call of `tiles` tiles costs, in blocks of the sum, if `split` pairs (1, 2
+// or 4) share a tile of `blocks`: the rounds, times a pair's share and `join` for
+// starting the clusters and adding up.  Shared tiles run in one round only: a
+// second would start its clusters anew (3 rows, 20000 -> 10240, bf16: 72 us with
+// one pair per tile, 92 with four in three rounds).
+int64_t split_cost(int64_t tiles, int64_t blocks, int32_t split, int64_t join) {
+  const int64_t room = clusters_at_once(split);
+  if (room < 1 || (split > 1 && tiles > room)) return INT64_MAX;
+  return (tiles + room - 1) / room * ((blocks + split - 1) / split + join);
 }
 
 template <int NMAP, int NOUT>
@@ -222,7 +253,20 @@ int product_launch(const himuon_mat *X, const float *x_scale, const himuon_mat *
   const int64_t most = most_tiles(1 << a.cap);
   a.mt_m = static_cast<int32_t>(mt_m);
   a.mt_n = 0;
-  a.split = split_of(most, (X->cols * static_cast<int64_t>(size_of(X->dtype)) + 127) / 128);
+  // Pairs share tiles where that is the shortest.  (A row, bf16, one pair, two and
+  // four per tile: 4096 -> 4096, 16 tiles, 16.6, 13.1 and 20.2 us, since 16 clusters
+  // of eight SMs do not run at once; 14336 -> 1024 44.5, 27.7 and 17.8; 1024 -> 4096
+  // 8.4, 8.8 and 16.6.)
+  if (a.cap == 7 || X->rows <= 128) {
+    const int64_t blocks = (X->cols * static_cast<int64_t>(size_of(X->dtype)) + 127) / 128;
+    int64_t best = split_cost(most, blocks, 1, 0);
+    for (int32_t s = 2; s <= 4; s *= 2) {
+      const int64_t cost = split_cost(most, blocks, s, s == 2 ? 12 : 16);
+      if (cost >= best) continue;
+      best = cost;
+      a.split = s;
+    }
+  }
   const bool fp32 = Y->dtype == HIMUON_FP32;
   if (X->dtype == HIMUON_I8)
     return a.split > 1 ? launch_mma<1, 0, 0, 1, 1>(a, most, stream) : launch_mma<1, 0, 0, 0, 0>(a, most, stream);
@@ -275,27 +319,38 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
   a.alpha = alpha;
   a.beta = beta;
   a.has_c = C != nullptr;
-  // Columns of a tile: as few tiles as 256 columns allow, or more of equal
-  // width where that fills the last round of the pairs better (a tile costs its
-  // columns and about as much as 64 more), in whole boxes of the epilogue.
+  // Columns of a tile, and pairs that share one: as few tiles as 256 columns
+  // allow, or more of equal width, in whole boxes of the epilogue, where that
+  // fills the last round of the pairs better.  A block of the sum costs a pair
+  // the tile's columns, 128 at least, and as much as 192 more (0.20 us at up to 128
+  // columns, 0.22 at 192, 0.29 at 256).  (bf16, 14808 rows 64 x 1408: one tile per
+  // pair 48.7 us at 128 columns, four pairs per tile 22.0; 8192 rows 1024 x 1024
+  // 31.4, and 25.0 with two; 8 groups of 512 rows 512 x 512 9.0, and 19.8 with two.)
   const bool wide = G->dtype == HIMUON_FP32 || (C && C->dtype == HIMUON_FP32);
   a.box_cols = wide ? 32 : 64;
   const int64_t m_tiles = n * ((A->cols + kTileM - 1) / kTileM), pairs = sm_count() / 2;
   const int64_t fewest = (B->cols + kTileN - 1) / kTileN;
+  const int64_t blocks = (A->rows + 64 * n - 1) / (64 * static_cast<int64_t>(n));   // of an even group
   int64_t best = INT64_MAX, most = 0;
   for (int64_t c = fewest; c <= 4 * fewest; ++c) {
-    const int64_t w = ((B->cols + c - 1) / c + a.box_cols - 1) / a.box_cols * a.box_cols;
-    const int64_t tiles = m_tiles * ((B->cols + w - 1) / w), cost = (tiles + pairs - 1) / pairs * (w + 64);
-    if (cost < best) {
+    for (int32_t s = 1; s <= 4; s *= 2) {
+      const int64_t box = s == 1 ? a.box_cols : 32;
+      const int64_t w = ((B->cols + c - 1) / c + box - 1) / box * box;
+      if (s > 1 && (w > 128 || blocks < 4 * s)) continue;
+      const int64_t tiles = m_tiles * ((B->cols + w - 1) / w), each = std::max<int64_t>(w, 128) + 192;
+      int64_t cost = split_cost(tiles, blocks, s, s == 1 ? 0 : s == 2 ? 17 : 25);
+      if (cost == INT64_MAX) continue;
+      cost = cost * each + (s == 1 ? (tiles + pairs - 1) / pairs * 10 * w : 0);   // (and a tile's way out)
+      if (cost >= best) continue;
       best = cost;
       most = tiles;
+      a.split = s;
       a.cap = static_cast<int32_t>(w);
       a.mt_n = static_cast<int32_t>(tiles / m_tiles);
     }
-    if (tiles >= 6 * pairs) break;
+    if (most >= 6 * pairs) break;
   }
   a.mt_m = static_cast<int32_t>(m_tiles / n);
-  a.split = split_of(most, (A->rows + 63) / 64);
   if (a.split > 1) a.box_cols = 32;
   for (int32_t i = 0; i < (NOUT > 1 ? n : 1); ++i) {
     if (!make_map(&a.g[i], G[e0 + i], NOUT > 1 ? 1 : n, g_stride, 32, a.box_cols)) return HIMUON_ERR_CUDA;
@@ -306,7 +361,7 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
   a.out_stride = g_stride;
   a.odtype = G->dtype;
   if (C) a.cdtype = C->dtype;
-  a.buffers = C ? 3 : 1;
+  a.buffers = C && a.split == 1 ? 3 : 1;   // (a split tile's warps have one box each)
   if (a.split > 1) return launch_mma<0, 1, 1, 1, 1>(a, most, stream);
   return G->dtype == HIMUON_FP32 ? launch_mma<0, 1, 1, 1, 0>(a, most, stream) : launch_mma<0, 1, 1, 0, 0>(a, most, stream);
 }

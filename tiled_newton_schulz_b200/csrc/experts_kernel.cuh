@@ -433,11 +433,11 @@ __device__ __forceinline__ void plan_rows(const Args &a, int32_t *start, int32_t
 
 // PREC: an epilogue warp's column groups half, half + 2, .. (below `in`) of
 // accumulator piece p, added to its running sums.
-template <int PREC>
-__device__ __forceinline__ void read_pieces(float (&sum)[PREC ? 4 : 1][32], uint32_t taddr, int half, int32_t in,
+template <int GROUPS>
+__device__ __forceinline__ void read_pieces(float (&sum)[GROUPS][32], uint32_t taddr, int half, int32_t in,
                                             int32_t p, bool none) {
 #pragma unroll
-  for (int g = 0; g < (PREC ? 4 : 1); ++g) {
+  for (int g = 0; g < GROUPS; ++g) {
     const int32_t i = half + 2 * g;
     if (i >= in) continue;
     if (none) {
@@ -460,23 +460,20 @@ __device__ __forceinline__ void read_pieces(float (&sum)[PREC ? 4 : 1][32], uint
 }
 
 // SPLIT: adds up the slices' sums of a tile.  Column group g of a warp belongs
-// to the pair g % split; every other pair's warp sends it its part over
-// distributed shared memory, into the ring (free by then: the first cluster
-// barrier follows every pair's last MMA), and the owner adds the parts in the
-// order of the slices, whatever their order of arrival.  4 KB per part: chunk k
-// (16 bytes) of lane l at k * 512 + 16 l.
-template <int KIND, int PREC>
-__device__ __forceinline__ void join_slices(float (&sum)[PREC ? 4 : 1][32], uint8_t *ring, int w, int lane, int half,
+// to the pair g % split; every pair's warp sends it its part over distributed
+// shared memory, into the ring (free by then: the first cluster barrier follows
+// every pair's last MMA), and the owner adds the parts in the order of the
+// slices, whatever their order of arrival.  A warp has two groups at most and
+// owns one: 4 KB per slice and warp, chunk k (16 bytes) of lane l at k * 512 + 16 l.
+template <int GROUPS>
+__device__ __forceinline__ void send_slices(float (&sum)[GROUPS][32], uint8_t *ring, int w, int lane, int half,
                                             int32_t in, int32_t rank, int32_t slice, int32_t split) {
-  const int per = 4 / split;   // groups that a warp owns
   __syncwarp();
   cluster_sync_all();
 #pragma unroll
-  for (int g = 0; g < (PREC ? 4 : 1); ++g) {
-    const int owner = g % split;
-    if (half + 2 * g >= in || owner == slice) continue;
-    const uint32_t to =
-        mapa_shared(smem_u32(ring + ((slice * per + g / split) * kEpiWarps + w) * kStageOut), 2 * owner + rank) + 16 * lane;
+  for (int g = 0; g < GROUPS; ++g) {
+    if (half + 2 * g >= in) continue;
+    const uint32_t to = mapa_shared(smem_u32(ring + (slice * kEpiWarps + w) * kStageOut), 2 * (g % split) + rank) + 16 * lane;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       st_cluster_v4(to + 512 * k, make_uint4(__float_as_uint(sum[g][4 * k]), __float_as_uint(sum[g][4 * k + 1]),
@@ -484,28 +481,26 @@ __device__ __forceinline__ void join_slices(float (&sum)[PREC ? 4 : 1][32], uint
   }
   __syncwarp();
   cluster_sync_all();
+}
+// The total of the column group that the warp owns.
+template <int KIND>
+__device__ __forceinline__ void add_slices(float (&v)[32], const uint8_t *ring, int w, int lane, int32_t split) {
+  const uint8_t *part = ring + w * kStageOut + 16 * lane;
 #pragma unroll
-  for (int g = 0; g < (PREC ? 4 : 1); ++g) {
-    if (half + 2 * g >= in || g % split != slice) continue;
-    float total[32];
-    for (int from = 0; from < split; ++from) {
-      const uint8_t *part = ring + ((from * per + g / split) * kEpiWarps + w) * kStageOut + 16 * lane;
+  for (int k = 0; k < 8; ++k) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float4 f = from == slice ? make_float4(sum[g][4 * k], sum[g][4 * k + 1], sum[g][4 * k + 2], sum[g][4 * k + 3])
-                                       : *reinterpret_cast<const float4 *>(part + 512 * k);
-        const float x[4] = {f.x, f.y, f.z, f.w};
+    for (int from = 0; from < 4; ++from) {
+      if (from >= split) break;
+      const float4 f = *reinterpret_cast<const float4 *>(part + from * kEpiWarps * kStageOut + 512 * k);
+      const float x[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float &t = total[4 * k + c];
-          if (from == 0) t = x[c];
-          else if (KIND) t = __int_as_float(__float_as_int(t) + __float_as_int(x[c]));
-          else t += x[c];
-        }
+      for (int c = 0; c < 4; ++c) {
+        float &t = v[4 * k + c];
+        if (from == 0) t = x[c];
+        else if (KIND) t = __int_as_float(__float_as_int(t) + __float_as_int(x[c]));
+        else t += x[c];
       }
     }
-#pragma unroll
-    for (int k = 0; k < 32; ++k) sum[g][k] = total[k];
   }
 }
 
@@ -513,7 +508,7 @@ __device__ __forceinline__ void join_slices(float (&sum)[PREC ? 4 : 1][32], uint
 // MN-major (W stored K x channels; the gradient's operands).  PREC: sums in
 // pieces of kChunk blocks (fp32 results).
 // SPLIT: the cluster's pairs share one tile, each a stretch of its sum (calls of
-// few tiles); comes with PREC's running sums in registers.
+// few tiles of 128 columns at most); comes with PREC's running sums in registers.
 //
 // A pair of CTAs (cluster of 2) works on one 256-row tile of D: each CTA holds
 // 128 of its rows (in its tensor memory) and of A's, and half of B's columns;
@@ -531,7 +526,7 @@ template <int KIND, int A_MN, int GRAD, int NMAP, int NOUT, int PREC, int SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_kernel(const __grid_constant__ MmaArgs<NMAP, NOUT> a) {
   constexpr int kElems = KIND ? 128 : 64;   // K elements per block of 128 bytes
-  constexpr int kSub = GRAD && PREC ? 1 : 2;   // blocks per stage
+  constexpr int kSub = GRAD && PREC && !SPLIT ? 1 : 2;   // blocks per stage
   constexpr int kStageK = kElems * kSub;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -548,6 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t *start = reinterpret_cast<int32_t *>(sm + kData + kBarBytes);   // [n + 1]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr bool kPieces = PREC && !KIND;   // (int32 sums are exact)
+  constexpr int kGroups = !PREC ? 1 : SPLIT ? 2 : 4;   // PREC: 32-column groups of an epilogue warp's sums
+  constexpr bool kMoved = PREC && (GRAD || !SPLIT);    // registers move to the epilogue
   const int32_t cta = static_cast<int32_t>(cluster_ctarank());
   const int32_t rank = cta & 1, even = cta & ~1, slice = SPLIT ? cta >> 1 : 0;
   const uint16_t pair_mask = static_cast<uint16_t>(3u << even);
@@ -589,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // PREC: the epilogue's running sums take 128 registers per thread: 3 x 168
   // per thread of the three warpgroups become 56 + 2 x 224
   if (warp == 0) {
-    if (PREC) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (kMoved) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     const uint32_t full0 = mapa_shared(smem_u32(full), even);
     int s = 0;
     uint32_t phase = 1;   // parity of the stage's last release; the first round finds it free
@@ -676,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int64_t i = max((int64_t)0, issued - stages); i < issued; ++i)
         warp_wait(full + i % stages, static_cast<uint32_t>((i / stages) & 1), a.status);
   } else if (warp == 1) {
-    if (PREC) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (kMoved) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (rank == 0) {
       // descriptors of stage 0, without the address
       const uint64_t a_bits = A_MN ? sw128_desc(0, 8192, 1024) : sw128_desc(0, 16, 1024);
@@ -752,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_wait(done, 0, a.status);
     }
   } else if (warp < 4) {
-    if (PREC) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (kMoved) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 3 && rank == 1) {
       // Passes the odd CTA's "drained" on to the even one.  An arrival there
       // waits for the thread's earlier stores to be performed (cluster scope,
@@ -776,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (GRAD) {
-    if (PREC) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if (kMoved) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // This warp's boxes of G, 32 rows x 32 or 64 columns, in the order of its tiles
     // and, inside one, of the columns.  With C, the boxes of C come by TMA up
     // to two ahead of the one at work, also from the next tile, and the result
@@ -879,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         at = at + 1 == a.buffers ? 0 : at + 1;
       };
       const int32_t pieces = kPieces ? max(1, (t.len + kChunk * kElems - 1) / (kChunk * kElems)) : 1;
-      float sum[PREC ? 4 : 1][32];
+      float sum[kGroups][32];
       for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
         const int b = j & 1;
         if (!(ok = warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status))) break;
@@ -891,11 +888,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) mbar_arrive(freed + b);
         };
         if (PREC && (SPLIT || pieces > 1)) {
-          read_pieces<PREC>(sum, taddr, half, in, p, t.len == 0);
+          read_pieces(sum, taddr, half, in, p, t.len == 0);
           release();
           if (!SPLIT && p + 1 == pieces) {
 #pragma unroll
-            for (int g = 0; g < (PREC ? 4 : 1); ++g)
+            for (int g = 0; g < kGroups; ++g)
               if (half + 2 * g < in && ok)
                 emit(half + 2 * g, [&](int, float(&v)[32]) {
 #pragma unroll
@@ -919,14 +916,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (SPLIT) {
-        join_slices<KIND, PREC>(sum, sm, warp - 4, lane, half, in, rank, slice, a.split);
-#pragma unroll
-        for (int g = 0; g < (PREC ? 4 : 1); ++g)
-          if (half + 2 * g < in && g % a.split == slice && ok)
-            emit(half + 2 * g, [&](int, float(&v)[32]) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = sum[g][k];
-            });
+        send_slices(sum, sm, warp - 4, lane, half, in, rank, slice, a.split);
+        if (half + 2 * slice < in && ok)
+          emit(half + 2 * slice, [&](int, float(&v)[32]) { add_slices<KIND>(v, sm, warp - 4, lane, a.split); });
       }
     }
     if (SPLIT && first >= n_tiles) {   // the cluster has no tile: keep step with its barriers
@@ -934,11 +926,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       cluster_sync_all();
     }
     if (!ok && a.has_c) {   // gave up: what was loaded ahead lands before the CTA ends (bounded)
-      for (int k = 0; k < 3; ++k) warp_wait(landed + k, (c_phase >> k) & 1, a.status);
+      for (int k = 0; k < a.buffers; ++k) warp_wait(landed + k, (c_phase >> k) & 1, a.status);
     }
     if (elect_one()) bulk_wait0();
   } else {
-    if (PREC) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if (kMoved) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int q = warp & 3;             // TMEM lanes 32 q .. 32 q + 31
     const int half = (warp - 4) >> 2;   // the warp's 32-column groups: half, half + 2, ..
     float *st = reinterpret_cast<float *>(sm + ring + (warp - 4) * kStageOut);
@@ -973,14 +965,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      reinterpret_cast<uint16_t *>(a.out[0]) + o, a.ldo, r_in, m_in);
       };
       const int32_t pieces = kPieces ? (t.len + kChunk * kElems - 1) / (kChunk * kElems) : 1;
-      float sum[PREC ? 4 : 1][32];
+      float sum[kGroups][32];
       for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
         const int b = j & 1;
         if (!(ok = warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status))) break;
         tc_fence_after();
         const uint32_t taddr = tmem + static_cast<uint32_t>(b * kTileN) + (static_cast<uint32_t>(q * 32) << 16);
         if (PREC && (SPLIT || pieces > 1)) {
-          read_pieces<PREC>(sum, taddr, half, in, p, false);
+          read_pieces(sum, taddr, half, in, p, false);
         } else {
 #pragma unroll 1
           for (int32_t i = half; i < in; i += 2) {
@@ -994,15 +986,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) mbar_arrive(freed + b);
         if (PREC && !SPLIT && pieces > 1 && p + 1 == pieces) {
 #pragma unroll
-          for (int g = 0; g < (PREC ? 4 : 1); ++g)
+          for (int g = 0; g < kGroups; ++g)
             if (half + 2 * g < in) emit(half + 2 * g, sum[g]);
         }
       }
       if (SPLIT) {
-        join_slices<KIND, PREC>(sum, sm, warp - 4, lane, half, in, rank, slice, a.split);
-#pragma unroll
-        for (int g = 0; g < (PREC ? 4 : 1); ++g)
-          if (half + 2 * g < in && g % a.split == slice) emit(half + 2 * g, sum[g]);
+        send_slices(sum, sm, warp - 4, lane, half, in, rank, slice, a.split);
+        if (half + 2 * slice < in) {
+          float v[32];
+          add_slices<KIND>(v, sm, warp - 4, lane, a.split);
+          emit(half + 2 * slice, v);
+        }
       }
     }
     if (SPLIT && first >= n_tiles) {   // the cluster has no tile: keep step with its barriers
@@ -1010,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cluster_sync_all();
     }
   }
-  if (SPLIT && warp < 4) {   // the two barriers of join_slices
+  if (SPLIT && warp < 4) {   // the two barriers of send_slices
     __syncwarp();
     cluster_sync_all();
     cluster_sync_all();
