@@ -236,6 +236,7 @@ int product_launch(const himuon_mat *X, const float *x_scale, const himuon_mat *
     a.w_scale = static_cast<const float *>(w_scale->data) + e0 * w_scale->ld;
     a.ld_scale = w_scale->ld;
   }
+  if (Y->dtype == HIMUON_FP32 && !make_map(&a.g[0], *Y, 0, 0, 16, 32)) return HIMUON_ERR_CUDA;
   a.out[0] = static_cast<char *>(Y->data);
   a.ldo = Y->ld;
   a.odtype = Y->dtype;
