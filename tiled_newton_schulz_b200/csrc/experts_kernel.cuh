@@ -160,15 +160,13 @@ struct Tile {
   int32_t k0, len;  // the sums' stretch: product, of K; gradient, rows (of the slice, where a tile is split)
 };
 
-// Tile `idx` of the launch, found by a whole warp.  `from`: a group not after
-// the tile's (the last one found: a role's tiles come in order).
-template <int GRAD, int SPLIT, int kElems, typename Args>
-__device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int32_t slice, int32_t idx, int32_t from) {
+// Tile `idx` of the launch: the same for the whole warp (ALONE), or each lane's own.
+template <int GRAD, int SPLIT, int kElems, bool ALONE, typename Args>
+__device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int32_t slice, int32_t idx) {
   Tile t;
-  const int32_t mt_m = a.mt_m;
+  const uint32_t mt_m = a.mt_m, u = static_cast<uint32_t>(idx) / mt_m;
   if (GRAD) {
-    const int32_t u = idx / mt_m;
-    t.e = u / a.mt_n;
+    t.e = u / static_cast<uint32_t>(a.mt_n);
     t.m0 = (idx - u * mt_m) * kTileM;
     t.n0 = (u - t.e * a.mt_n) * a.cap;
     t.valid = min(a.cap, a.N - t.n0);
@@ -176,22 +174,30 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int
     t.k0 = bound_at(a.offsets, t.e, a.rows);
     t.len = max(0, bound_at(a.offsets, t.e + 1, a.rows) - t.k0);
   } else {
-    // the group whose row tiles hold row tile idx / mt_m: the last with start[e] <= it
-    const int32_t u = idx / mt_m, lane = threadIdx.x & 31;
-    for (;; from += 32) {
-      const uint32_t before = __ballot_sync(0xffffffffu, from + 1 + lane < a.n && start[from + 1 + lane] <= u);
-      if (before != 0xffffffffu) {
-        t.e = from + __popc(before);
+    // the group whose row tiles hold row tile u: the last with start[e] <= u
+    t.e = 0;
+    if (ALONE) {
+      for (const int lane = threadIdx.x & 31;; t.e += 32) {
+        const int32_t e = t.e + 1 + lane;
+        const uint32_t before = __ballot_sync(0xffffffffu, e < a.n && start[e] <= static_cast<int32_t>(u));
+        if (before == 0xffffffffu) continue;
+        t.e += __popc(before);
         break;
+      }
+    } else {
+      for (int32_t end = a.n; end - t.e > 1;) {
+        const int32_t mid = (t.e + end) / 2;
+        if (start[mid] <= static_cast<int32_t>(u)) t.e = mid;
+        else end = mid;
       }
     }
     const int32_t lo = bound_at(a.offsets, t.e, a.rows), hi = max(lo, bound_at(a.offsets, t.e + 1, a.rows));
     const int32_t cnt = hi - lo, mt = row_tiles(cnt, a.cap);
     // bands of up to 8 row tiles, row tile fastest: the tiles in flight share
     // a few panels of W and of X
-    const int32_t r = idx - start[t.e] * mt_m;
-    const int32_t g = mt <= 8 ? 0 : r / (8 * mt_m), rr = r - g * 8 * mt_m;
-    const int32_t gm = min(8, mt - 8 * g), mc = gm == 1 ? rr : rr / gm;
+    const uint32_t r = idx - start[t.e] * mt_m;
+    const uint32_t g = mt <= 8 ? 0 : r / (8 * mt_m), rr = r - g * 8 * mt_m;
+    const uint32_t gm = min(8, mt - 8 * static_cast<int32_t>(g)), mc = gm == 1 ? rr : rr / gm;
     const int32_t tt = 8 * g + rr - mc * gm;
     t.m0 = mc * kTileM;
     const int32_t units = (cnt + 31) / 32, each = mt <= 1 ? units : units / mt, more = units - each * mt;
@@ -209,6 +215,40 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int
   }
   return t;
 }
+
+// A role's tiles in order: first, first + step, ..  Finding one takes about 1200
+// cycles of divisions and loads, a fifth of a tile of a short sum; so the lanes of
+// the warp find one each, 32 tiles ahead, and hand them round.  A product's first
+// one, which the launch waits for, is found by the whole warp.  (bf16, 7052 rows
+// 128 -> 10968 55 -> 48 us, 16381 rows of 61 groups 1024 -> 4096 151 -> 148;
+// gradients of 79 groups, 4688 rows, 4325 x 553, 235 -> 226; calls of a few tiles
+// per pair are up to 2% slower.)
+// AHEAD = 0: one at a time, where the registers are taken.
+template <int GRAD, int SPLIT, int kElems, int AHEAD = 1>
+struct Tiles {
+  Tile own;
+  int32_t taken = 0;
+  template <typename Args>
+  __device__ __forceinline__ Tile next(const Args &a, const int32_t *start, int32_t slice, int32_t idx, int32_t step,
+                                       int32_t n_tiles) {
+    const int lane = threadIdx.x & 31, from = taken & 31;
+    if (!AHEAD || (!GRAD && idx < step)) return tile_at<GRAD, SPLIT, kElems, true>(a, start, slice, idx);
+    ++taken;
+    if (from == 0) {
+      const int64_t mine = min(idx + int64_t(step) * lane, int64_t(n_tiles) - 1);
+      own = tile_at<GRAD, SPLIT, kElems, false>(a, start, slice, static_cast<int32_t>(mine));
+    }
+    Tile t;
+    t.e = __shfl_sync(0xffffffffu, own.e, from);
+    t.m0 = __shfl_sync(0xffffffffu, own.m0, from);
+    t.n0 = __shfl_sync(0xffffffffu, own.n0, from);
+    t.valid = __shfl_sync(0xffffffffu, own.valid, from);
+    t.width = GRAD ? round32(t.valid) : __shfl_sync(0xffffffffu, own.width, from);
+    t.k0 = GRAD || SPLIT ? __shfl_sync(0xffffffffu, own.k0, from) : 0;
+    t.len = GRAD || SPLIT ? __shfl_sync(0xffffffffu, own.len, from) : a.K;
+    return t;
+  }
+};
 
 // The product's output: 32 rows of Y x 32 channels, of which `rows` x `cols`
 // are inside.  A lane comes with one channel of every row and leaves with runs
@@ -502,7 +542,8 @@ __device__ __forceinline__ void send_slices(float (&sum)[GROUPS][32], uint8_t *r
 #pragma unroll
   for (int g = 0; g < GROUPS; ++g) {
     if (half + 2 * g >= in) continue;
-    const uint32_t to = mapa_shared(smem_u32(ring + (slice * kEpiWarps + w) * kStageOut), 2 * (g % split) + rank) + 16 * lane;
+    const uint32_t part = smem_u32(ring + (slice * kEpiWarps + w) * kStageOut);
+    const uint32_t to = mapa_shared(part, 2 * (g % split) + rank) + 16 * lane;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       st_cluster_v4(to + 512 * k, make_uint4(__float_as_uint(sum[g][4 * k]), __float_as_uint(sum[g][4 * k + 1]),
@@ -621,12 +662,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 1;   // parity of the stage's last release; the first round finds it free
     bool ok = true;
     int64_t issued = 0;
+    Tiles<GRAD, SPLIT, kElems, !SPLIT && !(GRAD && PREC)> tiles;
     Tile t, next;
-    if (first < n_tiles) next = tile_at<GRAD, SPLIT, kElems>(a, start, slice, first, 0);
+    if (first < n_tiles) next = tiles.next(a, start, slice, first, step, n_tiles);
     for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
       t = next;
       const bool more = idx + step < n_tiles;   // the next tile is looked up behind this one's first block
-      if (more && t.len == 0) next = tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx + step, t.e);
+      if (more && t.len == 0) next = tiles.next(a, start, slice, idx + step, step, n_tiles);
       const int32_t len = t.len;
       const CUtensorMap *mw = NMAP > 1 ? &a.w[t.e] : &a.w[0];
       const int32_t z = NMAP > 1 ? 0 : t.e;
@@ -688,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
-        if (k == 0 && more) next = tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx + step, t.e);
+        if (k == 0 && more) next = tiles.next(a, start, slice, idx + step, step, n_tiles);
         ++issued;
         if (++s == stages) {
           s = 0;
@@ -712,12 +754,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       int32_t j = 0;
       bool ok = !a.stall || blockIdx.x != 0 || warp_wait(done, 0, a.status);
+      Tiles<GRAD, SPLIT, kElems, !SPLIT && !(GRAD && PREC)> tiles;
       Tile t, next;
-      if (first < n_tiles) next = tile_at<GRAD, SPLIT, kElems>(a, start, slice, first, 0);
+      if (first < n_tiles) next = tiles.next(a, start, slice, first, step, n_tiles);
       for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
         t = next;
         const bool more = idx + step < n_tiles;
-        if (more && t.len == 0) next = tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx + step, t.e);
+        if (more && t.len == 0) next = tiles.next(a, start, slice, idx + step, step, n_tiles);
         const int32_t len = t.len;
         const uint32_t idesc = a.idesc | (static_cast<uint32_t>(t.width >> 3) << 17);
         uint32_t d = 0;
@@ -765,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           if (left <= kStageK || (kPieces && (k + kStageK) % (kChunk * kElems) == 0)) hand_over();
-          if (k == 0 && more) next = tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx + step, t.e);
+          if (k == 0 && more) next = tiles.next(a, start, slice, idx + step, step, n_tiles);
           if (++s == stages) {
             s = 0;
             phase ^= 1;
@@ -785,11 +828,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // 1 to 2.5 thousand cycles beside a tile's stores); the epilogue's warps
       // arrive in their own CTA instead.
       const uint32_t free0 = mapa_shared(smem_u32(acc_empty), even);
-      const int32_t from = 0;
+      Tiles<GRAD, SPLIT, kElems, !SPLIT && !(GRAD && PREC)> tiles;
       int32_t j = 0;
       bool ok = true;
       for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
-        const int32_t len = GRAD || SPLIT ? tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx, from).len : a.K;
+        const int32_t len = GRAD || SPLIT ? tiles.next(a, start, slice, idx, step, n_tiles).len : a.K;
         const int32_t pieces = kPieces ? max(1, (len + kChunk * kElems - 1) / (kChunk * kElems)) : 1;
         for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
           const int b = j & 1;
@@ -821,6 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // overwritten); where G's width is no multiple of 16 bytes the warp copies
     // the last boxes itself.
     const bool whole_runs = a.N % (a.odtype == HIMUON_FP32 ? 4 : 8) == 0;
+    Tiles<GRAD, SPLIT, kElems, !PREC> tiles, c_tiles;   // at work; C's boxes
     struct Box {
       int32_t idx, i;   // tile, column group; idx >= n_tiles: none left
       Tile t;
@@ -832,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (x.idx < n_tiles && x.i >= groups(x.t)) {
         x.idx += step;
         x.i = i0;
-        if (x.idx < n_tiles) x.t = tile_at<GRAD, SPLIT, kElems>(a, start, slice, x.idx, 0);
+        if (x.idx < n_tiles) x.t = c_tiles.next(a, start, slice, x.idx, step, n_tiles);
       }
     };
     auto load_c = [&](Box &x, int at) {   // box x into buffer `at`, then on to the next box
@@ -848,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     Box ahead{first, i0, {}};
     if (a.has_c && first < n_tiles) {
-      ahead.t = tile_at<GRAD, SPLIT, kElems>(a, start, slice, first, 0);
+      ahead.t = c_tiles.next(a, start, slice, first, step, n_tiles);
       settle(ahead);
       load_c(ahead, 0);
       load_c(ahead, 1);
@@ -858,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int32_t j = 0;
     for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
-      const Tile t = tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx, 0);
+      const Tile t = tiles.next(a, start, slice, idx, step, n_tiles);
       const int32_t in = groups(t);
       // column group i: combine with C, store.  fetch(h, v): its 32-column
       // part h from the accumulator or the running sums.
@@ -965,11 +1009,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *st = reinterpret_cast<float *>(sm + ring + (warp - 4) * kStageOut);
     uint64_t *freed = rank == 0 ? acc_empty : drained;
     const bool whole_runs = a.M % 4 == 0;   // (a box stores 16 bytes at a time)
-    int32_t j = 0, from = 0;
+    int32_t j = 0;
+    Tiles<GRAD, SPLIT, kElems, !PREC> tiles;
     bool ok = true;
     for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
-      const Tile t = tile_at<GRAD, SPLIT, kElems>(a, start, slice, idx, from);
-      from = t.e;
+      const Tile t = tiles.next(a, start, slice, idx, step, n_tiles);
       const int32_t m = t.m0 + 128 * rank + 32 * q;   // this warp's 32 channels
       const int32_t m_in = min(32, a.M - m);
       float chan = 1.f;
