@@ -184,3 +184,45 @@ def test_stacked_matrices_are_described_as_the_list_is(lib):
     got = (hm.Mat * n).from_address(a)
     for g, e in zip(got, arr_):
         assert (g.data, g.rows, g.cols, g.ld, g.dtype) == (e.data, e.rows, e.cols, e.ld, e.dtype)
+
+
+def _blocks(text):
+    """(opening brace, closing brace, what stands before the opening one on its line or, for an else, `if ... else`)
+    of every block of a source text, comments and strings aside."""
+    import re
+    text = re.sub(r"//[^\n]*", lambda m: " " * len(m.group()), text)
+    text = re.sub(r'"(?:[^"\\\n]|\\.)*"', lambda m: '"' + " " * (len(m.group()) - 2) + '"', text)
+    out, stack = [], []
+    for i, c in enumerate(text):
+        if c == "{":
+            stack.append(i)
+        elif c == "}":
+            a = stack.pop()
+            out.append((a, i, text[text.rfind("\n", 0, a) + 1:a].strip()))
+    assert not stack
+    return out
+
+
+def test_register_moves_are_one_instruction_per_warpgroup():
+    """setmaxnreg is undefined unless all threads of a warpgroup run the same instruction, and an increase waits for
+    the decreases: one of each per kernel, in the blocks that tell the warpgroups apart and outside every branch
+    between the warps of one."""
+    import re
+    from tiled_newton_schulz_b200 import build
+    found = 0
+    for name in build.SOURCES + build.HEADERS:
+        with open(f"{build.CSRC}/{name}") as f:
+            text = f.read()
+        where = {d: [m.start() for m in re.finditer(rf"setmaxnreg\.{d}", text)] for d in ("dec", "inc")}
+        if not (where["dec"] or where["inc"]):
+            continue
+        found += 1
+        assert len(where["dec"]) == len(where["inc"]) == 1, name
+        blocks = _blocks(text)
+        around = {d: sorted((b for b in blocks if b[0] < w[0] < b[1]), reverse=True) for d, w in where.items()}
+        dec, inc = around["dec"][0], around["inc"][0]
+        assert dec[2] == "if (warp < 4)" and inc[2] == "} else"
+        assert text[dec[1]:inc[0] + 1] == "} else {"                      # the other warpgroups are the block's else
+        assert around["dec"][1] == around["inc"][1]                      # both directly in the kernel's body
+        assert around["dec"][1][2].startswith("expert_kernel(")
+    assert found == 1

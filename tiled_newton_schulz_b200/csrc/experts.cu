@@ -102,13 +102,18 @@ bool stacked(const himuon_mat *m, int32_t n, int64_t *stride) {
   return true;
 }
 
-// Loads both list forms of a variant of the kernel and allows them their shared memory.
+// Loads both list forms of a variant of the kernel, allows them their shared memory
+// and sees to it that they are launched with the registers that they move.
 template <int KIND, int A_MN, int GRAD, int PREC, int SPLIT>
 bool load_variant() {
-  return cudaFuncSetAttribute(expert_kernel<KIND, A_MN, GRAD, 1, 1, PREC, SPLIT>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess &&
-         cudaFuncSetAttribute(expert_kernel<KIND, A_MN, GRAD, GRAD ? 1 : kMaxList, GRAD ? kMaxList : 1, PREC, SPLIT>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess;
+  auto load = [](auto kern) {
+    cudaFuncAttributes f;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess &&
+           cudaFuncGetAttributes(&f, kern) == cudaSuccess &&
+           (!kMovesRegisters<GRAD, PREC, SPLIT> || f.numRegs >= kRegsLaunch);
+  };
+  return load(expert_kernel<KIND, A_MN, GRAD, 1, 1, PREC, SPLIT>) &&
+         load(expert_kernel<KIND, A_MN, GRAD, GRAD ? 1 : kMaxList, GRAD ? kMaxList : 1, PREC, SPLIT>);
 }
 // How many clusters of `split` pairs run at once: fewer than the pairs would
 // make, since a cluster lives inside one of the device's processor clusters

@@ -29,6 +29,14 @@ constexpr uint32_t kStageOut = 4096;    // an epilogue warp's buffer: 32 x 32 fp
 constexpr int kEpiWarps = 8;
 constexpr int kTileM = 256, kTileN = 256;   // a CTA pair's tile of D
 constexpr int kThreads = 128 + 32 * kEpiWarps;   // three warpgroups: loads and MMAs (warps 0, 1), epilogue (4..11)
+// Registers per thread of a kernel whose epilogue holds running sums: as launched,
+// and after the loading warpgroup has given its own to the two of the epilogue.  A
+// warpgroup that asks for more than the launch left over waits without an end, so
+// the host refuses a build with fewer at launch (load_variant).
+constexpr int kRegsLaunch = 168, kRegsLoad = 56, kRegsSums = 224;
+static_assert(kRegsLoad + 2 * kRegsSums <= 3 * kRegsLaunch, "registers of the three warpgroups");
+template <int GRAD, int PREC, int SPLIT>
+constexpr bool kMovesRegisters = PREC && (GRAD || !SPLIT);   // the variants that do
 // fp32 results of 16-bit operands: the tensor core's accumulator truncates at
 // every K = 16 step, which costs an fp32 result about 1e-8 of itself per step
 // (K = 1100: 1.1e-6 against 2.6e-7 for rounded fp32 sums).  Their sums are cut
@@ -614,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr bool kPieces = PREC && !KIND;   // (int32 sums are exact)
   constexpr int kGroups = !PREC ? 1 : SPLIT ? 2 : 4;   // PREC: 32-column groups of an epilogue warp's sums
-  constexpr bool kMoved = PREC && (GRAD || !SPLIT);    // registers move to the epilogue
+  constexpr bool kMoved = kMovesRegisters<GRAD, PREC, SPLIT>;
   const int32_t cta = static_cast<int32_t>(cluster_ctarank());
   const int32_t rank = cta & 1, even = cta & ~1, slice = SPLIT ? cta >> 1 : 0;
   const uint16_t pair_mask = static_cast<uint16_t>(3u << even);
@@ -653,176 +661,177 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t block_bytes = (kABytes + b_bytes + 1023) / 1024 * 1024, stage_bytes = kSub * block_bytes;
   const int stages = min(static_cast<int>(ring / stage_bytes), kMaxStages);
 
-  // PREC: the epilogue's running sums take 128 registers per thread: 3 x 168
-  // per thread of the three warpgroups become 56 + 2 x 224
-  if (warp == 0) {
-    if (kMoved) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    const uint32_t full0 = mapa_shared(smem_u32(full), even);
-    int s = 0;
-    uint32_t phase = 1;   // parity of the stage's last release; the first round finds it free
-    bool ok = true;
-    int64_t issued = 0;
-    Tiles<GRAD, SPLIT, kElems, !SPLIT && !(GRAD && PREC)> tiles;
-    Tile t, next;
-    if (first < n_tiles) next = tiles.next(a, start, slice, first, step, n_tiles);
-    for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
-      t = next;
-      const bool more = idx + step < n_tiles;   // the next tile is looked up behind this one's first block
-      if (more && t.len == 0) next = tiles.next(a, start, slice, idx + step, step, n_tiles);
-      const int32_t len = t.len;
-      const CUtensorMap *mw = NMAP > 1 ? &a.w[t.e] : &a.w[0];
-      const int32_t z = NMAP > 1 ? 0 : t.e;
-      const int32_t half = t.width / 2;
-      const int32_t m0 = t.m0 + 128 * rank, n0 = t.n0 + half * rank;
-      const int32_t boxes = GRAD ? (half + 63) / 64 : half / 16;
-      const uint32_t bytes = kABytes + boxes * (GRAD ? 8192u : kBoxBytes);
-      for (int32_t k = 0; k < len; k += kStageK) {
-        if (!(ok = warp_wait(empty + s, phase, a.status))) break;
-        uint8_t *As = sm + s * stage_bytes, *Bs = As + kABytes;
-        const uint32_t bar = full0 + 8 * s;
-        if (GRAD) {
-          // a group's last rows, fewer than a block: they go to the block's end,
-          // behind rows of zeros (rows -(64 - left) .. of their window), so that
-          // no row of another group, whatever it holds, meets the MMAs
-          if (elect_one()) {
-            const bool both = kSub > 1 && k + kElems < len;
-            if (rank == 0) mbar_arrive_expect_tx(full + s, both ? 4 * bytes : 2 * bytes);
-#pragma unroll
-            for (int u = 0; u < kSub; ++u) {
-              if (u > 0 && !both) break;
-              uint8_t *Au = As + u * block_bytes, *Bu = Bs + u * block_bytes;
-              const int32_t y = t.k0 + k + u * kElems, left = len - k - u * kElems;
-              if (left < kElems) {
-                tma_load_3d_pair(Au, &a.x[2], m0, left - kElems, y, bar);
-                tma_load_3d_pair(Au + 8192, &a.x[2], m0 + 64, left - kElems, y, bar);
-                tma_load_3d_pair(Bu, &a.x[1], n0, left - kElems, y, bar);
-                if (boxes > 1) tma_load_3d_pair(Bu + 8192, &a.x[1], n0 + 64, left - kElems, y, bar);
-              } else {
-                tma_load_2d_pair(Au, &a.w[0], m0, y, bar);
-                tma_load_2d_pair(Au + 8192, &a.w[0], m0 + 64, y, bar);
-                tma_load_2d_pair(Bu, &a.x[0], n0, y, bar);
-                if (boxes > 1) tma_load_2d_pair(Bu + 8192, &a.x[0], n0 + 64, y, bar);
-              }
-            }
-          }
-        } else if (elect_one()) {
-          const bool both = kSub > 1 && k + kElems < len;
-          if (rank == 0) mbar_arrive_expect_tx(full + s, both ? 4 * bytes : 2 * bytes);
-#pragma unroll
-          for (int u = 0; u < kSub; ++u) {
-            if (u > 0 && !both) break;
-            uint8_t *Au = As + u * block_bytes, *Bu = Bs + u * block_bytes;
-            const int32_t ku = t.k0 + k + u * kElems;
-            if (A_MN) {
-              tma_load_3d_pair(Au, mw, m0, ku, z, bar);
-              tma_load_3d_pair(Au + 8192, mw, m0 + 64, ku, z, bar);
-            } else {
-              tma_load_3d_pair(Au, mw, ku, m0, z, bar);
-            }
-            // this CTA's rows of the tile in at most four boxes, the largest first
-            int32_t at = 0;
-#pragma unroll
-            for (int32_t i = 0; i < 4; ++i)
-              if (boxes & (8 >> i)) {
-                tma_load_2d_pair(Bu + kBoxBytes * at, &a.x[i], ku, n0 + 16 * at, bar);
-                at += 8 >> i;
-              }
-          }
-        }
-        __syncwarp();
-        if (k == 0 && more) next = tiles.next(a, start, slice, idx + step, step, n_tiles);
-        ++issued;
-        if (++s == stages) {
-          s = 0;
-          phase ^= 1;
-        }
-      }
-    }
-    // the last loads have landed before the CTA ends, also when something gave
-    // up (the even CTA's barriers see both CTAs' loads; the CTAs leave together)
-    if (rank == 0)
-      for (int64_t i = max((int64_t)0, issued - stages); i < issued; ++i)
-        warp_wait(full + i % stages, static_cast<uint32_t>((i / stages) & 1), a.status);
-  } else if (warp == 1) {
-    if (kMoved) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (rank == 0) {
-      // descriptors of stage 0, without the address
-      const uint64_t a_bits = A_MN ? sw128_desc(0, 8192, 1024) : sw128_desc(0, 16, 1024);
-      const uint64_t b_bits = GRAD ? sw128_desc(0, 8192, 1024) : sw128_desc(0, 16, 1024);
-      constexpr uint32_t kStepA = (A_MN ? 2048 : 32) >> 4, kStepB = (GRAD ? 2048 : 32) >> 4;
+  // The three warpgroups take their roles here.  PREC: the epilogue's running sums
+  // take 128 registers per thread, so 3 x 168 per thread become 56 + 2 x 224
+  // (kRegsLoad, kRegsSums): one instruction for a whole warpgroup, as setmaxnreg
+  // asks, ahead of any branch between its warps.
+  if (warp < 4) {
+    if (kMoved) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
+    if (warp == 0) {
+      const uint32_t full0 = mapa_shared(smem_u32(full), even);
       int s = 0;
-      uint32_t phase = 0;
-      int32_t j = 0;
-      bool ok = !a.stall || blockIdx.x != 0 || warp_wait(done, 0, a.status);
+      uint32_t phase = 1;   // parity of the stage's last release; the first round finds it free
+      bool ok = true;
+      int64_t issued = 0;
       Tiles<GRAD, SPLIT, kElems, !SPLIT && !(GRAD && PREC)> tiles;
       Tile t, next;
       if (first < n_tiles) next = tiles.next(a, start, slice, first, step, n_tiles);
       for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
         t = next;
-        const bool more = idx + step < n_tiles;
+        const bool more = idx + step < n_tiles;   // the next tile is looked up behind this one's first block
         if (more && t.len == 0) next = tiles.next(a, start, slice, idx + step, step, n_tiles);
         const int32_t len = t.len;
-        const uint32_t idesc = a.idesc | (static_cast<uint32_t>(t.width >> 3) << 17);
-        uint32_t d = 0;
-        // the next accumulator, once the epilogue has drained it
-        auto acquire = [&] {
-          const int b = j & 1;
-          d = tmem + static_cast<uint32_t>(b * kTileN);
-          const bool free = j < 2 || warp_wait<true>(acc_empty + b, static_cast<uint32_t>(((j >> 1) - 1) & 1), a.status);
-          tc_fence_after();
-          return free;
-        };
-        auto hand_over = [&] {
-          if (elect_one()) mma_commit_pair(acc_full + (j & 1), pair_mask);
-          __syncwarp();
-          ++j;
-        };
-        if (len == 0) {
-          if (!(ok = acquire())) break;
-          hand_over();
-        }
+        const CUtensorMap *mw = NMAP > 1 ? &a.w[t.e] : &a.w[0];
+        const int32_t z = NMAP > 1 ? 0 : t.e;
+        const int32_t half = t.width / 2;
+        const int32_t m0 = t.m0 + 128 * rank, n0 = t.n0 + half * rank;
+        const int32_t boxes = GRAD ? (half + 63) / 64 : half / 16;
+        const uint32_t bytes = kABytes + boxes * (GRAD ? 8192u : kBoxBytes);
         for (int32_t k = 0; k < len; k += kStageK) {
-          const uint32_t as = smem_u32(sm) + s * stage_bytes;
-          const int32_t left = len - k;
-          const bool fresh = kPieces ? k % (kChunk * kElems) == 0 : k == 0;
-          if (fresh && !(ok = acquire())) break;
-          if (!(ok = warp_wait(full + s, phase, a.status))) break;
-          tc_fence_after();
-          // (a shared-memory address carries the CTA's rank above the descriptor's field)
-          const uint64_t ad = a_bits | ((as >> 4) & 0x3FFF), bd = b_bits | (((as + kABytes) >> 4) & 0x3FFF);
-          const int32_t begin = GRAD ? (kElems - min(left, kElems)) / 16 : 0;
-          if (elect_one()) {
-#pragma unroll
-            for (int32_t kk = 0; kk < 4 * kSub; ++kk) {
-              // 16 (int8: 32) elements of K at a time; of a block that is not
-              // full, the product's lie at its start, the gradient's at its end
-              if (kk > 0 && (GRAD ? kk / 4 * kElems : kk * (kElems / 4)) >= left) break;
-              if (GRAD && kk % 4 < (kElems - min(left - kk / 4 * kElems, kElems)) / 16) continue;
-              const uint32_t off = (kk / 4) * (block_bytes >> 4);
-              const uint64_t au = ad + off + (kk % 4) * kStepA, bu = bd + off + (kk % 4) * kStepB;
-              const uint32_t add = !fresh || kk > begin ? 1u : 0u;
-              if (KIND) mma_i8_ss_pair(d, au, bu, idesc, add);
-              else mma_ss_pair(d, au, bu, idesc, add);
+          if (!(ok = warp_wait(empty + s, phase, a.status))) break;
+          uint8_t *As = sm + s * stage_bytes, *Bs = As + kABytes;
+          const uint32_t bar = full0 + 8 * s;
+          if (GRAD) {
+            // a group's last rows, fewer than a block: they go to the block's end,
+            // behind rows of zeros (rows -(64 - left) .. of their window), so that
+            // no row of another group, whatever it holds, meets the MMAs
+            if (elect_one()) {
+              const bool both = kSub > 1 && k + kElems < len;
+              if (rank == 0) mbar_arrive_expect_tx(full + s, both ? 4 * bytes : 2 * bytes);
+  #pragma unroll
+              for (int u = 0; u < kSub; ++u) {
+                if (u > 0 && !both) break;
+                uint8_t *Au = As + u * block_bytes, *Bu = Bs + u * block_bytes;
+                const int32_t y = t.k0 + k + u * kElems, left = len - k - u * kElems;
+                if (left < kElems) {
+                  tma_load_3d_pair(Au, &a.x[2], m0, left - kElems, y, bar);
+                  tma_load_3d_pair(Au + 8192, &a.x[2], m0 + 64, left - kElems, y, bar);
+                  tma_load_3d_pair(Bu, &a.x[1], n0, left - kElems, y, bar);
+                  if (boxes > 1) tma_load_3d_pair(Bu + 8192, &a.x[1], n0 + 64, left - kElems, y, bar);
+                } else {
+                  tma_load_2d_pair(Au, &a.w[0], m0, y, bar);
+                  tma_load_2d_pair(Au + 8192, &a.w[0], m0 + 64, y, bar);
+                  tma_load_2d_pair(Bu, &a.x[0], n0, y, bar);
+                  if (boxes > 1) tma_load_2d_pair(Bu + 8192, &a.x[0], n0 + 64, y, bar);
+                }
+              }
             }
-            mma_commit_pair(empty + s, pair_mask);   // the stage is free in both CTAs once these MMAs have read it
+          } else if (elect_one()) {
+            const bool both = kSub > 1 && k + kElems < len;
+            if (rank == 0) mbar_arrive_expect_tx(full + s, both ? 4 * bytes : 2 * bytes);
+  #pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+              if (u > 0 && !both) break;
+              uint8_t *Au = As + u * block_bytes, *Bu = Bs + u * block_bytes;
+              const int32_t ku = t.k0 + k + u * kElems;
+              if (A_MN) {
+                tma_load_3d_pair(Au, mw, m0, ku, z, bar);
+                tma_load_3d_pair(Au + 8192, mw, m0 + 64, ku, z, bar);
+              } else {
+                tma_load_3d_pair(Au, mw, ku, m0, z, bar);
+              }
+              // this CTA's rows of the tile in at most four boxes, the largest first
+              int32_t at = 0;
+  #pragma unroll
+              for (int32_t i = 0; i < 4; ++i)
+                if (boxes & (8 >> i)) {
+                  tma_load_2d_pair(Bu + kBoxBytes * at, &a.x[i], ku, n0 + 16 * at, bar);
+                  at += 8 >> i;
+                }
+            }
           }
           __syncwarp();
-          if (left <= kStageK || (kPieces && (k + kStageK) % (kChunk * kElems) == 0)) hand_over();
           if (k == 0 && more) next = tiles.next(a, start, slice, idx + step, step, n_tiles);
+          ++issued;
           if (++s == stages) {
             s = 0;
             phase ^= 1;
           }
         }
       }
-      // nothing is in flight when the pair leaves and releases its tensor memory
-      if (elect_one()) mma_commit_pair(done, static_cast<uint16_t>(1u << even));
-      __syncwarp();
-      warp_wait(done, 0, a.status);
-    }
-  } else if (warp < 4) {
-    if (kMoved) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 3 && rank == 1) {
+      // the last loads have landed before the CTA ends, also when something gave
+      // up (the even CTA's barriers see both CTAs' loads; the CTAs leave together)
+      if (rank == 0)
+        for (int64_t i = max((int64_t)0, issued - stages); i < issued; ++i)
+          warp_wait(full + i % stages, static_cast<uint32_t>((i / stages) & 1), a.status);
+    } else if (warp == 1) {
+      if (rank == 0) {
+        // descriptors of stage 0, without the address
+        const uint64_t a_bits = A_MN ? sw128_desc(0, 8192, 1024) : sw128_desc(0, 16, 1024);
+        const uint64_t b_bits = GRAD ? sw128_desc(0, 8192, 1024) : sw128_desc(0, 16, 1024);
+        constexpr uint32_t kStepA = (A_MN ? 2048 : 32) >> 4, kStepB = (GRAD ? 2048 : 32) >> 4;
+        int s = 0;
+        uint32_t phase = 0;
+        int32_t j = 0;
+        bool ok = !a.stall || blockIdx.x != 0 || warp_wait(done, 0, a.status);
+        Tiles<GRAD, SPLIT, kElems, !SPLIT && !(GRAD && PREC)> tiles;
+        Tile t, next;
+        if (first < n_tiles) next = tiles.next(a, start, slice, first, step, n_tiles);
+        for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
+          t = next;
+          const bool more = idx + step < n_tiles;
+          if (more && t.len == 0) next = tiles.next(a, start, slice, idx + step, step, n_tiles);
+          const int32_t len = t.len;
+          const uint32_t idesc = a.idesc | (static_cast<uint32_t>(t.width >> 3) << 17);
+          uint32_t d = 0;
+          // the next accumulator, once the epilogue has drained it
+          auto acquire = [&] {
+            const int b = j & 1;
+            d = tmem + static_cast<uint32_t>(b * kTileN);
+            const uint32_t parity = static_cast<uint32_t>(((j >> 1) - 1) & 1);
+          const bool free = j < 2 || warp_wait<true>(acc_empty + b, parity, a.status);
+            tc_fence_after();
+            return free;
+          };
+          auto hand_over = [&] {
+            if (elect_one()) mma_commit_pair(acc_full + (j & 1), pair_mask);
+            __syncwarp();
+            ++j;
+          };
+          if (len == 0) {
+            if (!(ok = acquire())) break;
+            hand_over();
+          }
+          for (int32_t k = 0; k < len; k += kStageK) {
+            const uint32_t as = smem_u32(sm) + s * stage_bytes;
+            const int32_t left = len - k;
+            const bool fresh = kPieces ? k % (kChunk * kElems) == 0 : k == 0;
+            if (fresh && !(ok = acquire())) break;
+            if (!(ok = warp_wait(full + s, phase, a.status))) break;
+            tc_fence_after();
+            // (a shared-memory address carries the CTA's rank above the descriptor's field)
+            const uint64_t ad = a_bits | ((as >> 4) & 0x3FFF), bd = b_bits | (((as + kABytes) >> 4) & 0x3FFF);
+            const int32_t begin = GRAD ? (kElems - min(left, kElems)) / 16 : 0;
+            if (elect_one()) {
+  #pragma unroll
+              for (int32_t kk = 0; kk < 4 * kSub; ++kk) {
+                // 16 (int8: 32) elements of K at a time; of a block that is not
+                // full, the product's lie at its start, the gradient's at its end
+                if (kk > 0 && (GRAD ? kk / 4 * kElems : kk * (kElems / 4)) >= left) break;
+                if (GRAD && kk % 4 < (kElems - min(left - kk / 4 * kElems, kElems)) / 16) continue;
+                const uint32_t off = (kk / 4) * (block_bytes >> 4);
+                const uint64_t au = ad + off + (kk % 4) * kStepA, bu = bd + off + (kk % 4) * kStepB;
+                const uint32_t add = !fresh || kk > begin ? 1u : 0u;
+                if (KIND) mma_i8_ss_pair(d, au, bu, idesc, add);
+                else mma_ss_pair(d, au, bu, idesc, add);
+              }
+              mma_commit_pair(empty + s, pair_mask);   // the stage is free in both CTAs once these MMAs have read it
+            }
+            __syncwarp();
+            if (left <= kStageK || (kPieces && (k + kStageK) % (kChunk * kElems) == 0)) hand_over();
+            if (k == 0 && more) next = tiles.next(a, start, slice, idx + step, step, n_tiles);
+            if (++s == stages) {
+              s = 0;
+              phase ^= 1;
+            }
+          }
+        }
+        // nothing is in flight when the pair leaves and releases its tensor memory
+        if (elect_one()) mma_commit_pair(done, static_cast<uint16_t>(1u << even));
+        __syncwarp();
+        warp_wait(done, 0, a.status);
+      }
+    } else if (warp == 3 && rank == 1) {
       // Passes the odd CTA's "drained" on to the even one.  An arrival there
       // waits for the thread's earlier stores to be performed (cluster scope,
       // 1 to 2.5 thousand cycles beside a tile's stores); the epilogue's warps
@@ -844,245 +853,246 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (GRAD) {
-    if (kMoved) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    // This warp's boxes of G, 32 rows x 32 or 64 columns, in the order of its tiles
-    // and, inside one, of the columns.  With C, the boxes of C come by TMA up
-    // to two ahead of the one at work, also from the next tile, and the result
-    // takes their place: three buffers, so that a buffer is loaded again one
-    // box after its store was issued.
-    const int q = warp & 3;             // TMEM lanes 32 q .. 32 q + 31
-    const int half = (warp - 4) >> 2;   // the warp's column groups: half, half + 2, .. (split: its slice's)
-    const int32_t i0 = SPLIT ? half + 2 * slice : half, di = SPLIT ? 2 * a.split : 2;
-    const int32_t bc = PREC ? 32 : a.box_cols;
-    uint8_t *buf = sm + ring + (warp - 4) * a.buffers * kStageOut;
-    uint64_t *landed = c_full + 3 * (warp - 4);
-    uint64_t *freed = rank == 0 ? acc_empty : drained;
-    const uint32_t c_bytes = bc * (a.cdtype == HIMUON_FP32 ? 128 : 64);
-    // A box that reaches over the last column is stored up to the end of that
-    // column's 16 bytes (observed: columns behind it in the row's pitch were
-    // overwritten); where G's width is no multiple of 16 bytes the warp copies
-    // the last boxes itself.
-    const bool whole_runs = a.N % (a.odtype == HIMUON_FP32 ? 4 : 8) == 0;
-    Tiles<GRAD, SPLIT, kElems, !PREC> tiles, c_tiles;   // at work; C's boxes
-    struct Box {
-      int32_t idx, i;   // tile, column group; idx >= n_tiles: none left
-      Tile t;
-    };
-    auto groups = [&](const Tile &t) {   // of this tile that are inside G
-      return t.m0 + 128 * rank + 32 * q < a.M ? (t.valid + bc - 1) / bc : 0;
-    };
-    auto settle = [&](Box &x) {   // to the first box at or after (idx, i)
-      while (x.idx < n_tiles && x.i >= groups(x.t)) {
-        x.idx += step;
-        x.i = i0;
-        if (x.idx < n_tiles) x.t = c_tiles.next(a, start, slice, x.idx, step, n_tiles);
-      }
-    };
-    auto load_c = [&](Box &x, int at) {   // box x into buffer `at`, then on to the next box
-      if (x.idx >= n_tiles) return;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(landed + at, c_bytes);
-        tma_load_3d(buf + at * kStageOut, NOUT > 1 ? &a.c[x.t.e] : &a.c[0], x.t.n0 + bc * x.i,
-                    x.t.m0 + 128 * rank + 32 * q, NOUT > 1 ? 0 : x.t.e, landed + at);
-      }
-      __syncwarp();
-      x.i += di;
-      settle(x);
-    };
-    Box ahead{first, i0, {}};
-    if (a.has_c && first < n_tiles) {
-      ahead.t = c_tiles.next(a, start, slice, first, step, n_tiles);
-      settle(ahead);
-      load_c(ahead, 0);
-      load_c(ahead, 1);
-    }
-    int at = 0;                  // buffer of the box at work
-    uint32_t c_phase = 0;        // per buffer
-    bool ok = true;
-    int32_t j = 0;
-    for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
-      const Tile t = tiles.next(a, start, slice, idx, step, n_tiles);
-      const int32_t in = groups(t);
-      // column group i: combine with C, store.  fetch(h, v): its 32-column
-      // part h from the accumulator or the running sums.
-      auto emit = [&](int32_t i, auto fetch) {
-        const int32_t m = t.m0 + 128 * rank + 32 * q, n0 = t.n0 + bc * i;
-        const bool by_box = n0 + bc <= a.N || whole_runs;
-        uint8_t *box = buf + at * kStageOut;
-        float v[32];
-        fetch(0, v);
-        if (a.has_c) {
-          if (!(ok = warp_wait(landed + at, (c_phase >> at) & 1, a.status))) return;
-          c_phase ^= 1u << at;
-        } else {
-          if (elect_one()) bulk_wait_read<0>();   // (the last box's store has read the buffer)
-          __syncwarp();
-        }
-#pragma unroll
-        for (int h = 0; h < (PREC ? 1 : 2); ++h) {
-          if (32 * h >= bc) break;
-          if (h > 0) fetch(h, v);
-          if (a.has_c) {
-            box_combine(box, lane, a.cdtype, 4 * h, bc == 64, a.alpha, a.beta, v);
-            if (bc == 32) __syncwarp();   // (G's rows may lie where C's of other lanes did)
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] *= a.alpha;
-          }
-          box_write(box, lane, a.odtype, 4 * h, bc == 64, v);
-        }
-        if (!by_box) {
-          __syncwarp();
-          box_copy(box, lane, a.odtype, bc, (NOUT > 1 ? a.out[t.e] : a.out[0] + t.e * a.out_stride), m * a.ldo + n0,
-                   a.ldo, min(32, a.M - m), a.N - n0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (elect_one()) {
-          if (by_box) tma_store_3d(NOUT > 1 ? &a.g[t.e] : &a.g[0], box, n0, m, NOUT > 1 ? 0 : t.e);
-          bulk_commit();
-          if (a.has_c) bulk_wait_read<1>();   // the store of the box before has read its buffer
-        }
-        __syncwarp();
-        if (a.has_c) load_c(ahead, at == 0 ? 2 : at - 1);
-        at = at + 1 == a.buffers ? 0 : at + 1;
+  } else {
+    if (kMoved) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSums));
+    if (GRAD) {
+      // This warp's boxes of G, 32 rows x 32 or 64 columns, in the order of its tiles
+      // and, inside one, of the columns.  With C, the boxes of C come by TMA up
+      // to two ahead of the one at work, also from the next tile, and the result
+      // takes their place: three buffers, so that a buffer is loaded again one
+      // box after its store was issued.
+      const int q = warp & 3;             // TMEM lanes 32 q .. 32 q + 31
+      const int half = (warp - 4) >> 2;   // the warp's column groups: half, half + 2, .. (split: its slice's)
+      const int32_t i0 = SPLIT ? half + 2 * slice : half, di = SPLIT ? 2 * a.split : 2;
+      const int32_t bc = PREC ? 32 : a.box_cols;
+      uint8_t *buf = sm + ring + (warp - 4) * a.buffers * kStageOut;
+      uint64_t *landed = c_full + 3 * (warp - 4);
+      uint64_t *freed = rank == 0 ? acc_empty : drained;
+      const uint32_t c_bytes = bc * (a.cdtype == HIMUON_FP32 ? 128 : 64);
+      // A box that reaches over the last column is stored up to the end of that
+      // column's 16 bytes (observed: columns behind it in the row's pitch were
+      // overwritten); where G's width is no multiple of 16 bytes the warp copies
+      // the last boxes itself.
+      const bool whole_runs = a.N % (a.odtype == HIMUON_FP32 ? 4 : 8) == 0;
+      Tiles<GRAD, SPLIT, kElems, !PREC> tiles, c_tiles;   // at work; C's boxes
+      struct Box {
+        int32_t idx, i;   // tile, column group; idx >= n_tiles: none left
+        Tile t;
       };
-      const int32_t pieces = kPieces ? max(1, (t.len + kChunk * kElems - 1) / (kChunk * kElems)) : 1;
-      float sum[kGroups][32];
-      for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
-        const int b = j & 1;
-        if (!(ok = warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status))) break;
-        tc_fence_after();
-        const uint32_t taddr = tmem + static_cast<uint32_t>(b * kTileN) + (static_cast<uint32_t>(q * 32) << 16);
-        auto release = [&] {
+      auto groups = [&](const Tile &t) {   // of this tile that are inside G
+        return t.m0 + 128 * rank + 32 * q < a.M ? (t.valid + bc - 1) / bc : 0;
+      };
+      auto settle = [&](Box &x) {   // to the first box at or after (idx, i)
+        while (x.idx < n_tiles && x.i >= groups(x.t)) {
+          x.idx += step;
+          x.i = i0;
+          if (x.idx < n_tiles) x.t = c_tiles.next(a, start, slice, x.idx, step, n_tiles);
+        }
+      };
+      auto load_c = [&](Box &x, int at) {   // box x into buffer `at`, then on to the next box
+        if (x.idx >= n_tiles) return;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(landed + at, c_bytes);
+          tma_load_3d(buf + at * kStageOut, NOUT > 1 ? &a.c[x.t.e] : &a.c[0], x.t.n0 + bc * x.i,
+                      x.t.m0 + 128 * rank + 32 * q, NOUT > 1 ? 0 : x.t.e, landed + at);
+        }
+        __syncwarp();
+        x.i += di;
+        settle(x);
+      };
+      Box ahead{first, i0, {}};
+      if (a.has_c && first < n_tiles) {
+        ahead.t = c_tiles.next(a, start, slice, first, step, n_tiles);
+        settle(ahead);
+        load_c(ahead, 0);
+        load_c(ahead, 1);
+      }
+      int at = 0;                  // buffer of the box at work
+      uint32_t c_phase = 0;        // per buffer
+      bool ok = true;
+      int32_t j = 0;
+      for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
+        const Tile t = tiles.next(a, start, slice, idx, step, n_tiles);
+        const int32_t in = groups(t);
+        // column group i: combine with C, store.  fetch(h, v): its 32-column
+        // part h from the accumulator or the running sums.
+        auto emit = [&](int32_t i, auto fetch) {
+          const int32_t m = t.m0 + 128 * rank + 32 * q, n0 = t.n0 + bc * i;
+          const bool by_box = n0 + bc <= a.N || whole_runs;
+          uint8_t *box = buf + at * kStageOut;
+          float v[32];
+          fetch(0, v);
+          if (a.has_c) {
+            if (!(ok = warp_wait(landed + at, (c_phase >> at) & 1, a.status))) return;
+            c_phase ^= 1u << at;
+          } else {
+            if (elect_one()) bulk_wait_read<0>();   // (the last box's store has read the buffer)
+            __syncwarp();
+          }
+  #pragma unroll
+          for (int h = 0; h < (PREC ? 1 : 2); ++h) {
+            if (32 * h >= bc) break;
+            if (h > 0) fetch(h, v);
+            if (a.has_c) {
+              box_combine(box, lane, a.cdtype, 4 * h, bc == 64, a.alpha, a.beta, v);
+              if (bc == 32) __syncwarp();   // (G's rows may lie where C's of other lanes did)
+            } else {
+  #pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] *= a.alpha;
+            }
+            box_write(box, lane, a.odtype, 4 * h, bc == 64, v);
+          }
+          if (!by_box) {
+            __syncwarp();
+            box_copy(box, lane, a.odtype, bc, (NOUT > 1 ? a.out[t.e] : a.out[0] + t.e * a.out_stride), m * a.ldo + n0,
+                     a.ldo, min(32, a.M - m), a.N - n0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (elect_one()) {
+            if (by_box) tma_store_3d(NOUT > 1 ? &a.g[t.e] : &a.g[0], box, n0, m, NOUT > 1 ? 0 : t.e);
+            bulk_commit();
+            if (a.has_c) bulk_wait_read<1>();   // the store of the box before has read its buffer
+          }
+          __syncwarp();
+          if (a.has_c) load_c(ahead, at == 0 ? 2 : at - 1);
+          at = at + 1 == a.buffers ? 0 : at + 1;
+        };
+        const int32_t pieces = kPieces ? max(1, (t.len + kChunk * kElems - 1) / (kChunk * kElems)) : 1;
+        float sum[kGroups][32];
+        for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
+          const int b = j & 1;
+          if (!(ok = warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status))) break;
+          tc_fence_after();
+          const uint32_t taddr = tmem + static_cast<uint32_t>(b * kTileN) + (static_cast<uint32_t>(q * 32) << 16);
+          auto release = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (elect_one()) mbar_arrive(freed + b);
+          };
+          if (PREC && (SPLIT || pieces > 1)) {
+            read_pieces(sum, taddr, half, in, p, t.len == 0);
+            release();
+            if (!SPLIT && p + 1 == pieces) {
+  #pragma unroll
+              for (int g = 0; g < kGroups; ++g)
+                if (half + 2 * g < in && ok)
+                  emit(half + 2 * g, [&](int, float(&v)[32]) {
+  #pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = sum[g][k];
+                  });
+            }
+          } else {
+            for (int32_t i = half; i < in && ok; i += 2) {
+              emit(i, [&](int h, float(&v)[32]) {
+                if (t.len == 0) {
+  #pragma unroll
+                  for (int k = 0; k < 32; ++k) v[k] = 0.f;
+                } else {
+                  tmem_ld32(taddr + bc * i + 32 * h, v);
+                  tmem_wait_ld();
+                }
+                if (i + 2 >= in && 32 * (h + 1) >= bc) release();   // the accumulator is read
+              });
+            }
+            if (in <= half) release();   // no box of this warp's in the tile
+          }
+        }
+        if (SPLIT) {
+          send_slices(sum, sm, warp - 4, lane, half, in, rank, slice, a.split);
+          if (half + 2 * slice < in && ok)
+            emit(half + 2 * slice, [&](int, float(&v)[32]) { add_slices<KIND>(v, sm, warp - 4, lane, a.split); });
+        }
+      }
+      if (SPLIT && first >= n_tiles) {   // the cluster has no tile: keep step with its barriers
+        cluster_sync_all();
+        cluster_sync_all();
+      }
+      if (!ok && a.has_c) {   // gave up: what was loaded ahead lands before the CTA ends (bounded)
+        for (int k = 0; k < a.buffers; ++k) warp_wait(landed + k, (c_phase >> k) & 1, a.status);
+      }
+      if (elect_one()) bulk_wait0();
+    } else {
+      const int q = warp & 3;             // TMEM lanes 32 q .. 32 q + 31
+      const int half = (warp - 4) >> 2;   // the warp's 32-column groups: half, half + 2, ..
+      float *st = reinterpret_cast<float *>(sm + ring + (warp - 4) * kStageOut);
+      uint64_t *freed = rank == 0 ? acc_empty : drained;
+      const bool whole_runs = a.M % 4 == 0;   // (a box stores 16 bytes at a time)
+      int32_t j = 0;
+      Tiles<GRAD, SPLIT, kElems, !PREC> tiles;
+      bool ok = true;
+      for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
+        const Tile t = tiles.next(a, start, slice, idx, step, n_tiles);
+        const int32_t m = t.m0 + 128 * rank + 32 * q;   // this warp's 32 channels
+        const int32_t m_in = min(32, a.M - m);
+        float chan = 1.f;
+        if (KIND && lane < m_in) chan = a.w_scale[t.e * a.ld_scale + m + lane];
+        const int32_t in = m_in > 0 ? (t.valid + 31) / 32 : 0;
+        auto emit = [&](int32_t i, float(&v)[32]) {   // rows 32 i .. of the tile
+          const int64_t r0 = t.n0 + 32 * i;
+          const int32_t r_in = min(32, t.valid - 32 * i);
+          if (KIND) {   // int32 sums: scales of this lane's channel and of each row
+            const float mine = lane < r_in ? a.x_scale[r0 + lane] : 0.f;
+  #pragma unroll
+            for (int k = 0; k < 32; ++k)
+              v[k] = static_cast<float>(__float_as_int(v[k])) * chan * __shfl_sync(0xffffffffu, mine, k);
+          }
+          const int64_t o = r0 * a.ldo + m;
+          if ((PREC && !SPLIT) || a.odtype == HIMUON_FP32) {
+            if (r_in == 32 && (m_in == 32 || whole_runs)) {
+              put_boxes32(&a.g[0], reinterpret_cast<uint8_t *>(st), lane, v, m, static_cast<int32_t>(r0));
+            } else {   // a box would reach the next group's rows, or 16 bytes into the padding
+              if (elect_one()) bulk_wait_read<0>();
+              put_rows32(st, lane, v, reinterpret_cast<float *>(a.out[0]) + o, a.ldo, r_in, m_in);
+            }
+          } else if (a.odtype == HIMUON_FP16)
+            put_rows16<__half2>(reinterpret_cast<uint32_t *>(st), lane, v, reinterpret_cast<uint16_t *>(a.out[0]) + o,
+                                a.ldo, r_in, m_in);
+          else
+            put_rows16<__nv_bfloat162>(reinterpret_cast<uint32_t *>(st), lane, v,
+                                       reinterpret_cast<uint16_t *>(a.out[0]) + o, a.ldo, r_in, m_in);
+        };
+        const int32_t pieces = kPieces ? (t.len + kChunk * kElems - 1) / (kChunk * kElems) : 1;
+        float sum[kGroups][32];
+        for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
+          const int b = j & 1;
+          if (!(ok = warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status))) break;
+          tc_fence_after();
+          const uint32_t taddr = tmem + static_cast<uint32_t>(b * kTileN) + (static_cast<uint32_t>(q * 32) << 16);
+          if (PREC && (SPLIT || pieces > 1)) {
+            read_pieces(sum, taddr, half, in, p, false);
+          } else {
+  #pragma unroll 1
+            for (int32_t i = half; i < in; i += 2) {
+              tmem_ld32(taddr + 32 * i, sum[0]);
+              tmem_wait_ld();
+              emit(i, sum[0]);
+            }
+          }
           tc_fence_before();
           __syncwarp();
           if (elect_one()) mbar_arrive(freed + b);
-        };
-        if (PREC && (SPLIT || pieces > 1)) {
-          read_pieces(sum, taddr, half, in, p, t.len == 0);
-          release();
-          if (!SPLIT && p + 1 == pieces) {
-#pragma unroll
+          if (PREC && !SPLIT && pieces > 1 && p + 1 == pieces) {
+  #pragma unroll
             for (int g = 0; g < kGroups; ++g)
-              if (half + 2 * g < in && ok)
-                emit(half + 2 * g, [&](int, float(&v)[32]) {
-#pragma unroll
-                  for (int k = 0; k < 32; ++k) v[k] = sum[g][k];
-                });
-          }
-        } else {
-          for (int32_t i = half; i < in && ok; i += 2) {
-            emit(i, [&](int h, float(&v)[32]) {
-              if (t.len == 0) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = 0.f;
-              } else {
-                tmem_ld32(taddr + bc * i + 32 * h, v);
-                tmem_wait_ld();
-              }
-              if (i + 2 >= in && 32 * (h + 1) >= bc) release();   // the accumulator is read
-            });
-          }
-          if (in <= half) release();   // no box of this warp's in the tile
-        }
-      }
-      if (SPLIT) {
-        send_slices(sum, sm, warp - 4, lane, half, in, rank, slice, a.split);
-        if (half + 2 * slice < in && ok)
-          emit(half + 2 * slice, [&](int, float(&v)[32]) { add_slices<KIND>(v, sm, warp - 4, lane, a.split); });
-      }
-    }
-    if (SPLIT && first >= n_tiles) {   // the cluster has no tile: keep step with its barriers
-      cluster_sync_all();
-      cluster_sync_all();
-    }
-    if (!ok && a.has_c) {   // gave up: what was loaded ahead lands before the CTA ends (bounded)
-      for (int k = 0; k < a.buffers; ++k) warp_wait(landed + k, (c_phase >> k) & 1, a.status);
-    }
-    if (elect_one()) bulk_wait0();
-  } else {
-    if (kMoved) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    const int q = warp & 3;             // TMEM lanes 32 q .. 32 q + 31
-    const int half = (warp - 4) >> 2;   // the warp's 32-column groups: half, half + 2, ..
-    float *st = reinterpret_cast<float *>(sm + ring + (warp - 4) * kStageOut);
-    uint64_t *freed = rank == 0 ? acc_empty : drained;
-    const bool whole_runs = a.M % 4 == 0;   // (a box stores 16 bytes at a time)
-    int32_t j = 0;
-    Tiles<GRAD, SPLIT, kElems, !PREC> tiles;
-    bool ok = true;
-    for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
-      const Tile t = tiles.next(a, start, slice, idx, step, n_tiles);
-      const int32_t m = t.m0 + 128 * rank + 32 * q;   // this warp's 32 channels
-      const int32_t m_in = min(32, a.M - m);
-      float chan = 1.f;
-      if (KIND && lane < m_in) chan = a.w_scale[t.e * a.ld_scale + m + lane];
-      const int32_t in = m_in > 0 ? (t.valid + 31) / 32 : 0;
-      auto emit = [&](int32_t i, float(&v)[32]) {   // rows 32 i .. of the tile
-        const int64_t r0 = t.n0 + 32 * i;
-        const int32_t r_in = min(32, t.valid - 32 * i);
-        if (KIND) {   // int32 sums: scales of this lane's channel and of each row
-          const float mine = lane < r_in ? a.x_scale[r0 + lane] : 0.f;
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            v[k] = static_cast<float>(__float_as_int(v[k])) * chan * __shfl_sync(0xffffffffu, mine, k);
-        }
-        const int64_t o = r0 * a.ldo + m;
-        if ((PREC && !SPLIT) || a.odtype == HIMUON_FP32) {
-          if (r_in == 32 && (m_in == 32 || whole_runs)) {
-            put_boxes32(&a.g[0], reinterpret_cast<uint8_t *>(st), lane, v, m, static_cast<int32_t>(r0));
-          } else {   // a box would reach the next group's rows, or 16 bytes into the padding
-            if (elect_one()) bulk_wait_read<0>();
-            put_rows32(st, lane, v, reinterpret_cast<float *>(a.out[0]) + o, a.ldo, r_in, m_in);
-          }
-        } else if (a.odtype == HIMUON_FP16)
-          put_rows16<__half2>(reinterpret_cast<uint32_t *>(st), lane, v, reinterpret_cast<uint16_t *>(a.out[0]) + o,
-                              a.ldo, r_in, m_in);
-        else
-          put_rows16<__nv_bfloat162>(reinterpret_cast<uint32_t *>(st), lane, v,
-                                     reinterpret_cast<uint16_t *>(a.out[0]) + o, a.ldo, r_in, m_in);
-      };
-      const int32_t pieces = kPieces ? (t.len + kChunk * kElems - 1) / (kChunk * kElems) : 1;
-      float sum[kGroups][32];
-      for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
-        const int b = j & 1;
-        if (!(ok = warp_wait(acc_full + b, static_cast<uint32_t>((j >> 1) & 1), a.status))) break;
-        tc_fence_after();
-        const uint32_t taddr = tmem + static_cast<uint32_t>(b * kTileN) + (static_cast<uint32_t>(q * 32) << 16);
-        if (PREC && (SPLIT || pieces > 1)) {
-          read_pieces(sum, taddr, half, in, p, false);
-        } else {
-#pragma unroll 1
-          for (int32_t i = half; i < in; i += 2) {
-            tmem_ld32(taddr + 32 * i, sum[0]);
-            tmem_wait_ld();
-            emit(i, sum[0]);
+              if (half + 2 * g < in) emit(half + 2 * g, sum[g]);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (elect_one()) mbar_arrive(freed + b);
-        if (PREC && !SPLIT && pieces > 1 && p + 1 == pieces) {
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g)
-            if (half + 2 * g < in) emit(half + 2 * g, sum[g]);
+        if (SPLIT) {
+          send_slices(sum, sm, warp - 4, lane, half, in, rank, slice, a.split);
+          if (half + 2 * slice < in) {
+            float v[32];
+            add_slices<KIND>(v, sm, warp - 4, lane, a.split);
+            emit(half + 2 * slice, v);
+          }
         }
       }
-      if (SPLIT) {
-        send_slices(sum, sm, warp - 4, lane, half, in, rank, slice, a.split);
-        if (half + 2 * slice < in) {
-          float v[32];
-          add_slices<KIND>(v, sm, warp - 4, lane, a.split);
-          emit(half + 2 * slice, v);
-        }
+      if (SPLIT && first >= n_tiles) {   // the cluster has no tile: keep step with its barriers
+        cluster_sync_all();
+        cluster_sync_all();
       }
+      if (elect_one()) bulk_wait0();
     }
-    if (SPLIT && first >= n_tiles) {   // the cluster has no tile: keep step with its barriers
-      cluster_sync_all();
-      cluster_sync_all();
-    }
-    if (elect_one()) bulk_wait0();
   }
   if (SPLIT && warp < 4) {   // the two barriers of send_slices
     __syncwarp();
