@@ -273,8 +273,12 @@ HIMUON_API int64_t himuon_plan_tiles(const himuon_mat *mats, int32_t n, const hi
  * word.
  *
  * Row operands may have 0 rows (their data pointer is then not read).  Sums are
- * held in fp32 (int32 for the 8-bit product); each result is rounded once to
- * its storage type.  Every data pointer is 16-byte aligned and every
+ * held in fp32 (int32 for the 8-bit product, exact); each result is rounded
+ * once to its storage type.  The tensor cores' fp32 sums truncate, by about
+ * 1e-7 of a sum of terms of one sign per 16 of them, so longer sums than 512
+ * (FP32 results), 4096 (FP16) or 32768 terms (BF16) run in pieces of that
+ * length (beyond 2^20 terms at least the root of twice the sum's), which are
+ * added up in rounded fp32.  Every data pointer is 16-byte aligned and every
  * ld * sizeof a multiple of 16 bytes where a matrix has more than one row
  * (HIMUON_ERR_ALIGNMENT); scale vectors need 4-byte alignment only.  The n
  * matrices of one argument have the same shape, ld and dtype.  Outputs must not overlap inputs (except C and G

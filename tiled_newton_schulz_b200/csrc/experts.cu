@@ -151,7 +151,8 @@ bool load_kernels() {
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (loaded.load(std::memory_order_relaxed) & bit) return true;
   const bool ok =
-      load_variant<0, 0, 0, 0, 0>() && load_variant<0, 0, 0, 1, 0>() && load_variant<0, 0, 0, 1, 1>() &&
+      load_variant<0, 0, 0, 0, 0>() && load_variant<0, 0, 0, 1, 0>() && load_variant<0, 0, 0, 2, 0>() &&
+      load_variant<0, 0, 0, 1, 1>() && load_variant<0, 1, 0, 2, 0>() &&
       load_variant<0, 1, 0, 0, 0>() && load_variant<0, 1, 0, 1, 0>() && load_variant<0, 1, 0, 1, 1>() &&
       load_variant<1, 0, 0, 0, 0>() && load_variant<1, 0, 0, 1, 1>() && load_variant<0, 1, 1, 0, 0>() &&
       load_variant<0, 1, 1, 1, 0>() && load_variant<0, 1, 1, 1, 1>() && device_status_word() != nullptr &&
@@ -273,15 +274,18 @@ int product_launch(const himuon_mat *X, const float *x_scale, const himuon_mat *
       a.split = s;
     }
   }
-  const bool fp32 = Y->dtype == HIMUON_FP32;
+  const bool fp32 = Y->dtype == HIMUON_FP32, pieces = in_pieces(X->cols, Y->dtype);
+  a.piece_log = piece_log(X->cols, a.split > 1 ? HIMUON_FP32 : Y->dtype);
   if (X->dtype == HIMUON_I8)
     return a.split > 1 ? launch_mma<1, 0, 0, 1, 1>(a, most, stream) : launch_mma<1, 0, 0, 0, 0>(a, most, stream);
   if (w_trans)
     return a.split > 1 ? launch_mma<0, 0, 0, 1, 1>(a, most, stream)
            : fp32      ? launch_mma<0, 0, 0, 1, 0>(a, most, stream)
+           : pieces    ? launch_mma<0, 0, 0, 2, 0>(a, most, stream)
                        : launch_mma<0, 0, 0, 0, 0>(a, most, stream);
   return a.split > 1 ? launch_mma<0, 1, 0, 1, 1>(a, most, stream)
          : fp32      ? launch_mma<0, 1, 0, 1, 0>(a, most, stream)
+         : pieces    ? launch_mma<0, 1, 0, 2, 0>(a, most, stream)
                      : launch_mma<0, 1, 0, 0, 0>(a, most, stream);
 }
 
@@ -332,8 +336,8 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
   // columns, 0.22 at 192, 0.29 at 256).  (bf16, 14808 rows 64 x 1408: one tile per
   // pair 48.7 us at 128 columns, four pairs per tile 22.0; 8192 rows 1024 x 1024
   // 31.4, and 25.0 with two; 8 groups of 512 rows 512 x 512 9.0, and 19.8 with two.)
-  const bool wide = G->dtype == HIMUON_FP32 || (C && C->dtype == HIMUON_FP32);
-  a.box_cols = wide ? 32 : 64;
+  const bool pieces = in_pieces(A->rows, G->dtype);   // (one group may have all the rows)
+  a.box_cols = pieces || (C && C->dtype == HIMUON_FP32) ? 32 : 64;
   const int64_t m_tiles = n * ((A->cols + kTileM - 1) / kTileM), pairs = sm_count() / 2;
   const int64_t fewest = (B->cols + kTileN - 1) / kTileN;
   const int64_t blocks = (A->rows + 64 * n - 1) / (64 * static_cast<int64_t>(n));   // of an even group
@@ -358,6 +362,7 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
   }
   a.mt_m = static_cast<int32_t>(m_tiles / n);
   if (a.split > 1) a.box_cols = 32;
+  a.piece_log = piece_log(A->rows, a.split > 1 ? HIMUON_FP32 : G->dtype);
   for (int32_t i = 0; i < (NOUT > 1 ? n : 1); ++i) {
     if (!make_map(&a.g[i], G[e0 + i], NOUT > 1 ? 1 : n, g_stride, 32, a.box_cols)) return HIMUON_ERR_CUDA;
     a.out[i] = static_cast<char *>(G[e0 + i].data);
@@ -369,7 +374,7 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
   if (C) a.cdtype = C->dtype;
   a.buffers = C && a.split == 1 ? 3 : 1;   // (a split tile's warps have one box each)
   if (a.split > 1) return launch_mma<0, 1, 1, 1, 1>(a, most, stream);
-  return G->dtype == HIMUON_FP32 ? launch_mma<0, 1, 1, 1, 0>(a, most, stream) : launch_mma<0, 1, 1, 0, 0>(a, most, stream);
+  return pieces ? launch_mma<0, 1, 1, 1, 0>(a, most, stream) : launch_mma<0, 1, 1, 0, 0>(a, most, stream);
 }
 
 }  // namespace

@@ -37,11 +37,26 @@ constexpr int kRegsLaunch = 168, kRegsLoad = 56, kRegsSums = 224;
 static_assert(kRegsLoad + 2 * kRegsSums <= 3 * kRegsLaunch, "registers of the three warpgroups");
 template <int GRAD, int PREC, int SPLIT>
 constexpr bool kMovesRegisters = PREC && (GRAD || !SPLIT);   // the variants that do
-// fp32 results of 16-bit operands: the tensor core's accumulator truncates at
-// every K = 16 step, which costs an fp32 result about 1e-8 of itself per step
-// (K = 1100: 1.1e-6 against 2.6e-7 for rounded fp32 sums).  Their sums are cut
-// every kChunk blocks of 64; the epilogue adds the pieces in fp32 registers.
-constexpr int kChunk = 8;
+// Sums of 16-bit operands: the tensor core's accumulator truncates at every K = 16
+// step.  Terms of changing sign lose about 1e-8 of the result per step (K = 1100:
+// 1.1e-6 against 2.6e-7 for rounded fp32 sums), terms of one sign 1e-7 (K = 2^22:
+// 2.6%), which fits products cut at a quarter of the accumulator's last place and
+// a sum cut at its last place: 2.5 places per step on average, 5 at most.  So long
+// sums run in pieces of 2^piece_log elements, which the epilogue adds in fp32
+// registers (PREC); the kernel without PREC is for sums of one piece.  2^12
+// elements for fp16 results and 2^15 for bf16 keep 5 places per step below a third
+// of a rounding to the type; fp32 results, and shared tiles, which have the sums in
+// registers anyway, take 2^9 (K = 1100: 4.6e-7).  Every addition of a piece is off
+// by 2^-24 of the sum so far, in one direction where the terms are equal, so beyond
+// 2^20 elements the pieces grow with the root of the sum's length.
+__host__ inline int32_t piece_log(int64_t length, int32_t dtype) {
+  int32_t log = dtype == HIMUON_FP32 ? 9 : dtype == HIMUON_FP16 ? 12 : 15;
+  while (length > (1 << 20) && ((int64_t)1 << 2 * log) < 2 * length) ++log;
+  return log;
+}
+__host__ inline bool in_pieces(int64_t length, int32_t dtype) {
+  return dtype == HIMUON_FP32 || length > (int64_t)1 << piece_log(length, dtype);
+}
 constexpr uint32_t kBarBytes = 448;
 constexpr uint32_t kSmem = kData + kBarBytes + 4 * (kMaxStack + 4) + 1024;
 static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -62,6 +77,7 @@ struct MmaArgs {
   int32_t mt_m, mt_n;      // tiles along M; gradient: along N
   int32_t cap;             // gradient: columns of a tile (a multiple of 32); product: log2 of a tile's most rows
   int32_t split;           // pairs that share a tile's sum (the cluster's)
+  int32_t piece_log;       // PREC: log2 of a piece's elements (whole stages)
   uint32_t idesc;          // without the N field
   int *status;
   const float *x_scale, *w_scale;
@@ -584,7 +600,9 @@ __device__ __forceinline__ void add_slices(float (&v)[32], const uint8_t *ring, 
 
 // KIND 0: 16-bit operands (kind::f16); 1: int8 (kind::i8).  A_MN: A is
 // MN-major (W stored K x channels; the gradient's operands).  PREC: sums in
-// pieces of kChunk blocks (fp32 results).
+// pieces (piece_log); a product whose tiles are not shared then has an fp32 (1)
+// or a 16-bit result (2): one kernel for both took 22.1 us for 1531 rows 1100 ->
+// 2050 with an fp32 result, where this takes 21.7.
 // SPLIT: the cluster's pairs share one tile, each a stretch of its sum (calls of
 // few tiles of 128 columns at most); comes with PREC's running sums in registers.
 //
@@ -623,6 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kPieces = PREC && !KIND;   // (int32 sums are exact)
   constexpr int kGroups = !PREC ? 1 : SPLIT ? 2 : 4;   // PREC: 32-column groups of an epilogue warp's sums
   constexpr bool kMoved = kMovesRegisters<GRAD, PREC, SPLIT>;
+  const int32_t piece = kPieces ? 1 << a.piece_log : 0;
   const int32_t cta = static_cast<int32_t>(cluster_ctarank());
   const int32_t rank = cta & 1, even = cta & ~1, slice = SPLIT ? cta >> 1 : 0;
   const uint16_t pair_mask = static_cast<uint16_t>(3u << even);
@@ -795,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int32_t k = 0; k < len; k += kStageK) {
             const uint32_t as = smem_u32(sm) + s * stage_bytes;
             const int32_t left = len - k;
-            const bool fresh = kPieces ? k % (kChunk * kElems) == 0 : k == 0;
+            const bool fresh = kPieces ? (k & (piece - 1)) == 0 : k == 0;
             if (fresh && !(ok = acquire())) break;
             if (!(ok = warp_wait(full + s, phase, a.status))) break;
             tc_fence_after();
@@ -818,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_commit_pair(empty + s, pair_mask);   // the stage is free in both CTAs once these MMAs have read it
             }
             __syncwarp();
-            if (left <= kStageK || (kPieces && (k + kStageK) % (kChunk * kElems) == 0)) hand_over();
+            if (left <= kStageK || (kPieces && ((k + kStageK) & (piece - 1)) == 0)) hand_over();
             if (k == 0 && more) next = tiles.next(a, start, slice, idx + step, step, n_tiles);
             if (++s == stages) {
               s = 0;
@@ -842,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int32_t idx = first; idx < n_tiles && ok; idx += step) {
         const int32_t len = GRAD || SPLIT ? tiles.next(a, start, slice, idx, step, n_tiles).len : a.K;
-        const int32_t pieces = kPieces ? max(1, (len + kChunk * kElems - 1) / (kChunk * kElems)) : 1;
+        const int32_t pieces = kPieces ? max(1, (len + piece - 1) >> a.piece_log) : 1;
         for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
           const int b = j & 1;
           ok = warp_wait(drained + b, static_cast<uint32_t>((j >> 1) & 1), a.status);
@@ -958,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (a.has_c) load_c(ahead, at == 0 ? 2 : at - 1);
           at = at + 1 == a.buffers ? 0 : at + 1;
         };
-        const int32_t pieces = kPieces ? max(1, (t.len + kChunk * kElems - 1) / (kChunk * kElems)) : 1;
+        const int32_t pieces = kPieces ? max(1, (t.len + piece - 1) >> a.piece_log) : 1;
         float sum[kGroups][32];
         for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
           const int b = j & 1;
@@ -971,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) mbar_arrive(freed + b);
           };
           if (PREC && (SPLIT || pieces > 1)) {
-            read_pieces(sum, taddr, half, in, p, t.len == 0);
+            read_pieces(sum, taddr, half, in, p, SPLIT && t.len == 0);   // (several pieces: not empty)
             release();
             if (!SPLIT && p + 1 == pieces) {
   #pragma unroll
@@ -1038,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               v[k] = static_cast<float>(__float_as_int(v[k])) * chan * __shfl_sync(0xffffffffu, mine, k);
           }
           const int64_t o = r0 * a.ldo + m;
-          if ((PREC && !SPLIT) || a.odtype == HIMUON_FP32) {
+          if (PREC != 2 && ((PREC && !SPLIT) || a.odtype == HIMUON_FP32)) {
             if (r_in == 32 && (m_in == 32 || whole_runs)) {
               put_boxes32(&a.g[0], reinterpret_cast<uint8_t *>(st), lane, v, m, static_cast<int32_t>(r0));
             } else {   // a box would reach the next group's rows, or 16 bytes into the padding
@@ -1052,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             put_rows16<__nv_bfloat162>(reinterpret_cast<uint32_t *>(st), lane, v,
                                        reinterpret_cast<uint16_t *>(a.out[0]) + o, a.ldo, r_in, m_in);
         };
-        const int32_t pieces = kPieces ? (t.len + kChunk * kElems - 1) / (kChunk * kElems) : 1;
+        const int32_t pieces = kPieces ? (t.len + piece - 1) >> a.piece_log : 1;
         float sum[kGroups][32];
         for (int32_t p = 0; p < pieces && ok; ++p, ++j) {
           const int b = j & 1;
