@@ -872,3 +872,26 @@ def test_product_16_bit_results_of_long_sums(hm, trans):
     check_product(hm, f16, f16, 32776, 264, [70, 0, 500, 3], trans, start=2, behind=5, margin=8)
     check_product(hm, bf, f16, 33001, 2050, [300, 513], trans, listed=True)
     check_product(hm, bf, bf, 262200, 72, [1] * 45, trans)
+
+
+def test_gradient_host_work_does_not_grow_with_the_width(hm):
+    """A call's work on the host is that of a few tile widths, whatever the columns (each time the quickest of several
+    calls, with nothing queued before it)."""
+    import time
+    g = gen(61)
+
+    def quickest(Q):
+        A, B = matrix((2000, 8), torch.bfloat16, g), torch.ones(2000, Q, device=DEV, dtype=torch.bfloat16)
+        G = torch.empty(1, 8, Q, device=DEV, dtype=torch.bfloat16)
+        best = float("inf")
+        for _ in range(20):
+            torch.cuda.synchronize()
+            t0 = time.perf_counter()
+            hm.expert_gradient(A, B, G)
+            best = min(best, time.perf_counter() - t0)
+        want = A.double().sum(0)[:, None].expand(-1, Q)
+        close(G[0], want, A.double().abs().sum(0)[:, None], 2000, torch.bfloat16)
+        return best
+
+    narrow, wide = quickest(4096), quickest(113408)
+    assert wide <= 3 * narrow, (narrow, wide)

@@ -182,12 +182,11 @@ int launch_mma(const MmaArgs<NMAP, NOUT> &a, int64_t most_tiles, cudaStream_t st
 }
 
 // What a call of `tiles` tiles costs, in blocks of the sum, if `split` pairs (1, 2
-// or 4) share a tile of `blocks`: the rounds, times a pair's share and `join` for
-// starting the clusters and adding up.  Shared tiles run in one round only: a
-// second would start its clusters anew (3 rows, 20000 -> 10240, bf16: 72 us with
-// one pair per tile, 92 with four in three rounds).
-int64_t split_cost(int64_t tiles, int64_t blocks, int32_t split, int64_t join) {
-  const int64_t room = clusters_at_once(split);
+// or 4) share a tile of `blocks` and `room` tiles run at once: the rounds, times a
+// pair's share and `join` for starting the clusters and adding up.  Shared tiles
+// run in one round only: a second would start its clusters anew (3 rows, 20000 ->
+// 10240, bf16: 72 us with one pair per tile, 92 with four in three rounds).
+int64_t split_cost(int64_t tiles, int64_t blocks, int32_t split, int64_t room, int64_t join) {
   if (room < 1 || (split > 1 && tiles > room)) return INT64_MAX;
   return (tiles + room - 1) / room * ((blocks + split - 1) / split + join);
 }
@@ -266,9 +265,9 @@ int product_launch(const himuon_mat *X, const float *x_scale, const himuon_mat *
   // 8.4, 8.8 and 16.6.)
   if (a.cap == 7 || X->rows <= 128) {
     const int64_t blocks = (X->cols * static_cast<int64_t>(size_of(X->dtype)) + 127) / 128;
-    int64_t best = split_cost(most, blocks, 1, 0);
+    int64_t best = split_cost(most, blocks, 1, pairs, 0);
     for (int32_t s = 2; s <= 4; s *= 2) {
-      const int64_t cost = split_cost(most, blocks, s, s == 2 ? 12 : 16);
+      const int64_t cost = split_cost(most, blocks, s, clusters_at_once(s), s == 2 ? 12 : 16);
       if (cost >= best) continue;
       best = cost;
       a.split = s;
@@ -304,6 +303,45 @@ int run_product(const himuon_mat *X, const float *x_scale, const himuon_mat *W, 
   return HIMUON_OK;
 }
 
+// A gradient's tiles: their columns, how many lie across G, and the pairs that share
+// one.  As few as 256 columns allow, or up to four times as many of equal width, in
+// whole boxes of the epilogue, where that fills the last round of the pairs better.
+// A block of the sum costs a pair the tile's columns, 128 at least, and as much as
+// 192 more (0.20 us at up to 128 columns, 0.22 at 192, 0.29 at 256).  (bf16, 14808
+// rows 64 x 1408: one tile per pair 48.7 us at 128 columns, four pairs per tile 22.0;
+// 8192 rows 1024 x 1024 31.4, and 25.0 with two; 8 groups of 512 rows 512 x 512 9.0,
+// and 19.8 with two.)  Only the widths are gone through, not every count of tiles
+// (2000 rows 8 x 113408: 100 us of host time per call, now 15).
+struct GradientTiles {
+  int64_t across;
+  int32_t width, split;
+};
+GradientTiles gradient_tiles(int64_t rows, int32_t n, int64_t m_tiles, int64_t cols, int32_t box_cols) {
+  const int64_t room[3] = {sm_count() / 2, clusters_at_once(2), clusters_at_once(4)}, pairs = room[0];
+  const int64_t fewest = (cols + kTileN - 1) / kTileN;
+  const int64_t blocks = (rows + 64 * n - 1) / (64 * static_cast<int64_t>(n));   // of an even group
+  GradientTiles t = {0, 0, 1};
+  int64_t best = INT64_MAX;
+  for (int64_t w = kTileN; w > 0; w -= 32) {
+    const int64_t across = (cols + w - 1) / w, even = (cols + across - 1) / across;
+    if (across > 4 * fewest) break;
+    for (int32_t i = 0; i < 3; ++i) {
+      const int32_t s = 1 << i;
+      const int64_t box = s == 1 ? box_cols : 32;
+      if (w != (even + box - 1) / box * box || (s > 1 && (w > 128 || blocks < 4 * s))) continue;
+      const int64_t tiles = m_tiles * across, each = std::max<int64_t>(w, 128) + 192;
+      int64_t cost = split_cost(tiles, blocks, s, room[i], s == 1 ? 0 : s == 2 ? 17 : 25);
+      if (cost == INT64_MAX) continue;
+      cost = cost * each + (s == 1 ? (tiles + pairs - 1) / pairs * 10 * w : 0);   // (and a tile's way out)
+      if (cost >= best) continue;
+      best = cost;
+      t = {across, static_cast<int32_t>(w), s};
+    }
+    if (m_tiles * t.across >= 6 * pairs) break;
+  }
+  return t;
+}
+
 template <int NOUT>
 int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_t n, const int32_t *offsets,
                     float alpha, float beta, const himuon_mat *C, int64_t c_stride, const himuon_mat *G,
@@ -329,37 +367,14 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
   a.alpha = alpha;
   a.beta = beta;
   a.has_c = C != nullptr;
-  // Columns of a tile, and pairs that share one: as few tiles as 256 columns
-  // allow, or more of equal width, in whole boxes of the epilogue, where that
-  // fills the last round of the pairs better.  A block of the sum costs a pair
-  // the tile's columns, 128 at least, and as much as 192 more (0.20 us at up to 128
-  // columns, 0.22 at 192, 0.29 at 256).  (bf16, 14808 rows 64 x 1408: one tile per
-  // pair 48.7 us at 128 columns, four pairs per tile 22.0; 8192 rows 1024 x 1024
-  // 31.4, and 25.0 with two; 8 groups of 512 rows 512 x 512 9.0, and 19.8 with two.)
   const bool pieces = in_pieces(A->rows, G->dtype);   // (one group may have all the rows)
   a.box_cols = pieces || (C && C->dtype == HIMUON_FP32) ? 32 : 64;
-  const int64_t m_tiles = n * ((A->cols + kTileM - 1) / kTileM), pairs = sm_count() / 2;
-  const int64_t fewest = (B->cols + kTileN - 1) / kTileN;
-  const int64_t blocks = (A->rows + 64 * n - 1) / (64 * static_cast<int64_t>(n));   // of an even group
-  int64_t best = INT64_MAX, most = 0;
-  for (int64_t c = fewest; c <= 4 * fewest; ++c) {
-    for (int32_t s = 1; s <= 4; s *= 2) {
-      const int64_t box = s == 1 ? a.box_cols : 32;
-      const int64_t w = ((B->cols + c - 1) / c + box - 1) / box * box;
-      if (s > 1 && (w > 128 || blocks < 4 * s)) continue;
-      const int64_t tiles = m_tiles * ((B->cols + w - 1) / w), each = std::max<int64_t>(w, 128) + 192;
-      int64_t cost = split_cost(tiles, blocks, s, s == 1 ? 0 : s == 2 ? 17 : 25);
-      if (cost == INT64_MAX) continue;
-      cost = cost * each + (s == 1 ? (tiles + pairs - 1) / pairs * 10 * w : 0);   // (and a tile's way out)
-      if (cost >= best) continue;
-      best = cost;
-      most = tiles;
-      a.split = s;
-      a.cap = static_cast<int32_t>(w);
-      a.mt_n = static_cast<int32_t>(tiles / m_tiles);
-    }
-    if (most >= 6 * pairs) break;
-  }
+  const int64_t m_tiles = n * ((A->cols + kTileM - 1) / kTileM);
+  const GradientTiles tiles = gradient_tiles(A->rows, n, m_tiles, B->cols, a.box_cols);
+  const int64_t most = m_tiles * tiles.across;
+  a.split = tiles.split;
+  a.cap = tiles.width;
+  a.mt_n = static_cast<int32_t>(tiles.across);
   a.mt_m = static_cast<int32_t>(m_tiles / n);
   if (a.split > 1) a.box_cols = 32;
   a.piece_log = piece_log(A->rows, a.split > 1 ? HIMUON_FP32 : G->dtype);
