@@ -895,3 +895,58 @@ def test_gradient_host_work_does_not_grow_with_the_width(hm):
 
     narrow, wide = quickest(4096), quickest(113408)
     assert wide <= 3 * narrow, (narrow, wide)
+
+
+@pytest.mark.parametrize("form", ["plain", "add", "views", "listed", "bf16", "none_long", "all_empty"])
+def test_gradient_long_groups_in_a_launch_of_their_own(hm, form):
+    """Large calls with 16-bit results: groups whose sums run in one piece and the others, in two launches."""
+    f16, bf, n = torch.float16, torch.bfloat16, 64
+    rng = np.random.default_rng(71)
+    counts = rng.integers(0, 90, n)
+    counts[[0, 7, 31, 32, 63]] = 4097, 4096, 9000, 0, 5001
+    if form == "none_long":
+        counts[[0, 31, 63]] = 4096, 4095, 1
+    if form == "bf16":
+        counts[[3, 9]] = 32769, 32768
+    if form == "all_empty":
+        counts[:] = 0
+    kw = dict(plain=dict(), add=dict(beta=0.5, alias=True), views=dict(start=5, behind=77, margin=8, beta=1.0, cdtype=bf),
+              listed=dict(listed=True, beta=-1.0, cdtype=torch.float32), bf16=dict(beta=1.0), none_long=dict(),
+              all_empty=dict(beta=2.0, behind=5000))[form]
+    dtype = bf if form == "bf16" else f16
+    before = hm.launch_count()
+    check_gradient(hm, dtype, dtype, 1032, 1027, counts.tolist(), alpha=2.0 ** -4, **kw)
+    assert hm.launch_count() - before == 2
+
+
+def test_gradient_long_groups_replayed_with_other_offsets(hm):
+    """A captured call: groups that become longer or shorter than a piece go to the other launch."""
+    g, n, rows, P, Q = gen(72), 80, 12000, 520, 1288
+    A, B = matrix((rows, P), torch.float16, g, 0.1), matrix((rows, Q), torch.float16, g)
+    first, second = [150] * n, [0] * n
+    second[4], second[5], second[79] = 5000, 4096, 2904
+    cur = offsets(first)
+    G = torch.empty(n, P, Q, device=DEV, dtype=torch.float16)
+    hm.expert_gradient(A, B, G, cur)
+    torch.cuda.synchronize()
+    before = hm.launch_count()
+    gph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gph):
+        hm.expert_gradient(A, B, G, cur)
+    assert hm.launch_count() - before == 2
+    for counts in (second, first, second):
+        off = offsets(counts)
+        cur.copy_(off)
+        G.fill_(float("nan"))
+        gph.replay()
+        torch.cuda.synchronize()
+        for e, (a, b) in enumerate(groups(off)):
+            if b == a:
+                assert (G[e] == 0).all()
+                continue
+            x, y = A[a:b].double(), B[a:b].double()
+            close(G[e], x.T @ y, x.abs().T @ y.abs(), b - a, torch.float16)
+    cur.copy_(torch.tensor([0, 40, 20] + [12000] * (n - 2), dtype=torch.int32))
+    gph.replay()
+    assert hm.device_status() == -7
+    assert hm.device_status() == 0

@@ -204,6 +204,8 @@ void common_args(MmaArgs<NMAP, NOUT> &a, const int32_t *offsets, int32_t e0, int
   a.buffers = 1;
   a.box_cols = 0;
   a.split = 1;
+  a.least = 0;
+  a.most = INT32_MAX;
   // HIMUON_TEST_STALL=1 exercises the device timeout path (tests only)
   const char *stall = getenv("HIMUON_TEST_STALL");
   a.stall = stall && stall[0] == '1';
@@ -273,7 +275,7 @@ int product_launch(const himuon_mat *X, const float *x_scale, const himuon_mat *
       a.split = s;
     }
   }
-  const bool fp32 = Y->dtype == HIMUON_FP32, pieces = in_pieces(X->cols, Y->dtype);
+  const bool fp32 = Y->dtype == HIMUON_FP32, pieces = X->cols > 1 << longest_log(Y->dtype);
   a.piece_log = piece_log(X->cols, a.split > 1 ? HIMUON_FP32 : Y->dtype);
   if (X->dtype == HIMUON_I8)
     return a.split > 1 ? launch_mma<1, 0, 0, 1, 1>(a, most, stream) : launch_mma<1, 0, 0, 0, 0>(a, most, stream);
@@ -342,12 +344,35 @@ GradientTiles gradient_tiles(int64_t rows, int32_t n, int64_t m_tiles, int64_t c
   return t;
 }
 
+// A launch's groups: all, those whose sums run in one piece, or those of several.
+enum Groups { kAll, kShort, kLong };
 template <int NOUT>
 int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_t n, const int32_t *offsets,
                     float alpha, float beta, const himuon_mat *C, int64_t c_stride, const himuon_mat *G,
-                    int64_t g_stride, cudaStream_t stream) {
+                    int64_t g_stride, Groups groups, cudaStream_t stream) {
   MmaArgs<1, NOUT> a;
   common_args(a, offsets, e0, n, A->rows);
+  const int64_t longest = (int64_t)1 << longest_log(G->dtype);
+  const bool pieces = groups == kLong || G->dtype == HIMUON_FP32 || (groups == kAll && A->rows > longest);
+  a.box_cols = pieces || (C && C->dtype == HIMUON_FP32) ? 32 : 64;
+  const int64_t m_tiles = n * ((A->cols + kTileM - 1) / kTileM);
+  const GradientTiles tiles = gradient_tiles(A->rows, n, m_tiles, B->cols, a.box_cols);
+  const int64_t most = m_tiles * tiles.across;
+  // Any group may have all the rows, as far as the host knows, but few need the
+  // kernel of pieces, which has half the stages' length and narrower boxes: large
+  // calls launch it for those alone (which costs 8 us where there is none).  fp16,
+  // 64 groups 1024 x 4096: 32768 rows 299 us in one launch, 272 in two, 8192 rows 202
+  // and 163; 32 groups 1024 x 2048, 1024 tiles, 97 and 98; 40 groups 768 x 768 25 and 30.
+  if (groups == kAll && pieces && G->dtype != HIMUON_FP32 && tiles.split == 1 && A->rows <= n * longest &&
+      most >= 16 * (sm_count() / 2)) {
+    const int rc = gradient_launch<NOUT>(A, B, e0, n, offsets, alpha, beta, C, c_stride, G, g_stride, kShort, stream);
+    return rc ? rc : gradient_launch<NOUT>(A, B, e0, n, offsets, alpha, beta, C, c_stride, G, g_stride, kLong, stream);
+  }
+  if (groups == kShort) a.most = static_cast<int32_t>(longest);
+  if (groups == kLong) a.least = static_cast<int32_t>(longest) + 1;
+  a.split = tiles.split;
+  a.cap = tiles.width;
+  a.mt_n = static_cast<int32_t>(tiles.across);
   if (A->rows == 0) {
     // no row is ever loaded: the maps only have to be valid, and G's memory is
     himuon_mat any = *G;
@@ -367,14 +392,6 @@ int gradient_launch(const himuon_mat *A, const himuon_mat *B, int32_t e0, int32_
   a.alpha = alpha;
   a.beta = beta;
   a.has_c = C != nullptr;
-  const bool pieces = in_pieces(A->rows, G->dtype);   // (one group may have all the rows)
-  a.box_cols = pieces || (C && C->dtype == HIMUON_FP32) ? 32 : 64;
-  const int64_t m_tiles = n * ((A->cols + kTileM - 1) / kTileM);
-  const GradientTiles tiles = gradient_tiles(A->rows, n, m_tiles, B->cols, a.box_cols);
-  const int64_t most = m_tiles * tiles.across;
-  a.split = tiles.split;
-  a.cap = tiles.width;
-  a.mt_n = static_cast<int32_t>(tiles.across);
   a.mt_m = static_cast<int32_t>(m_tiles / n);
   if (a.split > 1) a.box_cols = 32;
   a.piece_log = piece_log(A->rows, a.split > 1 ? HIMUON_FP32 : G->dtype);
@@ -471,8 +488,8 @@ int himuon_expert_gradient(const himuon_mat *A, const himuon_mat *B, int32_t n, 
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (int32_t e0 = 0; e0 < n; e0 += cap) {
     const int32_t cnt = std::min(n - e0, cap);
-    rc = st ? gradient_launch<1>(A, B, e0, cnt, offsets, alpha, beta, C, c_stride, G, g_stride, s)
-            : gradient_launch<kMaxList>(A, B, e0, cnt, offsets, alpha, beta, C, 0, G, 0, s);
+    rc = st ? gradient_launch<1>(A, B, e0, cnt, offsets, alpha, beta, C, c_stride, G, g_stride, kAll, s)
+            : gradient_launch<kMaxList>(A, B, e0, cnt, offsets, alpha, beta, C, 0, G, 0, kAll, s);
     if (rc) return rc;
   }
   return HIMUON_OK;

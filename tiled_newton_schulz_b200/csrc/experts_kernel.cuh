@@ -49,13 +49,13 @@ constexpr bool kMovesRegisters = PREC && (GRAD || !SPLIT);   // the variants tha
 // registers anyway, take 2^9 (K = 1100: 4.6e-7).  Every addition of a piece is off
 // by 2^-24 of the sum so far, in one direction where the terms are equal, so beyond
 // 2^20 elements the pieces grow with the root of the sum's length.
+__host__ inline int32_t longest_log(int32_t dtype) {   // of a sum in one piece
+  return dtype == HIMUON_FP32 ? 9 : dtype == HIMUON_FP16 ? 12 : 15;
+}
 __host__ inline int32_t piece_log(int64_t length, int32_t dtype) {
-  int32_t log = dtype == HIMUON_FP32 ? 9 : dtype == HIMUON_FP16 ? 12 : 15;
+  int32_t log = longest_log(dtype);
   while (length > (1 << 20) && ((int64_t)1 << 2 * log) < 2 * length) ++log;
   return log;
-}
-__host__ inline bool in_pieces(int64_t length, int32_t dtype) {
-  return dtype == HIMUON_FP32 || length > (int64_t)1 << piece_log(length, dtype);
 }
 constexpr uint32_t kBarBytes = 448;
 constexpr uint32_t kSmem = kData + kBarBytes + 4 * (kMaxStack + 4) + 1024;
@@ -78,6 +78,7 @@ struct MmaArgs {
   int32_t cap;             // gradient: columns of a tile (a multiple of 32); product: log2 of a tile's most rows
   int32_t split;           // pairs that share a tile's sum (the cluster's)
   int32_t piece_log;       // PREC: log2 of a piece's elements (whole stages)
+  int32_t least, most;     // gradient: rows of the groups that the launch takes
   uint32_t idesc;          // without the N field
   int *status;
   const float *x_scale, *w_scale;
@@ -190,9 +191,10 @@ __device__ __forceinline__ Tile tile_at(const Args &a, const int32_t *start, int
   Tile t;
   const uint32_t mt_m = a.mt_m, u = static_cast<uint32_t>(idx) / mt_m;
   if (GRAD) {
-    t.e = u / static_cast<uint32_t>(a.mt_n);
+    const uint32_t i = u / static_cast<uint32_t>(a.mt_n);
+    t.e = start[i];
     t.m0 = (idx - u * mt_m) * kTileM;
-    t.n0 = (u - t.e * a.mt_n) * a.cap;
+    t.n0 = (u - i * a.mt_n) * a.cap;
     t.valid = min(a.cap, a.N - t.n0);
     t.width = round32(t.valid);
     t.k0 = bound_at(a.offsets, t.e, a.rows);
@@ -467,45 +469,58 @@ __device__ __forceinline__ void put_boxes32(const CUtensorMap *map, uint8_t *st,
   }
 }
 
-// Reports offsets that decrease or leave 0 .. rows (a whole warp).
+// The rows of group lane + 32 i (a whole warp, all loads in flight together).
+// Reports offsets that decrease or leave 0 .. rows.
+constexpr int kPerLane = kMaxStack / 32;
 template <typename Args>
-__device__ __forceinline__ void check_offsets(const Args &a, int lane) {
-  if (!a.offsets) return;
-  for (int32_t e = lane; e < a.n; e += 32)
-    if (a.offsets[e] < 0 || a.offsets[e + 1] < a.offsets[e] || a.offsets[e + 1] > a.rows)
-      set_status(a.status, HIMUON_ERR_DEVICE);
+__device__ __forceinline__ void count_rows(const Args &a, int32_t (&cnt)[kPerLane], int lane) {
+  int32_t o[kPerLane + 1];
+#pragma unroll
+  for (int i = 0; i <= kPerLane; ++i) {
+    const int32_t e = lane + 32 * i;
+    o[i] = e > a.n ? 0 : a.offsets ? a.offsets[e] : e == 0 ? 0 : static_cast<int32_t>(a.rows);
+  }
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    cnt[i] = 0;
+    if (32 * i >= a.n) continue;
+    const int32_t e = lane + 32 * i;
+    const int32_t down = __shfl_down_sync(0xffffffffu, o[i], 1), over = __shfl_sync(0xffffffffu, o[i + 1], 0);
+    const int64_t lo = o[i], hi = lane == 31 ? over : down;
+    if (e < a.n) {
+      if (lo < 0 || hi < lo || hi > a.rows) set_status(a.status, HIMUON_ERR_DEVICE);
+      const int64_t first = min(max(lo, (int64_t)0), a.rows), last = min(max(hi, (int64_t)0), a.rows);
+      cnt[i] = static_cast<int32_t>(max(last - first, (int64_t)0));
+    }
+  }
+}
+
+// The gradient's groups (a whole warp): those of least .. most rows, in order.
+template <typename Args>
+__device__ __forceinline__ void plan_groups(const Args &a, int32_t *list, int32_t *taken, int lane) {
+  int32_t cnt[kPerLane];
+  count_rows(a, cnt, lane);
+  int32_t base = 0;
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    if (32 * i >= a.n) break;
+    const bool mine = lane + 32 * i < a.n && cnt[i] >= a.least && cnt[i] <= a.most;
+    const uint32_t all = __ballot_sync(0xffffffffu, mine);
+    if (mine) list[base + __popc(all & ((1u << lane) - 1))] = lane + 32 * i;
+    base += __popc(all);
+  }
+  if (lane == 0) *taken = base;
 }
 
 // The product's tiles, from the groups' bounds (a whole warp): start[e], the
 // row tiles of the groups before e, and the widest tile.
 template <typename Args>
 __device__ __forceinline__ void plan_rows(const Args &a, int32_t *start, int32_t *widest, int lane) {
-  constexpr int kPer = kMaxStack / 32;
-  int32_t cnt[kPer];   // of group lane + 32 i; all loads in flight together
-  {
-    int32_t o[kPer + 1];
-#pragma unroll
-    for (int i = 0; i <= kPer; ++i) {
-      const int32_t e = lane + 32 * i;
-      o[i] = e > a.n ? 0 : a.offsets ? a.offsets[e] : e == 0 ? 0 : static_cast<int32_t>(a.rows);
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      cnt[i] = 0;
-      if (32 * i >= a.n) continue;
-      const int32_t e = lane + 32 * i;
-      const int32_t down = __shfl_down_sync(0xffffffffu, o[i], 1), over = __shfl_sync(0xffffffffu, o[i + 1], 0);
-      const int64_t lo = o[i], hi = lane == 31 ? over : down;
-      if (e < a.n) {
-        if (lo < 0 || hi < lo || hi > a.rows) set_status(a.status, HIMUON_ERR_DEVICE);
-        const int64_t first = min(max(lo, (int64_t)0), a.rows), last = min(max(hi, (int64_t)0), a.rows);
-        cnt[i] = static_cast<int32_t>(max(last - first, (int64_t)0));
-      }
-    }
-  }
+  int32_t cnt[kPerLane];
+  count_rows(a, cnt, lane);
   int32_t base = 0, w = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
+  for (int i = 0; i < kPerLane; ++i) {
     if (32 * i >= a.n) break;
     w = max(w, tile_width(cnt[i], a.cap));
     int32_t s = row_tiles(cnt[i], a.cap);
@@ -635,8 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *done = drained + 2;                    // even CTA: every MMA issued has completed
   uint64_t *c_full = done + 1;                     // [3 per epilogue warp] a box of C has landed
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(c_full + 3 * kEpiWarps);
-  int32_t *widest = reinterpret_cast<int32_t *>(tmem_slot + 1);   // product: columns of the widest tile
-  int32_t *start = reinterpret_cast<int32_t *>(sm + kData + kBarBytes);   // [n + 1]
+  int32_t *widest = reinterpret_cast<int32_t *>(tmem_slot + 1);   // product: columns of the widest tile; gradient: groups
+  // product: [n + 1] the row tiles of the groups before; gradient: the groups of the launch
+  int32_t *start = reinterpret_cast<int32_t *>(sm + kData + kBarBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr bool kPieces = PREC && !KIND;   // (int32 sums are exact)
   constexpr int kGroups = !PREC ? 1 : SPLIT ? 2 : 4;   // PREC: 32-column groups of an epilogue warp's sums
@@ -664,13 +680,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_wait();   // nothing above reads or writes what earlier work of the stream does
   if (!GRAD && warp == 2) plan_rows(a, start, widest, lane);
-  if (GRAD && warp == 2) check_offsets(a, lane);
+  if (GRAD && warp == 2) plan_groups(a, start, widest, lane);
   __syncwarp();
   tc_fence_before();
   cluster_sync_all();   // barriers of both CTAs are ready before either is signalled
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int32_t all_tiles = (GRAD ? a.n * a.mt_n : start[a.n]) * a.mt_m;
+  const int32_t all_tiles = (GRAD ? *widest * a.mt_n : start[a.n]) * a.mt_m;
   const int32_t n_tiles = SPLIT ? min(all_tiles, step) : all_tiles;   // (split: one tile per cluster)
   // a stage holds 128 rows of A and half of the widest tile's columns of B;
   // narrow tiles (few rows per expert) get more stages, so that enough of W is
