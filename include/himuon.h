@@ -319,7 +319,7 @@ HIMUON_API int himuon_expert_gradient(const himuon_mat *A, const himuon_mat *B, 
  * (dim = 1, the codes are stored transposed: one row of codes per column of
  * the input).  With top = max |x| over the row or column:
  *     scale = top / 127,   code = round(127 x / top), ties to even,
- * so x ~ scale * code.  Where top = 0, scale and codes are 0; where the row or
+ * so x ~ scale * code; codes are those of the exact quotient.  Where top = 0, scale and codes are 0; where the row or
  * column holds an infinity or a NaN, scale is NaN and the codes are 0 (a
  * product with them gives NaN).  `in`: BF16, FP16 or FP32 (per matrix);
  * `codes`: I8, rows x cols (dim 0) or cols x rows (dim 1); `scale`: FP32,

@@ -950,3 +950,34 @@ def test_gradient_long_groups_replayed_with_other_offsets(hm):
     gph.replay()
     assert hm.device_status() == -7
     assert hm.device_status() == 0
+
+
+@pytest.mark.parametrize("dim", [0, 1])
+@pytest.mark.parametrize("scale,length", [(1.0, 0), (1.0, 13001), (1.0, 140003), (2.0 ** -75, 0), (2.0 ** 90, 5003),
+                                          (2.0 ** -130, 0)])
+def test_quantize_fp32_next_to_ties(hm, dim, scale, length):
+    """fp32 values at, and a few units to either side of, the borders between codes, with maxima inside and outside
+    the range of the short division and below the normal numbers.  127 x is exact in 64 bits and the quotient, if no
+    tie, at least 2^-33 from one, so its rounding in 64 bits falls to the right side."""
+    rows = 96
+    rng = np.random.default_rng(81)
+    top = (rng.random(rows) + 1).astype(np.float32)
+    top[:8] = 127 * 2.0 ** -6, 254 * 2.0 ** -7, 127 * 3 * 2.0 ** -8, 127 * 5 * 2.0 ** -9, 1.5, 1.25, 1, 127 * 7 * 2.0 ** -9
+    half = np.arange(-127, 127) + 0.5
+    bits = (half * top[:, None].astype(np.float64) / 127).astype(np.float32).view(np.int32)
+    x = np.concatenate([(bits + d).view(np.float32) for d in range(-4, 5)] + [top[:, None]], axis=1)
+    x = torch.from_numpy((x.astype(np.float64) * scale).astype(np.float32))
+    assert (x.abs().amax(1) == x[:, -1]).all()
+    length = length or x.shape[1]
+    x = x[:, torch.arange(length) % x.shape[1]]
+    pad = torch.zeros(rows, -(-length // 4) * 4 - length)
+    X = torch.cat([x, pad], 1).cuda()
+    X = X.T.contiguous() if dim else X
+    L, n = (X.shape[1], X.shape[0]) if dim else X.shape
+    q, s = torch.empty(L, -(-n // 16) * 16, dtype=torch.int8, device=DEV)[:, :n], torch.empty(L, device=DEV)
+    hm.quantize([X], [q], [s], dim=dim)
+    lines = X.T if dim else X
+    want, top = exact_codes(lines)
+    assert torch.equal(q.double(), want.round())
+    assert torch.equal(s, (top / 127).float())
+    assert hm.device_status() == 0

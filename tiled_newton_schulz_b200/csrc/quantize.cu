@@ -18,30 +18,80 @@ struct QuantArgs {
 };
 
 // code = round(127 x / top), ties to even.  With 127 / top = hi + lo (two fp32
-// numbers, the second the division's remainder), x hi + x lo summed without
-// losing the first product's low part is the quotient rounded once: ties of
-// 16-bit x, which are short numbers, come out exactly.  Adding 1.5 * 2^23 then
-// rounds to an integer and leaves it in the low bits.  Five operations per
-// element: the kernel is bound by its instructions (the plain division took 464
-// us for 8192 x 11008 bf16).  A maximum so small or large that hi or x hi could
-// leave fp32's range takes the division, scaled by a power of two.
-__device__ __forceinline__ uint32_t near_code(float x, float hi, float lo) {   // the code in the low byte
-  const float p = x * hi;
-  return __float_as_uint(p + fmaf(x, lo, fmaf(x, hi, -p)) + 12582912.f);
+// numbers, the second the division's remainder), p = x hi and e = what p lost, plus
+// x lo, p + e is the quotient up to 2^-39 and its fp32 sum s the quotient rounded
+// once.  Adding 1.5 * 2^23 then rounds to an integer and leaves it in the low bits.
+// Five operations per element: the kernel is bound by its instructions (the plain
+// division took 464 us for 8192 x 11008 bf16).  A quotient that is no
+// tie lies 2 * 127 x - (2 k + 1) top, at least one last place of x, over 2 top from
+// one.  For 16-bit x and a quotient in 2^m .. 2^(m + 1) that is 2^(m - 20), sixteen
+// times what s is off, and rounding twice is exact.  For fp32 it may be 2^-33, where
+// s is the tie itself; what s lost then decides.  A maximum
+// so small or large that hi or x hi could leave fp32's range is multiplied by a power
+// of two first, and x with it (an x that loses bits by that has the code 0).
+constexpr float kToInt = 12582912.f;
+template <int DT>
+__device__ __forceinline__ uint32_t exact_code(float x, float hi, float lo) {   // the code in the low byte
+  const float p = x * hi, e = fmaf(x, lo, fmaf(x, hi, -p)), s = p + e;
+  if (DT != HIMUON_FP32) return __float_as_uint(s + kToInt);
+  const float n = s + kToInt - kToInt, d = s - n, lost = e - (s - p);
+  const bool next = fabsf(d) == 0.5f && fabsf(lost) > 0x1p-36f && (lost > 0.f) == (d > 0.f);
+  return __float_as_uint(n + (next ? 2.f * d : 0.f) + kToInt);
+}
+// fp32, two at a time (packed arithmetic, 9 instructions a pair): the same codes but
+// where s is a tie, of which `ties` tells: it is multiplied by d^2 - 1/4, d being s's
+// distance from its integer, which is 0 there (and where the product underflows).
+// Those elements are read and coded again.  (8192 x 11008: 73 us; 79 with exact_code
+// for every element, 69 without a look at ties.)
+struct Pair {
+  uint64_t v;
+  __device__ __forceinline__ Pair(float a, float b) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(__float_as_uint(a)), "r"(__float_as_uint(b)));
+  }
+  __device__ __forceinline__ explicit Pair(uint64_t bits) : v(bits) {}
+  __device__ __forceinline__ void split(uint32_t &a, uint32_t &b) const { asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v)); }
+  __device__ __forceinline__ bool any_zero() const {
+    uint32_t a, b;
+    split(a, b);
+    return __uint_as_float(a) == 0.f || __uint_as_float(b) == 0.f;
+  }
+};
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a.v), "l"(b.v));
+  return Pair(d);
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a.v), "l"(b.v));
+  return Pair(d);
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return Pair(d);
+}
+__device__ __forceinline__ void near_codes(Pair x, Pair hi, Pair minus_hi, Pair minus_lo, uint32_t &c0, uint32_t &c1,
+                                           Pair &ties) {
+  const Pair minus(-1.f, -1.f), up(kToInt, kToInt), down(-kToInt, -kToInt), quarter(-0.25f, -0.25f);
+  const Pair p = x * hi, s = fma2(fma2(x, minus_lo, fma2(x, minus_hi, p)), minus, p);
+  const Pair u = s + up, d = fma2(u + down, minus, s);
+  ties = ties * fma2(d, d, quarter);
+  u.split(c0, c1);
 }
 struct Coder {
-  float hi, lo, top;
-  __device__ explicit Coder(float t) {
-    top = t;
+  float hi, lo, mul;
+  __device__ explicit Coder(float top) {
+    mul = top > 0x1p60f ? 0x1p-100f : top < 0x1p-60f ? 0x1p100f : 1.f;
+    const float t = top * mul;
     hi = __fdiv_rn(127.f, t);
     lo = __fdiv_rn(fmaf(-t, hi, 127.f), t);
   }
-  __device__ __forceinline__ bool in_range() const { return top >= 0x1p-60f && top <= 0x1p60f; }
-  __device__ __forceinline__ uint32_t far_code(float x) const {
-    const float mul = top > 1.f ? 0x1p-100f : 0x1p100f;
-    return __float_as_uint(__fdiv_rn(127.f * (x * mul), top * mul) + 12582912.f);
+  __device__ __forceinline__ bool in_range() const { return mul == 1.f; }   // (its codes take x itself)
+  template <int DT>
+  __device__ __forceinline__ uint32_t code(float x) const {
+    return exact_code<DT>(x * mul, hi, lo);
   }
-  __device__ __forceinline__ uint32_t operator()(float x) const { return in_range() ? near_code(x, hi, lo) : far_code(x); }
 };
 __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
@@ -59,7 +109,8 @@ __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x
 // One scale per row: TPR threads per row.  The row stays in registers between
 // the two passes (kHold runs of 8 elements per thread, all loads in flight
 // together; longer rows are read again, from L2).  HBM-bound: 3 bytes per
-// 16-bit element; 16384 x 4096 bf16 takes 38 us (5.3 TB/s), fp32 50 us (6.8).
+// 16-bit element; 16384 x 4096 bf16 takes 38 us (5.3 TB/s), fp32 50 us (6.7
+// TB/s, four fifths of it reads).
 __device__ __forceinline__ uint32_t max_s16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.s16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -188,24 +239,49 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const __grid_cons
   const bool ok = line_ok(top);
   const Coder code(ok ? __uint_as_float(top) : 1.f);
   if (!ok || !code.in_range()) {   // (rare: one element at a time)
-    for (int64_t i = t; i < cols; i += TPR) out[i] = ok ? static_cast<int8_t>(code.far_code(ld_any(in, DT, i))) : 0;
+    for (int64_t i = t; i < cols; i += TPR) out[i] = ok ? static_cast<int8_t>(code.template code<DT>(ld_any(in, DT, i))) : 0;
     return;
   }
-  auto put8 = [&](int32_t i, const Run8<DT> &x) {
-    uint32_t u[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = near_code(x.get(j), code.hi, code.lo);
+  auto put8 = [&](int32_t i, const uint32_t (&u)[8]) {
     *reinterpret_cast<uint2 *>(out + 8 * i) = make_uint2(bytes4(u[0], u[1], u[2], u[3]), bytes4(u[4], u[5], u[6], u[7]));
   };
+  auto exact8 = [&](int32_t i, const Run8<DT> &x) {
+    uint32_t u[8];
 #pragma unroll
-  for (int h = 0; h < kHold<DT>; ++h)
-    if (t + h * TPR < runs) put8(t + h * TPR, v[h]);
-  for (int32_t i = t + kHold<DT> * TPR; i < runs; i += TPR) {
+    for (int j = 0; j < 8; ++j) u[j] = exact_code<DT>(x.get(j), code.hi, code.lo);
+    put8(i, u);
+  };
+  auto near8 = [&](int32_t i, const Run8<DT> &x) {   // fp32; true: to be done again
+    const Pair hi(code.hi, code.hi), minus_hi(-code.hi, -code.hi), minus_lo(-code.lo, -code.lo);
+    Pair ties(1.f, 1.f);
+    uint32_t u[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2)
+      near_codes(Pair(x.get(j), x.get(j + 1)), hi, minus_hi, minus_lo, u[j], u[j + 1], ties);
+    put8(i, u);
+    return ties.any_zero();
+  };
+  auto again = [&](int32_t i) {
     Run8<DT> w;
     w.load(in, i);
-    put8(i, w);
+    exact8(i, w);
+  };
+  uint32_t ties = 0;
+#pragma unroll
+  for (int h = 0; h < kHold<DT>; ++h)
+    if (t + h * TPR < runs) {
+      if (DT != HIMUON_FP32) exact8(t + h * TPR, v[h]);
+      else if (near8(t + h * TPR, v[h])) ties |= 1u << h;
+    }
+  for (int32_t i = t + kHold<DT> * TPR, h = kHold<DT>; i < runs; i += TPR, ++h) {
+    Run8<DT> w;
+    w.load(in, i);
+    if (DT != HIMUON_FP32) exact8(i, w);
+    else if (near8(i, w)) ties |= 1u << (h & 31);
   }
-  for (int64_t i = 8ll * runs + t; i < cols; i += TPR) out[i] = static_cast<int8_t>(near_code(ld_any(in, DT, i), code.hi, code.lo));
+  for (; ties; ties &= ties - 1)   // (one run in 2^14 of normal values; past 32 runs a bit stands for every 32nd)
+    for (int64_t i = t + (__ffs(ties) - 1) * TPR; i < runs; i += 32 * TPR) again(static_cast<int32_t>(i));
+  for (int64_t i = 8ll * runs + t; i < cols; i += TPR) out[i] = static_cast<int8_t>(exact_code<DT>(ld_any(in, DT, i), code.hi, code.lo));
 }
 
 // One scale per column, codes transposed.  A cluster takes 64 columns (128 bytes
@@ -217,7 +293,8 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const __grid_cons
 // memory, so that a warp stores 128 rows of a column at once.
 constexpr int kTurnPitch = 33;   // words; with the columns' rotation below free of bank conflicts
 template <int DT>
-__global__ void __launch_bounds__(256) quantize_cols_kernel(const __grid_constant__ QuantArgs a) {
+__global__ void __launch_bounds__(256, 3)
+    quantize_cols_kernel(const __grid_constant__ QuantArgs a) {
   __shared__ uint32_t tops[64];
   __shared__ uint32_t turn[64 * kTurnPitch];
   grid_start_next();
@@ -285,19 +362,47 @@ __global__ void __launch_bounds__(256) quantize_cols_kernel(const __grid_constan
     Run8<DT> x[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) load(b + 4 * rg + k, x[k]);
+    uint32_t pairs = 0;   // fp32: to be done again
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t u[4];
-      if (near) {
+    for (int j = 0; j < 8; j += 2) {
+      uint32_t u[2][4];
+      if (near && DT == HIMUON_FP32) {
+        const Pair h(hi[j], hi[j + 1]), minus_h(-hi[j], -hi[j + 1]), minus_l(-lo[j], -lo[j + 1]);
+        Pair ties(1.f, 1.f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) u[k] = near_code(x[k].get(j), hi[j], lo[j]);
+        for (int k = 0; k < 4; ++k)
+          near_codes(Pair(x[k].get(j), x[k].get(j + 1)), h, minus_h, minus_l, u[0][k], u[1][k], ties);
+        if (ties.any_zero()) pairs |= 1u << j;
+      } else if (near) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k / 4][k % 4] = exact_code<DT>(x[k % 4].get(j + k / 4), hi[j + k / 4], lo[j + k / 4]);
       } else {
-        const uint32_t top = tops[8 * c8 + j];
-        const Coder code(line_ok(top) ? __uint_as_float(top) : 1.f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) u[k] = line_ok(top) ? code(x[k].get(j)) : 0;
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t top = tops[8 * c8 + j + i];
+          const Coder code(line_ok(top) ? __uint_as_float(top) : 1.f);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) u[i][k] = line_ok(top) ? code.template code<DT>(x[k].get(j + i)) : 0;
+        }
       }
-      turn[(8 * c8 + j) * kTurnPitch + ((rg + 4 * (c8 >> 2)) & 31)] = bytes4(u[0], u[1], u[2], u[3]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        turn[(8 * c8 + j + i) * kTurnPitch + ((rg + 4 * (c8 >> 2)) & 31)] = bytes4(u[i][0], u[i][1], u[i][2], u[i][3]);
+    }
+    for (; pairs; pairs &= pairs - 1) {   // (rare)
+      const int j = __ffs(pairs) - 1;
+#pragma unroll 1
+      for (int i = j; i < j + 2 && c + i < cols; ++i) {
+        const uint32_t top = tops[8 * c8 + i];
+        const Coder code(line_ok(top) ? __uint_as_float(top) : 1.f);
+        uint32_t u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t r = b + 4 * rg + k;
+          u[k] = exact_code<DT>(r < rows ? ld_any(a.in[z], DT, r * ld + c + i) : 0.f, code.hi, code.lo);
+        }
+        turn[(8 * c8 + i) * kTurnPitch + ((rg + 4 * (c8 >> 2)) & 31)] = bytes4(u[0], u[1], u[2], u[3]);
+      }
     }
     __syncthreads();
     const int64_t r = b + 4 * lane;
