@@ -981,3 +981,69 @@ def test_quantize_fp32_next_to_ties(hm, dim, scale, length):
     assert torch.equal(q.double(), want.round())
     assert torch.equal(s, (top / 127).float())
     assert hm.device_status() == 0
+
+
+# ---------------------------------------------------------------- fp32 results as a whole
+# An uncut sum of 1100 terms of either sign is off by 1.1e-6 of itself (relative norms), 1.6e-8 per 16 terms.  Pieces
+# of 512 make that 32 x 1.6e-8 = 5.1e-7 of each piece, whose errors are independent, so 5.1e-7 of the sum however
+# many there are; rounding adds 0.3e-7.  The limit lies half way (in ratio) to the uncut sum's error at 1100 terms;
+# 4096 uncut terms are off by 4e-6.
+NORM = 7.5e-7
+
+
+def norm_error(y, exact):
+    return float((y.double() - exact).norm() / exact.norm())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("length", [1100, 4096])
+def test_norm_of_errors_of_fp32_results(hm, dtype, length, few):
+    """few: tiles that several pairs share."""
+    g, t = gen(91), TYPES[dtype]
+    n, rows, N = (1, 100, 264) if few else (40, 400, 2056)
+    off = offsets([rows] if few else [rows // n] * n)
+    X = matrix((rows, length), t, g)
+    for trans in (False, True):
+        W = matrix((n, N, length) if trans else (n, length, N), t, g)
+        Y = torch.empty(rows, N, device=DEV)
+        hm.expert_product(X, W, Y, off, w_trans=trans)
+        exact = torch.cat([X[a:b].double() @ (w.double().T if trans else w.double()) for (a, b), w in zip(groups(off), W)])
+        assert norm_error(Y, exact) <= NORM, trans
+    P = 200 if few else 1032
+    counts = [length] if few else [length, 0, length]
+    A, B = matrix((sum(counts), P), t, g), matrix((sum(counts), N), t, g)
+    G = torch.empty(len(counts), P, N, device=DEV)
+    hm.expert_gradient(A, B, G, offsets(counts))
+    for e in range(0, len(counts), 2):
+        a = length * (e // 2)
+        assert norm_error(G[e], A[a:a + length].double().T @ B[a:a + length].double()) <= NORM, e
+    assert hm.device_status() == 0
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16", "fp16"])
+def test_a_group_alone_and_among_others(hm, out):
+    """The order of a group's sums may depend on the call's other groups (which tiles are shared), its values only
+    within the rounding: fp32 norms within two errors, 16-bit values at most one step apart beyond two sums' errors."""
+    g, t = gen(92), TYPES[out]
+    n, K, N, rows = 24, 1100, 520, 2400
+    counts = [100] * n
+    counts[7], counts[8] = 190, 10
+    off = offsets(counts)
+    a, b = groups(off)[7]
+    X, W, dY = matrix((rows, K), torch.bfloat16, g), matrix((n, K, N), torch.bfloat16, g, 0.1), matrix((rows, N), torch.bfloat16, g)
+    Y, Y1 = torch.empty(rows, N, device=DEV, dtype=t), torch.empty(b - a, N, device=DEV, dtype=t)
+    G, G1 = torch.empty(n, K, N, device=DEV, dtype=t), torch.empty(1, K, N, device=DEV, dtype=t)
+    hm.expert_product(X, W, Y, off)
+    hm.expert_product(X[a:b], W[7:8], Y1)
+    hm.expert_gradient(X, dY, G, off)
+    hm.expert_gradient(X[a:b], dY[a:b], G1)
+    x, w, dy = X[a:b].double(), W[7].double(), dY[a:b].double()
+    for many, one, size, k in ((Y[a:b], Y1, x.abs() @ w.abs(), K), (G[7], G1[0], x.abs().T @ dy.abs(), b - a)):
+        if out == "fp32":
+            assert norm_error(many, one.double()) <= 2 * NORM
+            continue
+        f = torch.finfo(t)
+        lim = f.eps * torch.maximum(many.double().abs(), one.double().abs()) + 2 * (k + 16) * 2.0 ** -23 * size + f.smallest_normal * f.eps
+        assert ((many.double() - one.double()).abs() <= lim).all()
+    assert hm.device_status() == 0
