@@ -156,7 +156,9 @@ bool load_kernels() {
       load_variant<0, 1, 0, 0, 0>() && load_variant<0, 1, 0, 1, 0>() && load_variant<0, 1, 0, 1, 1>() &&
       load_variant<1, 0, 0, 0, 0>() && load_variant<1, 0, 0, 1, 1>() && load_variant<0, 1, 1, 0, 0>() &&
       load_variant<0, 1, 1, 1, 0>() && load_variant<0, 1, 1, 1, 1>() && device_status_word() != nullptr &&
-      load_quantize() && clusters_at_once(2) >= 0 && clusters_at_once(4) >= 0;
+      load_quantize();
+  clusters_at_once(2);   // (looked up here, not in a later call's capture; with no room, tiles are not shared)
+  clusters_at_once(4);
   if (ok) loaded.fetch_or(bit, std::memory_order_relaxed);
   return ok;
 }

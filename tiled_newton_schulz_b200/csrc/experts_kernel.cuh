@@ -431,21 +431,6 @@ __device__ __forceinline__ void box_copy(const uint8_t *buf, int lane, int32_t d
     }
   }
 }
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int32_t x, int32_t y, int32_t z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
-               : "memory");
-}
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int32_t x, int32_t y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
-               "r"(y), "r"(smem_u32(src))
-               : "memory");
-}
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-
 // fp32, whole rows: the block goes by TMA in two boxes of 16 rows (128-byte swizzle),
 // from the buffer's halves in turn, turned without bank conflicts.  (7052 rows 128 -> 10968:
 // 93 us with plain stores, 71 with boxes; 16-bit results gain nothing, 53.6 and 53.7.)

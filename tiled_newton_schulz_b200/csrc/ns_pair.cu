@@ -373,7 +373,7 @@ __device__ void pair_main(const ResidentArgs &a, const PairSmem &sm, uint32_t tm
   for (int64_t tile = pair; tile < a.n_tiles && !bad; tile += n_pairs, ++it) {
     TileCoord *cur = sm.coord(it & 1u), *nxt = sm.coord((it + 1u) & 1u);
     if (tma) {
-      bulk_wait_read0();   // the previous tile's stores have finished reading X_s / S_s
+      bulk_wait_read<0>();   // the previous tile's stores have finished reading X_s / S_s
       mbar_arrive(sm.bar_sfree());
       if (!ld_issued) {
         mbar_arrive_expect_tx(sm.bar_ld(), ld_bytes);
@@ -453,7 +453,7 @@ __device__ void pair_main(const ResidentArgs &a, const PairSmem &sm, uint32_t tm
     convert_x(a.gamma0 / rho);
     // M' (and the previous tile's W' and O) must have left S_s / X_s before
     // MMA1 completes and the first conversion overwrites S_s
-    if (tma) bulk_wait_read0();
+    if (tma) bulk_wait_read<0>();
     ready();
     bad = !send_stage();
     if (leader && !bad) bad = !issue(kJobGram, nullptr, false);

@@ -555,7 +555,7 @@ __device__ void group_main(const ResidentArgs &a, const Smem &sm, uint32_t tmem,
     // this row's tile exists (the last super-tile may hold fewer than P tiles)
     const bool row_valid = P == 1 || P * st + jr < a.n_tiles;
     if (gt == 0) {
-      bulk_wait_read0();  // the previous super-tile's stores have finished reading S_s / W_s
+      bulk_wait_read<0>();  // the previous super-tile's stores have finished reading S_s / W_s
       if (!mg_issued) {
         issue_mg<P>(a, sm, g, cur);
         ++ld_armed;
@@ -706,7 +706,7 @@ __device__ void group_main(const ResidentArgs &a, const Smem &sm, uint32_t tmem,
       else tmem_row_to_op<1, true>(tX, tX, Xs, r, hf, a.gamma0 / rho);
     }
     // M' must have left S_s before the first conversion (after MMA1) overwrites it
-    if (step_mode && gt == 0) bulk_wait_read0();
+    if (step_mode && gt == 0) bulk_wait_read<0>();
     fence_proxy_async_smem();
     tc_fence_before();
     group_ready(sm, g, lane);
