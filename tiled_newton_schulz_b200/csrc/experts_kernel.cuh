@@ -611,9 +611,10 @@ __device__ __forceinline__ void add_slices(float (&v)[32], const uint8_t *ring, 
 // the even CTA issues the MMAs for both.  A single CTA with the same 128 x 256
 // tile writes and reads 96 + 96 bytes of operands per cycle of MMA in its
 // shared memory, more than its 128 bytes per cycle; the pair needs 64 + 64.
-// 8192 rows through 4096 -> 11008 take 460 to 490 us (1500 to 1600 TFLOP/s, the
-// tensor pipe 91% active; at the power cap 550 us), 64 gradients of 1024 x 4096
-// added in fp32 390 us (5.9 TB/s), 256 rows of 56 experts 84 us (5.6 TB/s).
+// 8192 rows through 4096 -> 11008 take 468 to 495 us (1490 to 1580 TFLOP/s, the
+// tensor pipe 91% active; at the power cap 556 us), 64 gradients of 1024 x 4096
+// added in fp32 389 to 423 us (5.5 to 6.0 TB/s), 256 rows of 56 experts 84 to 87 us
+// (5.4 to 5.6 TB/s).
 // Persistent: warp 0 streams its CTA's operands through a ring of stages (TMA,
 // completing on the even CTA's barriers), warp 1 of the even CTA issues each
 // tile's MMAs into one of two accumulators, warps 4..11 of both drain the other
